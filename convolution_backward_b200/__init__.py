@@ -20,6 +20,7 @@ import os
 import threading
 
 __all__ = ["pointwise", "pointwise_splitk", "pointwise_splitk_noalloc", "depthwise_tc", "depthwise_tc_workspace_bytes", "dense", "grouped", "splitk_workspace_bytes", "depthwise", "out_dims", "check_status", "DgradError", "DgradUnavailable",
+           "layernorm_forward", "layernorm_backward", "layernorm_backward_workspace_bytes", "dropout_forward", "dropout_backward",
            "Problem", "lib", "library_path", "selftest_timeout", "fma_probe", "STATUS"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -110,6 +111,16 @@ def lib():
             L.dgrad_depthwise_tc.restype = ctypes.c_int
             L.dgrad_depthwise_tc_workspace.argtypes = [P(Problem), P(ctypes.c_size_t)]
             L.dgrad_depthwise_tc_workspace.restype = ctypes.c_int
+            i64, u64, dbl, sz, ci = ctypes.c_int64, ctypes.c_uint64, ctypes.c_double, ctypes.c_size_t, ctypes.c_int
+            for name, args in {
+                    "layernorm_forward": [i64, i64, ci, dbl, vp, vp, vp, vp, vp, vp, vp],
+                    "layernorm_backward": [i64, i64, ci, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+                    "layernorm_backward_workspace": [i64, i64, ci, P(sz)],
+                    "dropout_forward": [i64, ci, dbl, u64, u64, vp, vp, vp, vp],
+                    "dropout_backward": [i64, ci, dbl, u64, u64, vp, vp, vp]}.items():
+                f = getattr(L, "dgrad_" + name)
+                f.argtypes = args
+                f.restype = ctypes.c_int
             _lib = L
     return _lib
 
@@ -148,15 +159,19 @@ def _call(dev, what, fn, *args, stream=None):
         _check(fn(*args, _stream_ptr(stream, dev)), what)
 
 
-def _dtype_code(t) -> int:
+def _code_of(dtype) -> int:
     import torch
-    if t.dtype == torch.float32:
+    if dtype == torch.float32:
         return 0
-    if t.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         return 1
-    if t.dtype == torch.float16:
+    if dtype == torch.float16:
         return 2
-    raise TypeError(f"unsupported dtype {t.dtype}; use float32, bfloat16 or float16")
+    raise TypeError(f"unsupported dtype {dtype}; use float32, bfloat16 or float16")
+
+
+def _dtype_code(t) -> int:
+    return _code_of(t.dtype)
 
 
 def _need_cuda(*ts):
@@ -395,6 +410,192 @@ def depthwise_tc(dY, W, *, H, W_out=None, pad_h=0, pad_w=-1, workspace=None, out
     _call(_device_of(dY, W, out, workspace), "dgrad_depthwise_tc", lib().dgrad_depthwise_tc, ctypes.byref(prob),
           _dtype_code(dY), dY.data_ptr(), W.data_ptr(), out.data_ptr(), workspace.data_ptr(),
           workspace.numel() * workspace.element_size(), stream=stream)
+    return out
+
+
+# ------------------------------------------------ the residual branch's operators
+
+def _rows_of(X):
+    """(M, C): the rows of X (..., C) and their length."""
+    if X.dim() < 1:
+        raise ValueError("expected a tensor of rows (..., C)")
+    C = X.shape[-1]
+    if C < 1:
+        raise ValueError("expected at least one channel")
+    M = 1
+    for d in X.shape[:-1]:
+        M *= d
+    return M, C
+
+
+def _like(t, shape, dtype, what):
+    """Check a tensor argument's shape and dtype."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+
+
+class _Allocator:
+    """Outputs and workspaces of one call, taken from the pool of the stream it runs on, so that
+    memory still in use on another stream is never handed out to it.  When that is not the
+    device's current stream, the tensors of the call are recorded on the stream they are used
+    on besides their own: freeing one early does not pull it away."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.device = device
+        self.stream = None
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device} but the tensors are on {device}")
+            current = torch.cuda.current_stream(device)
+            if stream != current:
+                self.stream, self.current = stream, current
+
+    def empty(self, shape, dtype):
+        import torch
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(self.current)
+        return t
+
+    def uses(self, *ts):
+        if self.stream is not None:
+            for t in ts:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def layernorm_forward(X, gamma=None, beta=None, eps=1e-5, stats=False, out=None, stream=None):
+    """Layer norm over the last axis of X (..., C) (dgrad_layernorm_forward).
+
+    gamma, beta: (C,) of X's dtype, or None for ones and zeros.  With ``stats`` the
+    result is (Y, mean, rstd), the fp32 statistics of shape X.shape[:-1] that
+    layernorm_backward takes.  ``out`` may be X."""
+    import torch
+    _need_cuda(X)
+    code = _dtype_code(X)
+    M, C = _rows_of(X)
+    given = [t for t in (gamma, beta, out) if t is not None]
+    _need_cuda(*given)
+    dev = _device_of(X, *given)
+    for t, what in ((gamma, "gamma"), (beta, "beta")):
+        if t is not None:
+            _like(t, (C,), X.dtype, what)
+    al = _Allocator(dev, stream)
+    if out is None:
+        out = al.empty(X.shape, X.dtype)
+    else:
+        _like(out, X.shape, X.dtype, "out")
+    mean = al.empty(X.shape[:-1], torch.float32) if stats else None
+    rstd = al.empty(X.shape[:-1], torch.float32) if stats else None
+    al.uses(X, *given)
+    _call(dev, "dgrad_layernorm_forward", lib().dgrad_layernorm_forward, M, C, code, float(eps), X.data_ptr(),
+          _ptr(gamma), _ptr(beta), out.data_ptr(), _ptr(mean), _ptr(rstd), stream=stream)
+    return (out, mean, rstd) if stats else out
+
+
+def layernorm_backward_workspace_bytes(M, C, dtype) -> int:
+    """Workspace bytes layernorm_backward needs for M rows of C elements of a torch dtype (host only)."""
+    nb = ctypes.c_size_t()
+    _check(lib().dgrad_layernorm_backward_workspace(int(M), int(C), _code_of(dtype), ctypes.byref(nb)),
+           "dgrad_layernorm_backward_workspace")
+    return nb.value
+
+
+def layernorm_backward(dY, X, mean, rstd, gamma=None, param_grads=True, workspace=None, out=None, stream=None):
+    """Gradients of layernorm_forward: (dX, dgamma, dbeta) (dgrad_layernorm_backward).
+
+    mean, rstd: the forward's statistics.  dgamma and dbeta (C,) have X's dtype; without
+    ``param_grads`` they are None and not computed.  ``out`` (dX) may be dY or X.
+    workspace: a CUDA tensor of at least layernorm_backward_workspace_bytes(...) bytes,
+    taken from torch when None."""
+    import torch
+    _need_cuda(dY, X, mean, rstd)
+    code = _dtype_code(X)
+    M, C = _rows_of(X)
+    _like(dY, X.shape, X.dtype, "dY")
+    _like(mean, X.shape[:-1], torch.float32, "mean")
+    _like(rstd, X.shape[:-1], torch.float32, "rstd")
+    given = [t for t in (gamma, workspace, out) if t is not None]
+    _need_cuda(*given)
+    dev = _device_of(dY, X, mean, rstd, *given)
+    if gamma is not None:
+        _like(gamma, (C,), X.dtype, "gamma")
+    al = _Allocator(dev, stream)
+    if out is None:
+        out = al.empty(X.shape, X.dtype)
+    else:
+        _like(out, X.shape, X.dtype, "out")
+    dgamma = dbeta = None
+    ws_bytes = 0
+    if param_grads:
+        dgamma, dbeta = al.empty((C,), X.dtype), al.empty((C,), X.dtype)
+        if workspace is None:
+            workspace = al.empty((max(layernorm_backward_workspace_bytes(M, C, X.dtype), 16),), torch.uint8)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    al.uses(dY, X, mean, rstd, *given)
+    _call(dev, "dgrad_layernorm_backward", lib().dgrad_layernorm_backward, M, C, code, dY.data_ptr(), X.data_ptr(),
+          _ptr(gamma), mean.data_ptr(), rstd.data_ptr(), out.data_ptr(), _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
+          ws_bytes, stream=stream)
+    return out, dgamma, dbeta
+
+
+def _counter(v, what):
+    v = int(v)
+    if not 0 <= v < 1 << 64:
+        raise ValueError(f"{what} must lie in [0, 2^64)")
+    return v
+
+
+def dropout_forward(X, p, seed, offset=0, residual=None, out=None, stream=None):
+    """Dropout with probability p, plus ``residual`` when given (dgrad_dropout_forward).
+
+    The mask is a function of (seed, offset) and the element's index, and is not stored:
+    give every call its own pair, and the backward pass its forward's.  ``out`` may be X
+    or residual."""
+    _need_cuda(X)
+    code = _dtype_code(X)
+    given = [t for t in (residual, out) if t is not None]
+    _need_cuda(*given)
+    dev = _device_of(X, *given)
+    if residual is not None:
+        _like(residual, X.shape, X.dtype, "residual")
+    al = _Allocator(dev, stream)
+    if out is None:
+        out = al.empty(X.shape, X.dtype)
+    else:
+        _like(out, X.shape, X.dtype, "out")
+    al.uses(X, *given)
+    _call(dev, "dgrad_dropout_forward", lib().dgrad_dropout_forward, X.numel(), code, float(p),
+          _counter(seed, "seed"), _counter(offset, "offset"), X.data_ptr(), _ptr(residual), out.data_ptr(),
+          stream=stream)
+    return out
+
+
+def dropout_backward(dY, p, seed, offset=0, out=None, stream=None):
+    """Gradient of dropout_forward in X (dgrad_dropout_backward); the residual's is dY itself.
+    ``out`` may be dY."""
+    _need_cuda(dY)
+    code = _dtype_code(dY)
+    given = [out] if out is not None else []
+    _need_cuda(*given)
+    dev = _device_of(dY, *given)
+    al = _Allocator(dev, stream)
+    if out is None:
+        out = al.empty(dY.shape, dY.dtype)
+    else:
+        _like(out, dY.shape, dY.dtype, "out")
+    al.uses(dY, *given)
+    _call(dev, "dgrad_dropout_backward", lib().dgrad_dropout_backward, dY.numel(), code, float(p),
+          _counter(seed, "seed"), _counter(offset, "offset"), dY.data_ptr(), out.data_ptr(), stream=stream)
     return out
 
 

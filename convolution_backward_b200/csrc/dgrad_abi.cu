@@ -253,6 +253,14 @@ int device_sm_count()
     DeviceState* st = nullptr;
     return device_state(&st) == DGRAD_OK ? st->sms : 148;
 }
+
+int device_status_word(int** status)
+{
+    DeviceState* st = nullptr;
+    const dgrad_status_t s = device_state(&st);
+    if (s == DGRAD_OK) *status = st->status;
+    return s;
+}
 }  // namespace dgrad
 
 extern "C" {

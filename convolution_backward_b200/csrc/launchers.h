@@ -164,7 +164,60 @@ cudaError_t launch_dw_rowstream_fast(const DwArgs& a, const CUtensorMap& dy_map,
 // problem has no fast instantiation.
 bool dw_rowstream_fast_box(const DwArgs& a, unsigned box[4], unsigned box_dx[4], unsigned* rows_dx8);
 
+// Layer norm over rows of C elements (ek: ElemKind of X, gamma, beta and Y).
+// Null gamma or beta: ones or zeros; null mean or rstd: not written.
+struct LnFwdArgs {
+    int64_t M, C;
+    int ek;
+    float eps;
+    const void* X;
+    const void* gamma;
+    const void* beta;
+    void* Y;
+    float* mean;
+    float* rstd;
+    int* status;
+};
+cudaError_t launch_layernorm_forward(const LnFwdArgs& a, cudaStream_t stream);
+
+// Its gradients.  ws holds fp32 column sums per block (layernorm_backward_workspace_bytes);
+// null dgamma and dbeta: not computed, and ws is not used.
+struct LnBwdArgs {
+    int64_t M, C;
+    int ek;
+    const void* dY;
+    const void* X;
+    const void* gamma;
+    const float* mean;
+    const float* rstd;
+    void* dX;
+    void* dgamma;
+    void* dbeta;
+    float* ws;
+    int* status;
+};
+size_t layernorm_backward_workspace_bytes(int64_t M, int64_t C, int ek);
+cudaError_t launch_layernorm_backward(const LnBwdArgs& a, cudaStream_t stream);
+
+// Dropout of n elements, kept where their 16-bit draw is >= threshold (0 .. 65536),
+// plus the residual when there is one.
+struct DropArgs {
+    int64_t n;
+    int ek;
+    const void* X;
+    const void* residual;
+    void* Y;
+    uint64_t seed, offset;
+    uint32_t threshold;
+    int* status;
+};
+cudaError_t launch_dropout(const DropArgs& a, cudaStream_t stream);
+
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
+
+// The status word of the current device (a dgrad_status_t as int; entry points
+// defined outside the ABI file get it through this).
+int device_status_word(int** status);
 
 }  // namespace dgrad

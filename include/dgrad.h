@@ -214,6 +214,62 @@ dgrad_status_t dgrad_depthwise_tc(const dgrad_problem_t* prob, dgrad_dtype_t dty
  * same refusals as dgrad_depthwise_tc for the problem (host only). */
 dgrad_status_t dgrad_depthwise_tc_workspace(const dgrad_problem_t* prob, size_t* bytes);
 
+/* ---- The residual branch around the gradients: x + dropout(f(layernorm(x))).
+ * No counterpart on the pages: these are the operators a training program runs on
+ * the same channel rows between its calls of the entry points above. Rows are the
+ * N*H*W positions of an NHWC tensor (or tokens): M rows of C channels, dense.
+ * Base pointers 16-byte aligned (fp32 statistics: 4-byte); unlike the gradients
+ * above, layer norm and dropout take any C or n >= 1: rows that do not start on
+ * 16 bytes run on element-wide loads.  Ranges an output shares with another
+ * argument are refused (DGRAD_ERR_INVALID) except where one is named below.
+ * Results repeat bit for bit: no atomics, sums in a fixed order, fp32 throughout
+ * and one rounding to the element type at the end.  M (or n) of 0 is a no-op, and
+ * sets gradients that are sums over rows to zero. ---- */
+
+/* Layer norm over C channels:
+ *     mean = sum(x)/C,  rstd = 1/sqrt(sum((x - mean)^2)/C + eps),
+ *     Y = (x - mean)*rstd*gamma + beta.
+ * All element types (gamma, beta and Y have X's).  gamma or beta null: ones, zeros.
+ * mean, rstd (fp32, M each, either may be null) are what the backward pass needs.
+ * Y may be X.  eps finite and >= 0 (a constant row at eps 0 gives NaN, as the
+ * formula does).  C <= 65536, M < 2^31 (else DGRAD_ERR_UNSUPPORTED). */
+dgrad_status_t dgrad_layernorm_forward(int64_t M, int64_t C, dgrad_dtype_t dtype, double eps, const void* X,
+                                       const void* gamma, const void* beta, void* Y, float* mean, float* rstd,
+                                       void* stream);
+
+/* Its gradients, with n = (x - mean)*rstd and q = dY*gamma:
+ *     dX = rstd*(q - sum(q)/C - n*sum(q*n)/C),
+ *     dgamma = sum over rows of dY*n,  dbeta = sum over rows of dY.
+ * dgamma or dbeta null: not computed.  dX may be dY or X.  workspace (16-byte
+ * aligned, at least dgrad_layernorm_backward_workspace bytes; contents do not
+ * matter and are clobbered) is needed when dgamma or dbeta is wanted; too small or
+ * null then: DGRAD_ERR_INVALID.  Two calls that may overlap need a workspace each. */
+dgrad_status_t dgrad_layernorm_backward(int64_t M, int64_t C, dgrad_dtype_t dtype, const void* dY, const void* X,
+                                        const void* gamma, const float* mean, const float* rstd, void* dX,
+                                        void* dgamma, void* dbeta, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
+/* Workspace bytes dgrad_layernorm_backward needs (host only, no CUDA call). */
+dgrad_status_t dgrad_layernorm_backward_workspace(int64_t M, int64_t C, dgrad_dtype_t dtype, size_t* bytes);
+
+/* Dropout of n elements with no stored mask: Y = keep ? X*scale : 0, plus residual
+ * when it is not null.  Element i of block b = i/8 draws 16 bits of Philox-4x32-10
+ * (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3", 2011) at counter
+ * (low word of b, high word of b, low word of offset, high word of offset) and key
+ * (low word of seed, high word of seed): word (i % 8)/2, its low half for even i.  It
+ * is kept where the draw is >= t = round(65536*p) (ties to even) and scale is
+ * 65536/(65536 - t); 0 <= p <= 1 is thus rounded to a multiple of 2^-16, and p = 1
+ * drops everything.  A dropped element does not enter the result (an infinity or NaN
+ * in X leaves no trace there).  Give every call its own (seed, offset); the backward
+ * pass takes its forward's.  All element types; Y may be X or residual. n <= 2^48. */
+dgrad_status_t dgrad_dropout_forward(int64_t n, dgrad_dtype_t dtype, double p, uint64_t seed, uint64_t offset,
+                                     const void* X, const void* residual, void* Y, void* stream);
+
+/* Its gradient, dX = keep ? dY*scale : 0 (the residual's gradient is dY itself).
+ * dX may be dY. */
+dgrad_status_t dgrad_dropout_backward(int64_t n, dgrad_dtype_t dtype, double p, uint64_t seed, uint64_t offset,
+                                      const void* dY, void* dX, void* stream);
+
 /* Output extents of the forward convolution the problem describes (host only,
  * no CUDA call).  Returns DGRAD_ERR_INVALID for an invalid problem. */
 dgrad_status_t dgrad_out_dims(const dgrad_problem_t* prob, int64_t* Ho, int64_t* Wo);
