@@ -21,6 +21,7 @@ import threading
 
 __all__ = ["pointwise", "pointwise_splitk", "pointwise_splitk_noalloc", "depthwise_tc", "depthwise_tc_workspace_bytes", "dense", "grouped", "splitk_workspace_bytes", "depthwise", "out_dims", "check_status", "DgradError", "DgradUnavailable",
            "layernorm_forward", "layernorm_backward", "layernorm_backward_workspace_bytes", "dropout_forward", "dropout_backward",
+           "gated_forward", "gated_backward", "gated_backward_workspace_bytes", "ACTIVATIONS",
            "Problem", "lib", "library_path", "selftest_timeout", "fma_probe", "STATUS"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -34,6 +35,7 @@ _lib = None
 STATUS = {0: "DGRAD_OK", 1: "DGRAD_ERR_INVALID", 2: "DGRAD_ERR_UNSUPPORTED", 3: "DGRAD_ERR_ALIGNMENT",
           4: "DGRAD_ERR_CUDA", 5: "DGRAD_ERR_TIMEOUT", 6: "DGRAD_ERR_BOUNDS"}
 DW_MODES = {"auto": 0, "rotated": 1, "rowstream": 2}
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}   # dgrad_act_t
 DTYPES = {"f32": 0, "bf16": 1, "f16": 2}
 SPLITK_SCRATCH_BYTES = 8 << 20   # DGRAD_SPLITK_SCRATCH_BYTES: the fixed per-device split-K buffer
 
@@ -116,6 +118,9 @@ def lib():
                     "layernorm_forward": [i64, i64, ci, dbl, vp, vp, vp, vp, vp, vp, vp],
                     "layernorm_backward": [i64, i64, ci, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
                     "layernorm_backward_workspace": [i64, i64, ci, P(sz)],
+                    "gated_forward": [i64, i64, i64, ci, ci, vp, vp, vp, vp, vp],
+                    "gated_backward": [i64, i64, i64, ci, ci, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+                    "gated_backward_workspace": [i64, i64, i64, P(sz)],
                     "dropout_forward": [i64, ci, dbl, u64, u64, vp, vp, vp, vp],
                     "dropout_backward": [i64, ci, dbl, u64, u64, vp, vp, vp]}.items():
                 f = getattr(L, "dgrad_" + name)
@@ -546,6 +551,86 @@ def layernorm_backward(dY, X, mean, rstd, gamma=None, param_grads=True, workspac
           _ptr(gamma), mean.data_ptr(), rstd.data_ptr(), out.data_ptr(), _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
           ws_bytes, stream=stream)
     return out, dgamma, dbeta
+
+
+def _act_code(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r}; use one of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[act]
+
+
+def _gated_width(W, C):
+    """F of W (2F, C)."""
+    if W.dim() != 2 or W.shape[1] != C or W.shape[0] % 2 or W.shape[0] == 0:
+        raise ValueError(f"expected W (2F, {C}), got {tuple(W.shape)}")
+    return W.shape[0] // 2
+
+
+def gated_forward(X, W, act="silu", preact=False, out=None, stream=None):
+    """Gated pointwise block (bf16 or f16; dgrad_gated_forward): H = act(X Wg^T) * (X Wu^T).
+
+    X (..., C); W (2F, C), the gate's F rows first -> H (..., F).  With ``preact`` the result
+    is (H, Z), the pre-activations (..., 2F) that gated_backward takes."""
+    _need_cuda(X, W)
+    code = _dtype_code(X)
+    acode = _act_code(act)
+    M, C = _rows_of(X)
+    F = _gated_width(W, C)
+    _like(W, W.shape, X.dtype, "W")
+    given = [out] if out is not None else []
+    _need_cuda(*given)
+    dev = _device_of(X, W, *given)
+    al = _Allocator(dev, stream)
+    shape = (*X.shape[:-1], F)
+    if out is None:
+        out = al.empty(shape, X.dtype)
+    else:
+        _like(out, shape, X.dtype, "out")
+    Z = al.empty((*X.shape[:-1], 2 * F), X.dtype) if preact else None
+    al.uses(X, W, *given)
+    _call(dev, "dgrad_gated_forward", lib().dgrad_gated_forward, M, C, F, code, acode, X.data_ptr(), W.data_ptr(),
+          out.data_ptr(), _ptr(Z), stream=stream)
+    return (out, Z) if preact else out
+
+
+def gated_backward_workspace_bytes(M, C, F) -> int:
+    """Workspace bytes gated_backward needs (host only)."""
+    nb = ctypes.c_size_t()
+    _check(lib().dgrad_gated_backward_workspace(int(M), int(C), int(F), ctypes.byref(nb)),
+           "dgrad_gated_backward_workspace")
+    return nb.value
+
+
+def gated_backward(dH, X, Z, W, act="silu", input_grad=True, weight_grad=True, workspace=None, stream=None):
+    """Gradients of gated_forward: (dX, dW) (bf16 or f16; dgrad_gated_backward).
+
+    Z: the pre-activations gated_forward kept.  Without ``input_grad`` dX, without
+    ``weight_grad`` dW is None and not computed.  workspace: a CUDA tensor of at least
+    gated_backward_workspace_bytes(...) bytes, taken from torch when None."""
+    import torch
+    _need_cuda(dH, X, Z, W)
+    code = _dtype_code(X)
+    acode = _act_code(act)
+    M, C = _rows_of(X)
+    F = _gated_width(W, C)
+    _like(W, W.shape, X.dtype, "W")
+    _like(dH, (*X.shape[:-1], F), X.dtype, "dH")
+    _like(Z, (*X.shape[:-1], 2 * F), X.dtype, "Z")
+    if not input_grad and not weight_grad:
+        raise ValueError("nothing to compute: neither input_grad nor weight_grad")
+    given = [workspace] if workspace is not None else []
+    _need_cuda(*given)
+    dev = _device_of(dH, X, Z, W, *given)
+    al = _Allocator(dev, stream)
+    dX = al.empty(X.shape, X.dtype) if input_grad else None
+    dW = al.empty(W.shape, W.dtype) if weight_grad else None
+    if workspace is None:
+        workspace = al.empty((max(gated_backward_workspace_bytes(M, C, F), 16),), torch.uint8)
+    al.uses(dH, X, Z, W, *given)
+    _call(dev, "dgrad_gated_backward", lib().dgrad_gated_backward, M, C, F, code, acode, dH.data_ptr(), X.data_ptr(),
+          Z.data_ptr(), W.data_ptr(), _ptr(dX), _ptr(dW), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), stream=stream)
+    return dX, dW
 
 
 def _counter(v, what):

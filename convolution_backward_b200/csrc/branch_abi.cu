@@ -1,5 +1,5 @@
 // branch_abi.cu -- the C entry points of the residual branch's operators (declared
-// in include/dgrad.h): layer norm and dropout, forward and backward.
+// in include/dgrad.h): layer norm, the gated pointwise block and dropout, forward and backward.
 //
 // Host side only: every argument is checked before anything is launched, then
 // the launchers enqueue their kernels on the caller's stream.
@@ -9,6 +9,7 @@
 
 #include "common.cuh"
 #include "dgrad.h"
+#include "gate_act.cuh"
 #include "launchers.h"
 
 namespace {
@@ -51,6 +52,25 @@ dgrad_status_t ln_shape(int64_t M, int64_t C, dgrad_dtype_t dtype)
     if (!valid_dtype(dtype) || M < 0 || C < 1) return DGRAD_ERR_INVALID;
     if (M > kMaxRows || C > kMaxChannels) return DGRAD_ERR_UNSUPPORTED;
     return DGRAD_OK;
+}
+
+dgrad_status_t gated_shape(int64_t M, int64_t C, int64_t F)
+{
+    if (M < 0 || C < 1 || F < 1) return DGRAD_ERR_INVALID;
+    if (M > kMaxRows || C > kMaxChannels || F > kMaxChannels / 2) return DGRAD_ERR_UNSUPPORTED;
+    if (C % 8 || F % 8) return DGRAD_ERR_ALIGNMENT;
+    return DGRAD_OK;
+}
+
+static_assert(int(DGRAD_ACT_SILU) == dgrad::kSilu && int(DGRAD_ACT_GELU) == dgrad::kGelu &&
+                  int(DGRAD_ACT_GELU_TANH) == dgrad::kGeluTanh && int(DGRAD_ACT_RELU) == dgrad::kRelu &&
+                  int(DGRAD_ACT_SIGMOID) == dgrad::kSigmoid,
+              "the kernels' activation codes are the ABI's");
+
+dgrad_status_t gated_types(dgrad_dtype_t dtype, dgrad_act_t act)
+{
+    if (!valid_dtype(dtype) || act < DGRAD_ACT_SILU || act > DGRAD_ACT_SIGMOID) return DGRAD_ERR_INVALID;
+    return dtype == DGRAD_F32 ? DGRAD_ERR_UNSUPPORTED : DGRAD_OK;
 }
 
 dgrad_status_t dropout_call(int64_t n, dgrad_dtype_t dtype, double p, uint64_t seed, uint64_t offset, const void* X,
@@ -152,6 +172,74 @@ dgrad_status_t dgrad_layernorm_backward(int64_t M, int64_t C, dgrad_dtype_t dtyp
     const dgrad::LnBwdArgs a{M, C, elem_kind(dtype), dY, X, gamma, mean, rstd, dX, dgamma, dbeta,
                              static_cast<float*>(workspace), status};
     return done(dgrad::launch_layernorm_backward(a, cs));
+}
+
+dgrad_status_t dgrad_gated_forward(int64_t M, int64_t C, int64_t F, dgrad_dtype_t dtype, dgrad_act_t act,
+                                   const void* X, const void* W, void* H, void* Z, void* stream)
+{
+    dgrad_status_t s = gated_types(dtype, act);
+    if (s == DGRAD_OK) s = gated_shape(M, C, F);
+    if (s != DGRAD_OK) return s;
+    if (M == 0) return DGRAD_OK;
+    if (!X || !W || !H) return DGRAD_ERR_INVALID;
+    if (!aligned16(X) || !aligned16(W) || !aligned16(H) || !aligned16(Z)) return DGRAD_ERR_ALIGNMENT;
+    const int64_t nx = M * C * 2, nw = 4 * F * C, nh = M * F * 2;
+    if (shared(H, nh, X, nx) || shared(H, nh, W, nw) || shared(Z, 2 * nh, X, nx) || shared(Z, 2 * nh, W, nw) ||
+        shared(Z, 2 * nh, H, nh))
+        return DGRAD_ERR_INVALID;
+    int* status = nullptr;
+    s = static_cast<dgrad_status_t>(dgrad::device_status_word(&status));
+    if (s != DGRAD_OK) return s;
+    const dgrad::GatedArgs a{M, C, F, dtype == DGRAD_F16, static_cast<int>(act), X, W, H, Z, status};
+    return done(dgrad::launch_gated_forward(a, static_cast<cudaStream_t>(stream)));
+}
+
+dgrad_status_t dgrad_gated_backward_workspace(int64_t M, int64_t C, int64_t F, size_t* bytes)
+{
+    if (!bytes) return DGRAD_ERR_INVALID;
+    const dgrad_status_t s = gated_shape(M, C, F);
+    if (s != DGRAD_OK) return s;
+    *bytes = M == 0 ? 0 : dgrad::gated_backward_workspace_bytes(M, C, F);
+    return DGRAD_OK;
+}
+
+dgrad_status_t dgrad_gated_backward(int64_t M, int64_t C, int64_t F, dgrad_dtype_t dtype, dgrad_act_t act,
+                                    const void* dH, const void* X, const void* Z, const void* W, void* dX, void* dW,
+                                    void* workspace, size_t workspace_bytes, void* stream)
+{
+    dgrad_status_t s = gated_types(dtype, act);
+    if (s == DGRAD_OK) s = gated_shape(M, C, F);
+    if (s != DGRAD_OK) return s;
+    if (!dX && !dW) return DGRAD_ERR_INVALID;
+    if (!aligned16(dH) || !aligned16(X) || !aligned16(Z) || !aligned16(W) || !aligned16(dX) || !aligned16(dW) ||
+        !aligned16(workspace))
+        return DGRAD_ERR_ALIGNMENT;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const int64_t nx = M * C * 2, nw = 4 * F * C, nh = M * F * 2;
+    if (M == 0)   // a sum over no rows
+        return dW ? done(cudaMemsetAsync(dW, 0, static_cast<size_t>(nw), cs)) : DGRAD_OK;
+    if (!dH || !Z || (dW && !X) || (dX && !W) || !workspace) return DGRAD_ERR_INVALID;
+    const size_t need = dgrad::gated_backward_workspace_bytes(M, C, F);
+    if (workspace_bytes < need) return DGRAD_ERR_INVALID;
+    const int64_t ws = static_cast<int64_t>(need);
+    struct Range {
+        const void* p;
+        int64_t n;
+    };
+    const Range out[3] = {{dX, nx}, {dW, nw}, {workspace, ws}};
+    const Range in[4] = {{dH, nh}, {X, dW ? nx : 0}, {Z, 2 * nh}, {W, dX ? nw : 0}};
+    for (int i = 0; i < 3; ++i) {
+        for (const Range& r : in)
+            if (shared(out[i].p, out[i].n, r.p, r.n)) return DGRAD_ERR_INVALID;
+        for (int j = 0; j < i; ++j)
+            if (shared(out[i].p, out[i].n, out[j].p, out[j].n)) return DGRAD_ERR_INVALID;
+    }
+    int* status = nullptr;
+    s = static_cast<dgrad_status_t>(dgrad::device_status_word(&status));
+    if (s != DGRAD_OK) return s;
+    const dgrad::GatedBwdArgs a{M, C, F, dtype == DGRAD_F16, static_cast<int>(act), dH, X, Z, W, dX, dW, workspace,
+                                status};
+    return done(dgrad::launch_gated_backward(a, cs));
 }
 
 dgrad_status_t dgrad_dropout_forward(int64_t n, dgrad_dtype_t dtype, double p, uint64_t seed, uint64_t offset,

@@ -254,6 +254,24 @@ int device_sm_count()
     return device_state(&st) == DGRAD_OK ? st->sms : 148;
 }
 
+bool encode_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
+                const uint64_t* strides, const uint32_t* box, bool swizzled)
+{
+    auto enc = tensor_map_encoder();
+    if (!enc || rank < 2 || rank > 5) return false;
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5];
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i + 1 < rank) s[i] = strides[i];
+    }
+    return enc(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, s, b, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int device_status_word(int** status)
 {
     DeviceState* st = nullptr;

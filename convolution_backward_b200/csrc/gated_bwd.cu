@@ -1,0 +1,438 @@
+// gated_bwd.cu -- gradients of the gated pointwise block H = act(G) * U, [G | U] = X W^T.
+//
+//     dZ = [dH U act'(G) | dH act(G)]          M x 2F, element by element
+//     dX = dZ W                                 M x C, sums over 2F
+//     dW = dZ^T X                               2F x C, sums over the M rows
+//
+// 8 M F C operations in two GEMMs of equal size; dZ is formed once, in fp32 from the
+// kept pre-activations, and rounded to the operands' 16 bits (the tensor cores take no
+// wider type at this rate; its rounding averages out over the sums) into the workspace,
+// from where both GEMMs read it.  dX is the pointwise dgrad GEMM with K = 2F.
+//
+// wgrad_pair_kernel: dW's tiles of 256 x BN on pairs of SMs.  The sums run over rows, so
+// both operands lie MN-major in memory (their columns contiguous) and go to the MMA as
+// they are: TMA boxes of 64 rows x 64 columns, 128-byte swizzle, descriptors with 8 KB
+// between the 64-column atoms.  A weight has few tiles and M is long, so the rows are
+// split over pairs until they fill the GPU; each split stores its fp32 tile into the
+// workspace and a second kernel adds the splits in order and rounds once (no atomics:
+// results repeat).  With one split the tile is rounded and stored directly.
+#include "common.cuh"
+#include "gate_act.cuh"
+#include "host_util.h"
+#include "launchers.h"
+
+namespace dgrad {
+namespace {
+
+constexpr int kBK = 64;
+constexpr int kThreads = 192;
+constexpr int kStages = 6;
+constexpr int kSms = 148;   // a B200; splits and workspaces must not depend on the device asked
+
+// ------------------------------------------------------------------- dZ
+
+// Eight columns per thread: 16 bytes of dH, G and U in, 16 bytes of dG and dU out.
+template <bool F16>
+__global__ void __launch_bounds__(256) gated_dz_kernel(const uint16_t* dH, const uint16_t* Z, uint16_t* dZ,
+                                                       long long nvec, int nv, int act, long long bytes, int* status)
+{
+    pdl_wait();      // the previous kernel on the stream has finished
+    pdl_trigger();   // the next one may start its set-up
+    constexpr int EK = F16 ? kF16 : kBF16;
+    const long long stride = static_cast<long long>(gridDim.x) * 256;
+    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < nvec; i += stride) {
+        const long long m = i / nv;
+        const long long g_at = m * 2 * nv + (i - m * nv);
+        const uint4 h = reinterpret_cast<const uint4*>(dH)[i];
+        const uint4 g = reinterpret_cast<const uint4*>(Z)[g_at];
+        const uint4 u = reinterpret_cast<const uint4*>(Z)[g_at + nv];
+        const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
+        uint32_t a[4], b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 hf = h16x2_to_float2<EK>(hw[j]), gf = h16x2_to_float2<EK>(gw[j]);
+            const float2 uf = h16x2_to_float2<EK>(uw[j]);
+            const float2 lo = gate_act_grad(act, gf.x), hi = gate_act_grad(act, gf.y);
+            a[j] = float2_to_h16x2<EK>(hf.x * uf.x * lo.y, hf.y * uf.y * hi.y);
+            b[j] = float2_to_h16x2<EK>(hf.x * lo.x, hf.y * hi.x);
+        }
+        uint4* out = reinterpret_cast<uint4*>(dZ) + g_at;
+        if (store_ok(dZ, bytes, out, 16, status)) out[0] = make_uint4(a[0], a[1], a[2], a[3]);
+        if (store_ok(dZ, bytes, out + nv, 16, status)) out[nv] = make_uint4(b[0], b[1], b[2], b[3]);
+    }
+}
+
+// ------------------------------------------------------------------- dW
+
+template <int BN>
+struct WgLayout {
+    static constexpr int kBHalf = (BN / 2) * kBK * 2;   // this CTA's X columns, one k-block
+    static constexpr int kStage = 16384 + kBHalf;
+    static constexpr int kEpi = kStages * kStage;       // 2 x 16 KB staging
+    static constexpr int kBars = kEpi + 2 * 16384;
+    static constexpr int kNumBars = 2 * kStages + 5;
+    static constexpr int kBytes = kBars + kNumBars * 8 + 16;
+    static constexpr int kAlloc = kBytes + 1024;
+};
+
+struct WgPlan {
+    int bn, splits, kb_per;   // k-blocks of 64 rows per split
+};
+
+// One launch's units: (tile of 256 x BN, split).  map_a: dZ, map_b: X (both 2-D, box 64 x
+// 64); map_d: dW (2-D, box 64 x 128) or, PART, the fp32 partials (3-D [split][2F][C],
+// box 32 x 128 x 1), all swizzled.
+template <int BN, bool PART, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    wgrad_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                      const __grid_constant__ CUtensorMap map_d, int M, int N2, int C, int splits, int kb_per,
+                      int* status)
+{
+    pdl_wait();      // the previous kernel on the stream has finished
+    pdl_trigger();   // the next one may start its set-up
+    using L = WgLayout<BN>;
+    constexpr int EK = F16 ? kF16 : kBF16;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
+    uint64_t* full = bars;                  // used in the rank-0 CTA
+    uint64_t* empty = bars + kStages;       // each CTA's own
+    uint64_t* tfull = bars + 2 * kStages;   // each CTA's own
+    uint64_t* tempty = tfull + 2;           // used in the rank-0 CTA
+    uint64_t* drain = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int num_n = (C + BN - 1) / BN;
+    const int num_kb = (M + kBK - 1) / kBK;
+    const int units = ((N2 + 255) / 256) * num_n * splits;
+    const int pair = blockIdx.x >> 1;
+    const int num_pairs = gridDim.x >> 1;
+    // unit -> row block of dW, column block, split; its k-blocks
+    auto unit = [&](int t, int& r0, int& c0, int& sp, int& kb0, int& kb1) {
+        sp = t % splits;
+        const int tile = t / splits;
+        r0 = (tile / num_n) * 256 + rank * 128;
+        c0 = (tile % num_n) * BN;
+        kb0 = sp * kb_per;
+        kb1 = min(num_kb, kb0 + kb_per);
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&tfull[a], 1);
+            mbar_init(&tempty[a], 256);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&map_a);
+        tma_prefetch_desc(&map_b);
+        tma_prefetch_desc(&map_d);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 2 * BN);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync();                          // barriers of both CTAs exist before any remote arrive
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint32_t full0 = leader_addr(&full[0]);
+            int stage = 0;
+            uint32_t phase = 0;
+            long long issued = 0;
+            bool ok = true;
+            for (int t = pair; t < units && ok; t += num_pairs) {
+                int r0, c0, sp, kb0, kb1;
+                unit(t, r0, c0, sp, kb0, kb1);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * L::kStage);
+                    uint8_t* a_tile = smem + stage * L::kStage;
+                    uint8_t* b_tile = a_tile + 16384;
+                    const uint32_t fb = full0 + static_cast<uint32_t>(stage * 8);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        tma_load_2d_pair(a_tile + j * 8192, &map_a, fb, r0 + j * 64, kb * kBK);
+#pragma unroll
+                    for (int j = 0; j < BN / 128; ++j)
+                        tma_load_2d_pair(b_tile + j * 8192, &map_b, fb, c0 + rank * (BN / 2) + j * 64, kb * kBK);
+                    ++issued;
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                report_timeout(status);
+                *abort_flag = 1;
+            }
+            // the last loads of this CTA land before it may exit: wait until the MMAs
+            // that read them have released the stages (multicast commit)
+            for (long long i = (issued > kStages ? issued - kStages : 0); i < issued; ++i)
+                if (!mbar_wait(&empty[i % kStages], static_cast<uint32_t>((i / kStages) & 1))) {
+                    report_timeout(status);
+                    *abort_flag = 1;
+                }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc =
+                (F16 ? idesc_f16_f32(256, BN, /*b_mn_major=*/true) : idesc_bf16_f32(256, BN, true)) | kIdescAMnMajor;
+            int stage = 0;
+            uint32_t phase = 0;
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            bool ok = true;
+            for (int t = pair; t < units && ok; t += num_pairs) {
+                int r0, c0, sp, kb0, kb1;
+                unit(t, r0, c0, sp, kb0, kb1);
+                if (!mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(&full[stage], phase, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a_addr = smem_u32(smem + stage * L::kStage);
+                    const uint32_t b_addr = a_addr + 16384;
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk)   // 16 rows: two groups of 8 rows of 128 bytes
+                        umma_f16_pair(d_tmem, sw128_desc(a_addr + kk * 2048, 8192, 1024),
+                                      sw128_desc(b_addr + kk * 2048, 8192, 1024), idesc,
+                                      (kb > kb0 || kk > 0) ? 1u : 0u);
+                    umma_commit_pair(&empty[stage]);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                umma_commit_pair(&tfull[acc]);
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            if (!ok) {
+                report_timeout(status);
+                *abort_flag = 1;
+            }
+            umma_commit_pair(drain);
+            if (!mbar_wait(drain, 0)) {
+                report_timeout(status);
+                *abort_flag = 1;
+            }
+        }
+    } else {
+        constexpr int kCols = PART ? 32 : 64;     // columns of one 16 KB staging box
+        const int quarter = warp & 3;
+        const int row = quarter * 32 + lane;
+        const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+        const bool issuer = warp == 2 && lane == 0;
+        const uint32_t tempty0 = leader_addr(&tempty[0]);
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        for (int t = pair; t < units; t += num_pairs) {
+            int r0, c0, sp, kb0, kb1;
+            unit(t, r0, c0, sp, kb0, kb1);
+            ok = named_barrier_and(1, 128, mbar_wait_cluster(&tfull[acc], acc_phase, abort_flag));
+            if (!ok) break;                       // the epilogue warps leave together
+            tc_fence_after();
+#pragma unroll 1
+            for (int chunk = 0; chunk < BN / kCols; ++chunk) {
+                const int c = c0 + chunk * kCols;
+                uint8_t* buf = smem + L::kEpi + (chunk & 1) * 16384;
+                uint8_t* rowp = buf + row * 128;
+                if (issuer) bulk_wait_group_read<1>();
+                named_barrier_sync(1, 128);
+                uint32_t v[kCols];
+#pragma unroll
+                for (int q = 0; q < kCols / 32; ++q)
+                    tmem_ld_32x32b_x32(tmem_base + lane_addr + static_cast<uint32_t>(acc * BN + chunk * kCols + q * 32),
+                                       *reinterpret_cast<uint32_t(*)[32]>(&v[q * 32]));
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    uint4 o;
+                    if constexpr (PART) {
+                        o = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    } else {
+                        o.x = float2_to_h16x2<EK>(__uint_as_float(v[8 * j + 0]), __uint_as_float(v[8 * j + 1]));
+                        o.y = float2_to_h16x2<EK>(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3]));
+                        o.z = float2_to_h16x2<EK>(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5]));
+                        o.w = float2_to_h16x2<EK>(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7]));
+                    }
+                    *reinterpret_cast<uint4*>(rowp + ((j ^ (row & 7)) << 4)) = o;
+                }
+                fence_proxy_async_smem();
+                named_barrier_sync(1, 128);
+                if (issuer) {
+                    if (c < C && r0 < N2) {       // the map clips the tails
+                        if constexpr (PART)
+                            tma_store_3d(&map_d, buf, c, r0, sp);
+                        else
+                            tma_store_2d(&map_d, buf, c, r0);
+                    }
+                    bulk_commit_group();
+                }
+            }
+            tc_fence_before();
+            mbar_arrive_cluster(tempty0 + static_cast<uint32_t>(acc * 8));
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+        if (!ok) {
+            report_timeout(status);
+            *abort_flag = 1;
+        }
+        if (issuer) bulk_wait_group<0>();
+    }
+
+    tc_fence_before();
+    cluster_sync();                              // no CTA leaves while its pair still needs it
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc_pair(tmem_base, 2 * BN);
+    }
+}
+
+// Tile width and row splits of dW.
+WgPlan wgrad_plan(int64_t M, int64_t N2, int64_t C)
+{
+    WgPlan p;
+    p.bn = C > 128 ? 256 : 128;
+    const int64_t tiles = ((N2 + 255) / 256) * ((C + p.bn - 1) / p.bn);
+    const int64_t num_kb = (M + kBK - 1) / kBK;
+    int64_t s = (kSms / 2) / tiles;
+    if (s > num_kb / 4) s = num_kb / 4;   // a split too short is all start-up and epilogue
+    if (s < 1) s = 1;
+    p.kb_per = static_cast<int>((num_kb + s - 1) / s);
+    p.splits = static_cast<int>((num_kb + p.kb_per - 1) / p.kb_per);   // no empty split
+    return p;
+}
+
+// dX runs split-K when its tiles would leave most SMs idle; the count is fixed by the sizes.
+int dx_splits(int64_t M, int64_t K, int64_t C)
+{
+    const int64_t tiles = ((M + 127) / 128) * ((C + 127) / 128);
+    if (tiles * 4 > kSms) return 1;
+    int64_t s = kSms / tiles;
+    const int64_t num_kb = (K + kBK - 1) / kBK;
+    if (s > num_kb / 2) s = num_kb / 2;
+    if (s > 32) s = 32;
+    return s < 1 ? 1 : static_cast<int>(s);
+}
+
+size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+template <int BN, bool PART, bool F16>
+cudaError_t run_wgrad(const GatedBwdArgs& a, const void* dZ, void* dst, const WgPlan& p, cudaStream_t stream)
+{
+    using L = WgLayout<BN>;
+    static_assert(L::kAlloc <= 232448, "shared memory budget");
+    const CUtensorMapDataType t = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint64_t M = static_cast<uint64_t>(a.M), C = static_cast<uint64_t>(a.C), N2 = 2 * static_cast<uint64_t>(a.F);
+    const uint64_t da[2] = {N2, M}, sa[1] = {2 * N2}, db[2] = {C, M}, sb[1] = {2 * C};
+    const uint32_t box[2] = {64, 64}, bd[2] = {64, 128}, bp[3] = {32, 128, 1};
+    const uint64_t dd[2] = {C, N2}, sd[1] = {2 * C};
+    const uint64_t dp[3] = {C, N2, static_cast<uint64_t>(p.splits)}, sp[2] = {4 * C, 4 * C * N2};
+    CUtensorMap ma, mb, md;
+    if (!encode_map(&ma, t, 2, dZ, da, sa, box, true) || !encode_map(&mb, t, 2, a.X, db, sb, box, true))
+        return cudaErrorInvalidValue;
+    if (!(PART ? encode_map(&md, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, dst, dp, sp, bp, true)
+               : encode_map(&md, t, 2, dst, dd, sd, bd, true)))
+        return cudaErrorInvalidValue;
+    auto kern = wgrad_pair_kernel<BN, PART, F16>;
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), L::kAlloc);
+    if (e != cudaSuccess) return e;
+    const int64_t units = static_cast<int64_t>((N2 + 255) / 256 * ((C + BN - 1) / BN)) * p.splits;
+    const int64_t most = device_sm_count() / 2;
+    const unsigned pairs = static_cast<unsigned>(units < most ? units : most);
+    return launch_kernel(kern, dim3(2 * pairs), dim3(kThreads), L::kAlloc, stream, 2, ma, mb, md,
+                         static_cast<int>(a.M), static_cast<int>(N2), static_cast<int>(a.C), p.splits, p.kb_per,
+                         a.status);
+}
+
+template <bool F16>
+cudaError_t run(const GatedBwdArgs& a, cudaStream_t stream)
+{
+    const int64_t N2 = 2 * a.F;
+    uint16_t* dZ = static_cast<uint16_t*>(a.ws);
+    const size_t dz_bytes = static_cast<size_t>(a.M) * N2 * 2;
+    // dX's and dW's partials share the rest: dX's are read before dW's kernel begins to write
+    float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + align256(dz_bytes));
+    const long long nvec = a.M * (a.F / 8);
+    const long long blocks = (nvec + 255) / 256, most = 64LL * kSms;
+    cudaError_t e = launch_kernel(gated_dz_kernel<F16>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
+                                  dim3(256), 0, stream, 1, static_cast<const uint16_t*>(a.dH),
+                                  static_cast<const uint16_t*>(a.Z), dZ, nvec, static_cast<int>(a.F / 8), a.act,
+                                  static_cast<long long>(dz_bytes), a.status);
+    if (e != cudaSuccess) return e;
+    if (a.dX) {
+        const CUtensorMapDataType t = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        const PwArgs g{a.M, N2, a.C, dZ, a.W, a.dX, a.status, F16};
+        const uint64_t M = static_cast<uint64_t>(a.M), C = static_cast<uint64_t>(a.C), K = static_cast<uint64_t>(N2);
+        const uint64_t da[2] = {K, M}, sa[1] = {2 * K}, db[2] = {C, K}, sb[1] = {2 * C}, dd[2] = {C, M};
+        const uint32_t tall[2] = {64, 128}, sq[2] = {64, 64};
+        CUtensorMap ma, mb, md;
+        if (!encode_map(&ma, t, 2, dZ, da, sa, tall, true) || !encode_map(&mb, t, 2, a.W, db, sb, sq, true) ||
+            !encode_map(&md, t, 2, a.dX, dd, sb, tall, true))
+            return cudaErrorInvalidValue;
+        const int splits = dx_splits(a.M, N2, a.C);
+        e = splits > 1 ? launch_pointwise_tc_splitk(g, ma, mb, splits, part, device_sm_count(), stream)
+                       : launch_pointwise_tc_pair(g, ma, mb, md, a.C > 128 ? 256 : 128, device_sm_count(), stream);
+        if (e != cudaSuccess) return e;
+    }
+    if (!a.dW) return cudaSuccess;
+    const WgPlan p = wgrad_plan(a.M, N2, a.C);
+    if (p.splits == 1)
+        return p.bn == 256 ? run_wgrad<256, false, F16>(a, dZ, a.dW, p, stream)
+                           : run_wgrad<128, false, F16>(a, dZ, a.dW, p, stream);
+    e = p.bn == 256 ? run_wgrad<256, true, F16>(a, dZ, part, p, stream)
+                    : run_wgrad<128, true, F16>(a, dZ, part, p, stream);
+    if (e != cudaSuccess) return e;
+    return launch_splitk_reduce(part, a.dW, N2 * a.C, p.splits, F16, a.status, stream);
+}
+
+}  // namespace
+
+size_t gated_backward_workspace_bytes(int64_t M, int64_t C, int64_t F)
+{
+    const int64_t N2 = 2 * F;
+    const WgPlan p = wgrad_plan(M, N2, C);
+    const int s = dx_splits(M, N2, C);
+    const size_t dw = p.splits > 1 ? static_cast<size_t>(p.splits) * N2 * C * 4 : 0;
+    const size_t dx = s > 1 ? static_cast<size_t>(s) * M * C * 4 : 0;
+    return align256(static_cast<size_t>(M) * N2 * 2) + (dw > dx ? dw : dx);
+}
+
+cudaError_t launch_gated_backward(const GatedBwdArgs& a, cudaStream_t stream)
+{
+    return a.f16 ? run<true>(a, stream) : run<false>(a, stream);
+}
+
+}  // namespace dgrad

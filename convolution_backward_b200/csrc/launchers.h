@@ -17,7 +17,7 @@ struct PwArgs {
     const void* W;
     void* dX;
     int* status;  // device status word
-    bool f16;     // 16-bit operands are f16 (split-K path; bf16 otherwise)
+    bool f16;     // 16-bit operands are f16 (split-K and pair kernels; bf16 otherwise)
 };
 
 // fp32 in / fp32 out, fp32 FMA (no reduced-precision tensor-core path).
@@ -51,6 +51,10 @@ int pointwise_splitk_auto(const PwArgs& a, int num_sms);
 size_t pointwise_splitk_workspace_bytes(const PwArgs& a, int splits);
 cudaError_t launch_pointwise_tc_splitk(const PwArgs& a, const CUtensorMap& map_a, const CUtensorMap& map_b,
                                        int splits, float* ws, int num_sms, cudaStream_t stream);
+
+// out[i] = round(sum over s of ws[s][i]), s in increasing order; n a multiple of 8.
+cudaError_t launch_splitk_reduce(const float* ws, void* out, int64_t n, int splits, bool f16, int* status,
+                                 cudaStream_t stream);
 
 // Dense or grouped KH x KW dgrad on tcgen05, by output phase (S*S sub-GEMMs),
 // bf16 or f16 (f16 = true).  G groups of Kg dY and Cg dX channels; W is
@@ -212,6 +216,43 @@ struct DropArgs {
     int* status;
 };
 cudaError_t launch_dropout(const DropArgs& a, cudaStream_t stream);
+
+// Gated pointwise block: Z = [G | U] = X W^T with X [M][C] and W [2F][C], H = act(G) U.
+// act is a dgrad_act_t.  Z null: the pre-activations are not kept.
+struct GatedArgs {
+    int64_t M, C, F;
+    bool f16;
+    int act;
+    const void* X;
+    const void* W;
+    void* H;
+    void* Z;
+    int* status;
+};
+cudaError_t launch_gated_forward(const GatedArgs& a, cudaStream_t stream);
+
+// Its gradients: dZ = [dH U act'(G) | dH act(G)] (in the workspace), dX = dZ W and
+// dW = dZ^T X; dX or dW null: not computed.
+struct GatedBwdArgs {
+    int64_t M, C, F;
+    bool f16;
+    int act;
+    const void* dH;
+    const void* X;
+    const void* Z;
+    const void* W;
+    void* dX;
+    void* dW;
+    void* ws;
+    int* status;
+};
+size_t gated_backward_workspace_bytes(int64_t M, int64_t C, int64_t F);
+cudaError_t launch_gated_backward(const GatedBwdArgs& a, cudaStream_t stream);
+
+// Encode a tensor map over a dense tensor (dims inner first, strides in bytes of the
+// outer dimensions, zero fill); swizzled: 128-byte swizzle.  Nothing is kept.
+bool encode_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
+                const uint64_t* strides, const uint32_t* box, bool swizzled);
 
 // Number of SMs of the current device (cached per device).
 int device_sm_count();

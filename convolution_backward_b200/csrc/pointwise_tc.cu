@@ -566,12 +566,13 @@ struct PwPairLayout {
     static constexpr int kAlloc = kBytes + 1024;
 };
 
-template <int BN, int STAGES>
+template <int BN, int STAGES, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
     pw_tc_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                       const __grid_constant__ CUtensorMap map_d, int M, int C, int K, int* status)
 {
     using L = PwPairLayout<BN, STAGES>;
+    constexpr int EK = F16 ? kF16 : kBF16;
     constexpr int kPairStages = STAGES;
     {
         // While the previous kernel may still run, only L2 prefetches of this CTA's first
@@ -691,8 +692,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
-            constexpr uint32_t idesc_full = idesc_bf16_f32(256, BN, /*b_mn_major=*/true);
-            constexpr uint32_t idesc_half = idesc_bf16_f32(256, BN / 2, /*b_mn_major=*/true);
+            constexpr uint32_t idesc_full =
+                F16 ? idesc_f16_f32(256, BN, /*b_mn_major=*/true) : idesc_bf16_f32(256, BN, /*b_mn_major=*/true);
+            constexpr uint32_t idesc_half = F16 ? idesc_f16_f32(256, BN / 2, /*b_mn_major=*/true)
+                                                : idesc_bf16_f32(256, BN / 2, /*b_mn_major=*/true);
             int stage = 0;
             uint32_t phase = 0;
             int acc = 0;
@@ -770,10 +773,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     uint4 o;
-                    o.x = float2_to_bf16x2(__uint_as_float(v[8 * j + 0]), __uint_as_float(v[8 * j + 1]));
-                    o.y = float2_to_bf16x2(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3]));
-                    o.z = float2_to_bf16x2(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5]));
-                    o.w = float2_to_bf16x2(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7]));
+                    o.x = float2_to_h16x2<EK>(__uint_as_float(v[8 * j + 0]), __uint_as_float(v[8 * j + 1]));
+                    o.y = float2_to_h16x2<EK>(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3]));
+                    o.z = float2_to_h16x2<EK>(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5]));
+                    o.w = float2_to_h16x2<EK>(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7]));
                     *reinterpret_cast<uint4*>(rowp + ((j ^ (row & 7)) << 4)) = o;
                 }
                 fence_proxy_async_smem();
@@ -1088,13 +1091,13 @@ cudaError_t launch_res(const PwArgs& a, const CUtensorMap& map_a, const CUtensor
     return cudaGetLastError();
 }
 
-template <int BN, int STAGES>
+template <int BN, int STAGES, bool F16>
 cudaError_t launch_pair(const PwArgs& a, const CUtensorMap& map_a, const CUtensorMap& map_b,
                         const CUtensorMap& map_d, int num_sms, cudaStream_t stream)
 {
     using L = PwPairLayout<BN, STAGES>;
     static_assert(L::kAlloc <= 232448, "shared memory budget");
-    auto kern = pw_tc_pair_kernel<BN, STAGES>;
+    auto kern = pw_tc_pair_kernel<BN, STAGES, F16>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), L::kAlloc);
     if (e != cudaSuccess) return e;
     const int num_tiles = static_cast<int>(((a.M + 255) / 256) * ((a.C + BN - 1) / BN));
@@ -1161,24 +1164,28 @@ cudaError_t launch_pointwise_tc_splitk(const PwArgs& a, const CUtensorMap& map_a
     }
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const long long MC = a.M * a.C;
-    const long long threads = (MC + 7) / 8;
-    auto reduce = a.f16 ? splitk_reduce_kernel<true> : splitk_reduce_kernel<false>;
-    {
-        const cudaError_t le_ = launch_kernel(reduce, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, stream, 1,
-                                             ws, static_cast<uint16_t*>(a.dX), MC,
-                                                                             S, a.status);
-        if (le_ != cudaSuccess) return le_;
-    }
-    return cudaGetLastError();
+    return launch_splitk_reduce(ws, a.dX, a.M * a.C, S, a.f16, a.status, stream);
+}
+
+cudaError_t launch_splitk_reduce(const float* ws, void* out, int64_t n, int splits, bool f16, int* status,
+                                 cudaStream_t stream)
+{
+    const long long threads = (n + 7) / 8;
+    auto reduce = f16 ? splitk_reduce_kernel<true> : splitk_reduce_kernel<false>;
+    const cudaError_t e = launch_kernel(reduce, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, stream,
+                                        1, ws, static_cast<uint16_t*>(out), static_cast<long long>(n), splits, status);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_pointwise_tc_pair(const PwArgs& a, const CUtensorMap& map_a, const CUtensorMap& map_b,
                                      const CUtensorMap& map_d, int bn, int num_sms, cudaStream_t stream)
 {
     if (a.M <= 0) return cudaSuccess;
-    if (bn == 256) return launch_pair<256, 6>(a, map_a, map_b, map_d, num_sms, stream);
-    return launch_pair<128, 8>(a, map_a, map_b, map_d, num_sms, stream);
+    if (bn == 256)
+        return a.f16 ? launch_pair<256, 6, true>(a, map_a, map_b, map_d, num_sms, stream)
+                     : launch_pair<256, 6, false>(a, map_a, map_b, map_d, num_sms, stream);
+    return a.f16 ? launch_pair<128, 8, true>(a, map_a, map_b, map_d, num_sms, stream)
+                 : launch_pair<128, 8, false>(a, map_a, map_b, map_d, num_sms, stream);
 }
 
 bool pointwise_tc_resident_ok(const PwArgs& a, int num_sms)

@@ -252,6 +252,42 @@ dgrad_status_t dgrad_layernorm_backward(int64_t M, int64_t C, dgrad_dtype_t dtyp
 /* Workspace bytes dgrad_layernorm_backward needs (host only, no CUDA call). */
 dgrad_status_t dgrad_layernorm_backward_workspace(int64_t M, int64_t C, dgrad_dtype_t dtype, size_t* bytes);
 
+/* The gate's activation: silu g/(1 + exp(-g)); gelu g*P(g) with the normal
+ * distribution P (exact) or its tanh form g*(1 + tanh(sqrt(2/pi)*(g + 0.044715 g^3)))/2;
+ * relu max(g, 0); sigmoid 1/(1 + exp(-g)). */
+typedef enum {
+    DGRAD_ACT_SILU = 0, DGRAD_ACT_GELU = 1, DGRAD_ACT_GELU_TANH = 2, DGRAD_ACT_RELU = 3, DGRAD_ACT_SIGMOID = 4
+} dgrad_act_t;
+
+/* Gated pointwise block in one kernel: two 1x1 projections of C to F channels, the
+ * activation and the product,
+ *     Z = [G | U] = X . W^T  (M x 2F),   H = act(G)*U  (M x F),
+ * X [M][C], W [2F][C] (rows 0..F-1 the gate's, rows F..2F-1 the other projection's: a
+ * pointwise filter with 2F output channels), H [M][F].  H comes from the fp32
+ * accumulators.  Z [M][2F], rounded to the element type, is what the backward pass
+ * takes; null: not kept.  DGRAD_BF16 or DGRAD_F16 (else DGRAD_ERR_UNSUPPORTED) on the
+ * tcgen05 tensor cores; up to eight rows run on a kernel that reads W once.  C and F
+ * multiples of 8 (else DGRAD_ERR_ALIGNMENT); C <= 65536, F <= 32768, M < 2^31 (else
+ * DGRAD_ERR_UNSUPPORTED).  H and Z overlap nothing. */
+dgrad_status_t dgrad_gated_forward(int64_t M, int64_t C, int64_t F, dgrad_dtype_t dtype, dgrad_act_t act,
+                                   const void* X, const void* W, void* H, void* Z, void* stream);
+
+/* Its gradients from dH [M][F], X, the kept Z and W:
+ *     dZ = [dH*U*act'(G) | dH*act(G)],   dX = dZ . W,   dW = dZ^T . X.
+ * dX or dW null: not computed (X is then needed for dW only, W for dX only; both null:
+ * DGRAD_ERR_INVALID).  dZ is computed in fp32 and rounded to the element type, the
+ * operand type of both products.  Types and limits as dgrad_gated_forward.
+ * workspace (16-byte aligned, at least dgrad_gated_backward_workspace bytes; contents
+ * do not matter and are clobbered) holds dZ and fp32 partial sums; too small or null:
+ * DGRAD_ERR_INVALID.  Two calls that may overlap need a workspace each.  dX, dW and
+ * the workspace overlap nothing. */
+dgrad_status_t dgrad_gated_backward(int64_t M, int64_t C, int64_t F, dgrad_dtype_t dtype, dgrad_act_t act,
+                                    const void* dH, const void* X, const void* Z, const void* W, void* dX, void* dW,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes dgrad_gated_backward needs (host only, no CUDA call). */
+dgrad_status_t dgrad_gated_backward_workspace(int64_t M, int64_t C, int64_t F, size_t* bytes);
+
 /* Dropout of n elements with no stored mask: Y = keep ? X*scale : 0, plus residual
  * when it is not null.  Element i of block b = i/8 draws 16 bits of Philox-4x32-10
  * (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3", 2011) at counter
