@@ -69,6 +69,8 @@ def library_path() -> str:
 def lib():
     """The loaded libdgrad (ctypes.CDLL) with argument types declared."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):
@@ -150,18 +152,24 @@ def _device_of(*ts):
     """The one CUDA device every tensor in `ts` lives on.  The C ABI works on the
     current device, so the wrappers make this device current around each call;
     tensors on different devices are refused."""
-    devs = {(t.device.type, t.device.index) for t in ts}
-    if len(devs) != 1:
-        raise ValueError("all tensors of one call must be on the same CUDA device, got "
-                         + ", ".join(sorted(f"{d[0]}:{d[1]}" for d in devs)))
-    return ts[0].device
+    dev = ts[0].device
+    for t in ts:
+        if t.device != dev:
+            raise ValueError("all tensors of one call must be on the same CUDA device, got "
+                             + ", ".join(sorted({f"{d.type}:{d.index}" for d in (u.device for u in ts)})))
+    return dev
 
 
 def _call(dev, what, fn, *args, stream=None):
     """Run C entry point `fn` with `dev` current and its stream appended."""
     import torch
-    with torch.cuda.device(dev):
-        _check(fn(*args, _stream_ptr(stream, dev)), what)
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, _stream_ptr(stream, dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream_ptr(stream, dev))
+    if status != 0:
+        _check(status, what)
 
 
 def _code_of(dtype) -> int:
