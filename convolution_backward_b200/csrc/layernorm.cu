@@ -134,15 +134,23 @@ struct LnParam {
     }
 };
 
+// Vectors (or elements) of a row that this lane holds: the first `mine` of its NV.
+template <int VEC>
+__device__ __forceinline__ int lane_vectors(int C, int T, int lane)
+{
+    const int n = C / VEC;
+    return lane < n ? (n - lane + T - 1) / T : 0;
+}
+
 // Zero the elements of unit u that lie behind the row's end (whole vectors, or either element).
 template <int VEC, int PER>
-__device__ __forceinline__ void mask_unit(int u, int C, int T, int lane, float2 (&f)[PER])
+__device__ __forceinline__ void mask_unit(int u, int mine, float2 (&f)[PER])
 {
     if constexpr (VEC == 1) {
-        if (lane + 2 * u * T >= C) f[0].x = 0.f;
-        if (lane + (2 * u + 1) * T >= C) f[0].y = 0.f;
+        if (2 * u >= mine) f[0].x = 0.f;
+        if (2 * u + 1 >= mine) f[0].y = 0.f;
     } else {
-        if ((lane + u * T) * VEC >= C) {
+        if (u >= mine) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) f[i] = make_float2(0.f, 0.f);
         }
@@ -332,6 +340,7 @@ __global__ void __launch_bounds__(MODE == 2 ? kLnMaxMulti : kLnBlock, ln_per_sm(
     const int lane = threadIdx.x - group * p.T;
     int turn = 0;
     const float fc = static_cast<float>(p.C);
+    const int mine = lane_vectors<VEC>(p.C, p.T, lane);
 
     // gamma and beta: in registers where whole warps share a row; where a row takes at most a
     // warp, every lane meets few of them often, and reads them widened from shared memory
@@ -341,15 +350,13 @@ __global__ void __launch_bounds__(MODE == 2 ? kLnMaxMulti : kLnBlock, ln_per_sm(
     gamma.init(params, p.gamma, 1.0f, p.C, p.T, lane);
     beta.init(params + p.C, p.beta, 0.f, p.C, p.T, lane);
     if constexpr (!MULTI) __syncthreads();
-    // row m, elements `at` of `from`; every thread of the block takes part in each reduction
-    auto one_row = [&](long long m, bool live, const void* from, long long at) {
-        const long long row = m * p.C;
+    // row m, read from `from`; every thread of the block takes part in each reduction
+    auto one_row = [&](long long m, bool live, const void* from) {
         P x;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = (lane + v * p.T) * VEC;
             x.v[v].zero();
-            if (live && c < p.C) x.v[v].load(from, at + c);
+            if (live && v < mine) x.v[v].load(from, (lane + v * p.T) * VEC);
         }
         float2 s = make_float2(0.f, 0.f);
 #pragma unroll
@@ -368,7 +375,7 @@ __global__ void __launch_bounds__(MODE == 2 ? kLnMaxMulti : kLnBlock, ln_per_sm(
             x.unit(u, f);
 #pragma unroll
             for (int i = 0; i < kPer; ++i) f[i] = __fadd2_rn(f[i], minus);
-            mask_unit<VEC>(u, p.C, p.T, lane, f);
+            mask_unit<VEC>(u, mine, f);
 #pragma unroll
             for (int i = 0; i < kPer; ++i) ss = ffma2(f[i], f[i], ss);
         }
@@ -382,7 +389,7 @@ __global__ void __launch_bounds__(MODE == 2 ? kLnMaxMulti : kLnBlock, ln_per_sm(
 #pragma unroll
         for (int u = 0; u < P::kUnits; ++u) {
             float2 f[kPer], g[kPer], b[kPer];
-            if (VEC > 1 && (lane + u * p.T) * VEC >= p.C) continue;
+            if (VEC > 1 && u >= mine) continue;
             x.unit(u, f);
             gamma.unit(u, p.C, p.T, lane, g);
             beta.unit(u, p.C, p.T, lane, b);
@@ -390,24 +397,23 @@ __global__ void __launch_bounds__(MODE == 2 ? kLnMaxMulti : kLnBlock, ln_per_sm(
             for (int i = 0; i < kPer; ++i) f[i] = ffma2(__fmul2_rn(__fadd2_rn(f[i], minus), r2), g[i], b[i]);
             x.set_unit(u, f);
         }
+        char* out = static_cast<char*>(p.y) + m * p.C * es;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (lane + v * p.T) * VEC;
-            if (c < p.C &&
-                store_ok(p.y, p.M * p.C * es, static_cast<char*>(p.y) + (row + c) * es, VEC * es, p.status))
-                x.v[v].store(p.y, row + c);
+            if (v < mine && store_ok(p.y, p.M * p.C * es, out + c * es, VEC * es, p.status)) x.v[v].store(out, c);
         }
     };
     if constexpr (!RING) {
         const long long m = static_cast<long long>(blockIdx.x) * p.G + group;
-        one_row(m, m < p.M, p.x, m * p.C);
+        one_row(m, m < p.M, static_cast<const char*>(p.x) + m * p.C * es);
     } else {
         const char* const src[1] = {static_cast<const char*>(p.x)};
         ln_chunks<1>(p.ring, src, nullptr, nullptr, p.M, static_cast<long long>(p.C) * es, ring, bars,
                      bars + kMaxStages, &abort_flag, p.status, [&](long long first, const uint8_t* st) {
                          st += slot_shift(first * p.C * es);
                          for (int r = group; r < p.ring.R; r += p.G)
-                             one_row(first + r, first + r < p.M, st, static_cast<long long>(r) * p.C);
+                             one_row(first + r, first + r < p.M, st + r * p.C * es);
                      });
     }
 }
@@ -503,12 +509,13 @@ __global__ void __launch_bounds__(MODE == 2 ? kLnMaxMulti : kLnBlock, ln_per_sm(
     __shared__ int abort_flag;
     extern __shared__ __align__(16) uint8_t dyn[];
     float* params = reinterpret_cast<float*>(dyn);
-    uint8_t* ring = dyn + ln_param_bytes(MODE, p.C, 1);   // at the end [2][C] column sums of a block of several rows
+    uint8_t* ring = dyn + ln_param_bytes(MODE, p.C, 1);   // at the end column sums [warps or groups][2][C]
     constexpr int es = elem_bytes<EK>();
     const int group = threadIdx.x / p.T;
     const int lane = threadIdx.x - group * p.T;
     int turn = 0;
-    const float fc = static_cast<float>(p.C);
+    const float inv_c = 1.0f / static_cast<float>(p.C);
+    const int mine = lane_vectors<VEC>(p.C, p.T, lane);
 
     using P = RowPart<EK, VEC, NV>;
     constexpr int kPer = P::kPer;
@@ -520,17 +527,16 @@ __global__ void __launch_bounds__(MODE == 2 ? kLnMaxMulti : kLnBlock, ln_per_sm(
     for (int u = 0; u < P::kUnits; ++u)
 #pragma unroll
         for (int i = 0; i < kPer; ++i) dg[u][i] = db[u][i] = make_float2(0.f, 0.f);
-    auto one_row = [&](long long m, bool live, const void* fx, const void* fd, long long at, float mean, float rstd) {
-        const long long row = m * p.C;
+    auto one_row = [&](long long m, bool live, const void* fx, const void* fd, float mean, float rstd) {
         P x, dy;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (lane + v * p.T) * VEC;
             x.v[v].zero();
             dy.v[v].zero();
-            if (live && c < p.C) {
-                x.v[v].load(fx, at + c);
-                dy.v[v].load(fd, at + c);
+            if (live && v < mine) {
+                x.v[v].load(fx, c);
+                dy.v[v].load(fd, c);
             }
         }
         const float2 minus = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
@@ -538,14 +544,14 @@ __global__ void __launch_bounds__(MODE == 2 ? kLnMaxMulti : kLnBlock, ln_per_sm(
 #pragma unroll
         for (int u = 0; u < P::kUnits; ++u) {
             // a dead row or column must add exactly nothing, whatever mean and rstd hold
-            if (!live || (VEC > 1 && (lane + u * p.T) * VEC >= p.C)) continue;
+            if (!live || (VEC > 1 && u >= mine)) continue;
             float2 n[kPer], d[kPer], g[kPer];
             x.unit(u, n);
             dy.unit(u, d);
             gamma.unit(u, p.C, p.T, lane, g);
 #pragma unroll
             for (int i = 0; i < kPer; ++i) n[i] = __fmul2_rn(__fadd2_rn(n[i], minus), r2);
-            mask_unit<VEC>(u, p.C, p.T, lane, n);
+            mask_unit<VEC>(u, mine, n);
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 const float2 q = __fmul2_rn(d[i], g[i]);
@@ -558,11 +564,11 @@ __global__ void __launch_bounds__(MODE == 2 ? kLnMaxMulti : kLnBlock, ln_per_sm(
         const float2 t = row_sum<MULTI, true>(sq.x + sq.y, sqn.x + sqn.y, p.T, group, red, turn);
         if (!live) return;
         // rstd (q - mq - n mqn) = q rstd + ((x - mean) (-rstd^2 mqn) - rstd mq)
-        const float a = -rstd * rstd * (t.y / fc), b = -rstd * (t.x / fc);
+        const float a = -rstd * rstd * (t.y * inv_c), b = -rstd * (t.x * inv_c);
         const float2 a2 = make_float2(a, a), b2 = make_float2(b, b);
 #pragma unroll
         for (int u = 0; u < P::kUnits; ++u) {
-            if (VEC > 1 && (lane + u * p.T) * VEC >= p.C) continue;
+            if (VEC > 1 && u >= mine) continue;
             float2 f[kPer], d[kPer], g[kPer];
             x.unit(u, f);
             dy.unit(u, d);
@@ -572,18 +578,18 @@ __global__ void __launch_bounds__(MODE == 2 ? kLnMaxMulti : kLnBlock, ln_per_sm(
                 f[i] = ffma2(__fmul2_rn(d[i], g[i]), r2, ffma2(__fadd2_rn(f[i], minus), a2, b2));
             x.set_unit(u, f);
         }
+        char* out = static_cast<char*>(p.dx) + m * p.C * es;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (lane + v * p.T) * VEC;
-            if (c < p.C &&
-                store_ok(p.dx, p.M * p.C * es, static_cast<char*>(p.dx) + (row + c) * es, VEC * es, p.status))
-                x.v[v].store(p.dx, row + c);
+            if (v < mine && store_ok(p.dx, p.M * p.C * es, out + c * es, VEC * es, p.status)) x.v[v].store(out, c);
         }
     };
     if constexpr (!RING) {
         const long long m = static_cast<long long>(blockIdx.x) * p.G + group;
         const bool live = m < p.M;
-        one_row(m, live, p.x, p.dy, m * p.C, live ? p.mean[m] : 0.f, live ? p.rstd[m] : 0.f);
+        one_row(m, live, static_cast<const char*>(p.x) + m * p.C * es, static_cast<const char*>(p.dy) + m * p.C * es,
+                live ? p.mean[m] : 0.f, live ? p.rstd[m] : 0.f);
     } else {
         const char* const src[2] = {static_cast<const char*>(p.x), static_cast<const char*>(p.dy)};
         ln_chunks<2>(p.ring, src, p.mean, p.rstd, p.M, static_cast<long long>(p.C) * es, ring, bars, bars + kMaxStages,
@@ -592,8 +598,8 @@ __global__ void __launch_bounds__(MODE == 2 ? kLnMaxMulti : kLnBlock, ln_per_sm(
                          const int shift = slot_shift(first * p.C * es);
                          for (int r = group; r < p.ring.R; r += p.G) {
                              const bool live = first + r < p.M;
-                             one_row(first + r, live, st + shift, st + p.ring.pitch + shift,
-                                     static_cast<long long>(r) * p.C, live ? sm[r] : 0.f,
+                             const uint8_t* at = st + shift + r * p.C * es;
+                             one_row(first + r, live, at, at + p.ring.pitch, live ? sm[r] : 0.f,
                                      live ? sm[p.ring.R + r] : 0.f);
                          }
                      });
@@ -633,20 +639,22 @@ __global__ void __launch_bounds__(MODE == 2 ? kLnMaxMulti : kLnBlock, ln_per_sm(
                     db[u][i].y += __shfl_xor_sync(0xFFFFFFFFu, db[u][i].y, o);
                 }
     }
+    // every warp's (or group's) sums side by side, then a thread per column in a fixed order
     float* cols = reinterpret_cast<float*>(ring);
-    const int mine = MULTI ? group : threadIdx.x >> 5;
-    const int rounds = MULTI ? p.G : kLnBlock / 32;
+    const int parts = MULTI ? p.G : kLnBlock / 32;
+    float* own = cols + (MULTI ? group : threadIdx.x >> 5) * 2 * p.C;
     __syncthreads();   // the ring has been read
-    for (int w = 0; w < rounds; ++w) {
-        if (mine == w && (MULTI || (threadIdx.x & 31) < p.T))
-            each([&](int c, float a, float b) {
-                cols[c] = w == 0 ? a : cols[c] + a;
-                cols[p.C + c] = w == 0 ? b : cols[p.C + c] + b;
-            });
-        __syncthreads();
+    if (MULTI || (threadIdx.x & 31) < p.T)
+        each([&](int c, float a, float b) {
+            own[c] = a;
+            own[p.C + c] = b;
+        });
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * p.C; c += blockDim.x) {
+        float a = cols[c];
+        for (int w = 1; w < parts; ++w) a += cols[w * 2 * p.C + c];
+        if (store_ok(p.part, part_bytes, out + c, 4, p.status)) out[c] = a;
     }
-    for (int c = threadIdx.x; c < 2 * p.C; c += blockDim.x)
-        if (store_ok(p.part, part_bytes, out + c, 4, p.status)) out[c] = cols[c];
 }
 
 // Long rows: the column sums first (dX may be dY or X), then dX row by row.
@@ -825,7 +833,7 @@ LnPlan ln_plan(int64_t M, int C, int ek, int tensors)
     // chunks of about 12 KB a tensor, stages for a third of an SM's shared memory (half where
     // threads hold column sums), two at least
     const int per_sm = ln_per_sm(ln_mode(p.T), p.nv * p.vec, tensors > 1);
-    int k = static_cast<int>(12288 / (row * p.G));
+    int k = static_cast<int>((tensors == 1 ? 16384 : 12288) / (row * p.G));
     if (k < 1) k = 1;
     p.ring.R = p.G * k;
     p.ring.pitch = static_cast<int>((p.ring.R * row + 32 + 15) / 16 * 16);
@@ -910,7 +918,7 @@ cudaError_t run_modes_bwd(const LnBwd& a, const LnPlan& p, size_t cols, cudaStre
 template <int EK, int VEC, int NV>
 cudaError_t run_bwd(const LnBwd& a, const LnPlan& p, cudaStream_t st)
 {
-    const size_t cols = p.G == 1 || !a.part ? 0 : static_cast<size_t>(a.C) * 8;
+    const size_t cols = p.G == 1 || !a.part ? 0 : static_cast<size_t>(a.C) * 8 * (p.T > 32 ? p.G : kLnBlock / 32);
     return run_modes_bwd<EK, VEC, NV, 0>(a, p, cols, st);
 }
 
