@@ -142,6 +142,11 @@ def _stream_ptr(stream, device=None):
     A given stream must belong to `device`."""
     import torch
     if stream is None:
+        index = None if device is None else device.index
+        # the raw handle, without the Stream object around it (2 us a call)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and index is not None:
+            return raw(index) or None
         stream = torch.cuda.current_stream(device)
     elif device is not None and stream.device != device:
         raise ValueError(f"stream is on {stream.device} but the tensors are on {device}")
@@ -450,36 +455,53 @@ def _like(t, shape, dtype, what):
 
 
 class _Allocator:
-    """Outputs and workspaces of one call, taken from the pool of the stream it runs on, so that
-    memory still in use on another stream is never handed out to it.  When that is not the
-    device's current stream, the tensors of the call are recorded on the stream they are used
+    """Outputs and workspaces of one call on a stream other than the device's current one: they
+    come from that stream's pool, so that memory still in use on another stream is never
+    handed out to it, and the tensors of the call are recorded on the stream they are used
     on besides their own: freeing one early does not pull it away."""
 
-    def __init__(self, device, stream):
-        import torch
-        self.device = device
-        self.stream = None
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device} but the tensors are on {device}")
-            current = torch.cuda.current_stream(device)
-            if stream != current:
-                self.stream, self.current = stream, current
+    def __init__(self, stream, current):
+        self.stream, self.current = stream, current
 
-    def empty(self, shape, dtype):
+    def empty(self, like, shape, dtype):
         import torch
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
         with torch.cuda.stream(self.stream):
-            t = torch.empty(shape, dtype=dtype, device=self.device)
+            t = like.new_empty(shape, dtype=dtype)
         t.record_stream(self.current)
         return t
 
     def uses(self, *ts):
-        if self.stream is not None:
-            for t in ts:
-                if t is not None:
-                    t.record_stream(self.stream)
+        for t in ts:
+            if t is not None:
+                t.record_stream(self.stream)
+
+
+def _allocator(device, stream):
+    """None where the call runs on the device's current stream."""
+    if stream is None:
+        return None
+    import torch
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device} but the tensors are on {device}")
+    current = torch.cuda.current_stream(device)
+    return None if stream == current else _Allocator(stream, current)
+
+
+def _empty(al, like, shape, dtype):
+    if al is not None:
+        return al.empty(like, shape, dtype)
+    return like.new_empty(shape, dtype=dtype)
+
+
+def _out(al, out, like, shape):
+    """The result tensor: `out` once checked, or a new one of `like`'s dtype."""
+    if out is not None:
+        _like(out, shape, like.dtype, "out")
+        return out
+    if al is None and shape == like.shape:
+        import torch
+        return torch.empty_like(like)
+    return _empty(al, like, shape, like.dtype)
 
 
 def _ptr(t):
@@ -502,14 +524,12 @@ def layernorm_forward(X, gamma=None, beta=None, eps=1e-5, stats=False, out=None,
     for t, what in ((gamma, "gamma"), (beta, "beta")):
         if t is not None:
             _like(t, (C,), X.dtype, what)
-    al = _Allocator(dev, stream)
-    if out is None:
-        out = al.empty(X.shape, X.dtype)
-    else:
-        _like(out, X.shape, X.dtype, "out")
-    mean = al.empty(X.shape[:-1], torch.float32) if stats else None
-    rstd = al.empty(X.shape[:-1], torch.float32) if stats else None
-    al.uses(X, *given)
+    al = _allocator(dev, stream)
+    out = _out(al, out, X, X.shape)
+    mean = _empty(al, X, X.shape[:-1], torch.float32) if stats else None
+    rstd = _empty(al, X, X.shape[:-1], torch.float32) if stats else None
+    if al is not None:
+        al.uses(X, *given)
     _call(dev, "dgrad_layernorm_forward", lib().dgrad_layernorm_forward, M, C, code, float(eps), X.data_ptr(),
           _ptr(gamma), _ptr(beta), out.data_ptr(), _ptr(mean), _ptr(rstd), stream=stream)
     return (out, mean, rstd) if stats else out
@@ -542,19 +562,17 @@ def layernorm_backward(dY, X, mean, rstd, gamma=None, param_grads=True, workspac
     dev = _device_of(dY, X, mean, rstd, *given)
     if gamma is not None:
         _like(gamma, (C,), X.dtype, "gamma")
-    al = _Allocator(dev, stream)
-    if out is None:
-        out = al.empty(X.shape, X.dtype)
-    else:
-        _like(out, X.shape, X.dtype, "out")
+    al = _allocator(dev, stream)
+    out = _out(al, out, X, X.shape)
     dgamma = dbeta = None
     ws_bytes = 0
     if param_grads:
-        dgamma, dbeta = al.empty((C,), X.dtype), al.empty((C,), X.dtype)
+        dgamma, dbeta = _empty(al, X, (C,), X.dtype), _empty(al, X, (C,), X.dtype)
         if workspace is None:
-            workspace = al.empty((max(layernorm_backward_workspace_bytes(M, C, X.dtype), 16),), torch.uint8)
+            workspace = _empty(al, X, (max(layernorm_backward_workspace_bytes(M, C, X.dtype), 16),), torch.uint8)
         ws_bytes = workspace.numel() * workspace.element_size()
-    al.uses(dY, X, mean, rstd, *given)
+    if al is not None:
+        al.uses(dY, X, mean, rstd, *given)
     _call(dev, "dgrad_layernorm_backward", lib().dgrad_layernorm_backward, M, C, code, dY.data_ptr(), X.data_ptr(),
           _ptr(gamma), mean.data_ptr(), rstd.data_ptr(), out.data_ptr(), _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
           ws_bytes, stream=stream)
@@ -588,14 +606,12 @@ def gated_forward(X, W, act="silu", preact=False, out=None, stream=None):
     given = [out] if out is not None else []
     _need_cuda(*given)
     dev = _device_of(X, W, *given)
-    al = _Allocator(dev, stream)
+    al = _allocator(dev, stream)
     shape = (*X.shape[:-1], F)
-    if out is None:
-        out = al.empty(shape, X.dtype)
-    else:
-        _like(out, shape, X.dtype, "out")
-    Z = al.empty((*X.shape[:-1], 2 * F), X.dtype) if preact else None
-    al.uses(X, W, *given)
+    out = _out(al, out, X, shape)
+    Z = _empty(al, X, (*X.shape[:-1], 2 * F), X.dtype) if preact else None
+    if al is not None:
+        al.uses(X, W, *given)
     _call(dev, "dgrad_gated_forward", lib().dgrad_gated_forward, M, C, F, code, acode, X.data_ptr(), W.data_ptr(),
           out.data_ptr(), _ptr(Z), stream=stream)
     return (out, Z) if preact else out
@@ -629,12 +645,13 @@ def gated_backward(dH, X, Z, W, act="silu", input_grad=True, weight_grad=True, w
     given = [workspace] if workspace is not None else []
     _need_cuda(*given)
     dev = _device_of(dH, X, Z, W, *given)
-    al = _Allocator(dev, stream)
-    dX = al.empty(X.shape, X.dtype) if input_grad else None
-    dW = al.empty(W.shape, W.dtype) if weight_grad else None
+    al = _allocator(dev, stream)
+    dX = _out(al, None, X, X.shape) if input_grad else None
+    dW = _out(al, None, W, W.shape) if weight_grad else None
     if workspace is None:
-        workspace = al.empty((max(gated_backward_workspace_bytes(M, C, F), 16),), torch.uint8)
-    al.uses(dH, X, Z, W, *given)
+        workspace = _empty(al, X, (max(gated_backward_workspace_bytes(M, C, F), 16),), torch.uint8)
+    if al is not None:
+        al.uses(dH, X, Z, W, *given)
     _call(dev, "dgrad_gated_backward", lib().dgrad_gated_backward, M, C, F, code, acode, dH.data_ptr(), X.data_ptr(),
           Z.data_ptr(), W.data_ptr(), _ptr(dX), _ptr(dW), workspace.data_ptr(),
           workspace.numel() * workspace.element_size(), stream=stream)
@@ -661,12 +678,10 @@ def dropout_forward(X, p, seed, offset=0, residual=None, out=None, stream=None):
     dev = _device_of(X, *given)
     if residual is not None:
         _like(residual, X.shape, X.dtype, "residual")
-    al = _Allocator(dev, stream)
-    if out is None:
-        out = al.empty(X.shape, X.dtype)
-    else:
-        _like(out, X.shape, X.dtype, "out")
-    al.uses(X, *given)
+    al = _allocator(dev, stream)
+    out = _out(al, out, X, X.shape)
+    if al is not None:
+        al.uses(X, *given)
     _call(dev, "dgrad_dropout_forward", lib().dgrad_dropout_forward, X.numel(), code, float(p),
           _counter(seed, "seed"), _counter(offset, "offset"), X.data_ptr(), _ptr(residual), out.data_ptr(),
           stream=stream)
@@ -681,12 +696,10 @@ def dropout_backward(dY, p, seed, offset=0, out=None, stream=None):
     given = [out] if out is not None else []
     _need_cuda(*given)
     dev = _device_of(dY, *given)
-    al = _Allocator(dev, stream)
-    if out is None:
-        out = al.empty(dY.shape, dY.dtype)
-    else:
-        _like(out, dY.shape, dY.dtype, "out")
-    al.uses(dY, *given)
+    al = _allocator(dev, stream)
+    out = _out(al, out, dY, dY.shape)
+    if al is not None:
+        al.uses(dY, *given)
     _call(dev, "dgrad_dropout_backward", lib().dgrad_dropout_backward, dY.numel(), code, float(p),
           _counter(seed, "seed"), _counter(offset, "offset"), dY.data_ptr(), out.data_ptr(), stream=stream)
     return out
