@@ -1,16 +1,25 @@
-// gate_act.cuh -- the gate's activations and their derivatives, in fp32.
+// gate_act.cuh -- the gate's activations and their derivatives, in fp32, two elements at a
+// time (packed FP32 instructions; the exponential and reciprocal units take one).
 //
-// With s(v) = 1/(1 + exp(-v)):
+// With s(v) = 1/(1 + exp(-v)) and P the normal distribution:
 //   silu       g s(g)                       s (1 + g (1 - s))
-//   gelu       g P(g), P(g) = erfc(-g/sqrt 2)/2     P + g exp(-g^2/2)/sqrt(2 pi)
+//   gelu       g P(g)                       P + g exp(-g^2/2)/sqrt(2 pi)
 //   gelu_tanh  g s(2v), v = sqrt(2/pi)(g + 0.044715 g^3)   (the same as g(1 + tanh v)/2)
 //                                           s + 2 g s (1 - s) dv/dg
 //   relu       max(g, 0)                    g > 0
 //   sigmoid    s(g)                         s (1 - s)
 // The forms keep their relative precision for large negative g, where 1 + tanh and
-// 1 + erf cancel.  exp and the quotient are the fast device functions: relative
-// errors of a few 2^-23 (times |v| for the exponential), far below a 16-bit result's.
+// 1 + erf cancel.  P's tail is t 2^(p(t) - g^2/(2 ln 2)), t = 1/(1 + 0.29|g|), with p a
+// polynomial of degree 8 fitted to log2(erfcx(|g|/sqrt 2)/(2t)) by weighted least squares
+// on Chebyshev nodes (relative error 1.5e-7; 8e-7 with fp32 rounding for |g| < 4).
+// ex2 and rcp are the hardware's approximations (about 2^-22), far below a 16-bit
+// result's half step.  An epilogue of 64 elements a thread spent more time in the
+// general-purpose exp, division and erfc than the tensor cores in the tile: 32768 rows,
+// 768 to 2048 channels, bf16 silu took 149 us with those and 126 us with these forms,
+// gelu 203 and 133 us.
 #pragma once
+
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -18,44 +27,111 @@ namespace dgrad {
 
 enum GateAct : int { kSilu = 0, kGelu = 1, kGeluTanh = 2, kRelu = 3, kSigmoid = 4 };
 
-__device__ __forceinline__ float logistic(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 
+__device__ __forceinline__ float2 ex2_pair(float2 v)
+{
+    float2 r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(v.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(v.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 rcp_pair(float2 v)
+{
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(v.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(v.y));
+    return r;
+}
+
+// 1/(1 + 2^w): s(v) for w = -v log2(e).
+__device__ __forceinline__ float2 logistic2(float2 w) { return rcp_pair(__fadd2_rn(ex2_pair(w), splat(1.0f))); }
+
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTanhA = 0.7978845608028654f;             // sqrt(2/pi)
 constexpr float kTanhB = 0.7978845608028654f * 0.044715f;
 
-__device__ __forceinline__ float gate_act(int act, float g)
+// P(g), and e = 2^(-g^2/(2 ln 2)) = exp(-g^2/2) when E.
+template <bool E>
+__device__ __forceinline__ float2 normal_cdf(float2 g, float2* e)
 {
-    switch (act) {
-    case kSilu: return g * logistic(g);
-    case kGelu: return g * (0.5f * erfcf(g * -0.7071067811865476f));
-    case kGeluTanh: return g * logistic(2.0f * g * fmaf(kTanhB * g, g, kTanhA));
-    case kRelu: return g <= 0.f ? 0.f : g;
-    default: return logistic(g);
+    const float2 a = make_float2(fabsf(g.x), fabsf(g.y));
+    const float2 t = rcp_pair(ffma2(a, splat(0.29f), splat(1.0f)));
+    float2 p = splat(-0.27778888f);
+    p = ffma2(p, t, splat(1.1824034f));
+    p = ffma2(p, t, splat(-1.7660975f));
+    p = ffma2(p, t, splat(1.0227866f));
+    p = ffma2(p, t, splat(-0.42359963f));
+    p = ffma2(p, t, splat(0.34500575f));
+    p = ffma2(p, t, splat(0.58516502f));
+    p = ffma2(p, t, splat(1.4437800f));
+    p = ffma2(p, t, splat(-3.1116550f));
+    const float2 h = __fmul2_rn(g, splat(-0.5f * kLog2e));
+    const float2 q = __fmul2_rn(t, ex2_pair(ffma2(h, g, p)));
+    if constexpr (E) *e = ex2_pair(__fmul2_rn(h, g));
+    return make_float2(g.x > 0.f ? 1.0f - q.x : q.x, g.y > 0.f ? 1.0f - q.y : q.y);
+}
+
+template <int ACT>
+__device__ __forceinline__ float2 gate_act(float2 g)
+{
+    if constexpr (ACT == kSilu) {
+        return __fmul2_rn(g, logistic2(__fmul2_rn(g, splat(-kLog2e))));
+    } else if constexpr (ACT == kGelu) {
+        return __fmul2_rn(g, normal_cdf<false>(g, nullptr));
+    } else if constexpr (ACT == kGeluTanh) {
+        const float2 c = ffma2(__fmul2_rn(g, splat(-2.0f * kLog2e * kTanhB)), g, splat(-2.0f * kLog2e * kTanhA));
+        return __fmul2_rn(g, logistic2(__fmul2_rn(g, c)));
+    } else if constexpr (ACT == kRelu) {
+        return make_float2(g.x <= 0.f ? 0.f : g.x, g.y <= 0.f ? 0.f : g.y);   // NaN stays
+    } else {
+        return logistic2(__fmul2_rn(g, splat(-kLog2e)));
     }
 }
 
-// act(g) and act'(g).
-__device__ __forceinline__ float2 gate_act_grad(int act, float g)
+// a = act(g), d = act'(g).
+template <int ACT>
+__device__ __forceinline__ void gate_act_grad(float2 g, float2& a, float2& d)
+{
+    if constexpr (ACT == kSilu) {
+        const float2 s = logistic2(__fmul2_rn(g, splat(-kLog2e)));
+        a = __fmul2_rn(g, s);
+        const float2 rest = ffma2(s, splat(-1.0f), splat(1.0f));
+        d = __fmul2_rn(s, ffma2(g, rest, splat(1.0f)));
+    } else if constexpr (ACT == kGelu) {
+        float2 e;
+        const float2 p = normal_cdf<true>(g, &e);
+        a = __fmul2_rn(g, p);
+        d = ffma2(__fmul2_rn(g, splat(0.3989422804014327f)), e, p);
+    } else if constexpr (ACT == kGeluTanh) {
+        const float2 g2 = __fmul2_rn(g, g);
+        const float2 s = logistic2(__fmul2_rn(g, ffma2(g2, splat(-2.0f * kLog2e * kTanhB), splat(-2.0f * kLog2e * kTanhA))));
+        float2 dv = ffma2(g2, splat(3.0f * kTanhB), splat(kTanhA));
+        dv = make_float2(fminf(dv.x, 1e30f), fminf(dv.y, 1e30f));   // finite: s (1 - s) is 0 there
+        a = __fmul2_rn(g, s);
+        const float2 rest = ffma2(s, splat(-1.0f), splat(1.0f));
+        d = ffma2(__fmul2_rn(__fmul2_rn(splat(2.0f), a), rest), dv, s);
+    } else if constexpr (ACT == kRelu) {
+        a = gate_act<kRelu>(g);
+        d = make_float2(g.x > 0.f ? 1.0f : 0.f, g.y > 0.f ? 1.0f : 0.f);
+    } else {
+        a = logistic2(__fmul2_rn(g, splat(-kLog2e)));
+        d = __fmul2_rn(a, ffma2(a, splat(-1.0f), splat(1.0f)));
+    }
+}
+
+// Calls f with the activation as a compile-time constant: the branch lies outside the
+// element loops, so that the elements' long-latency instructions overlap.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f)
 {
     switch (act) {
-    case kSilu: {
-        const float s = logistic(g);
-        return make_float2(g * s, s * fmaf(g, 1.0f - s, 1.0f));
-    }
-    case kGelu: {
-        const float p = 0.5f * erfcf(g * -0.7071067811865476f);
-        return make_float2(g * p, fmaf(g * 0.3989422804014327f, __expf(-0.5f * g * g), p));
-    }
-    case kGeluTanh: {
-        const float s = logistic(2.0f * g * fmaf(kTanhB * g, g, kTanhA));
-        const float dv = fminf(fmaf(3.0f * kTanhB * g, g, kTanhA), 1e30f);   // finite: s (1 - s) is 0 there
-        return make_float2(g * s, fmaf(2.0f * g * s * (1.0f - s), dv, s));
-    }
-    case kRelu: return make_float2(g <= 0.f ? 0.f : g, g > 0.f ? 1.0f : 0.f);
-    default: {
-        const float s = logistic(g);
-        return make_float2(s, s * (1.0f - s));
-    }
+    case kSilu: f(std::integral_constant<int, kSilu>{}); break;
+    case kGelu: f(std::integral_constant<int, kGelu>{}); break;
+    case kGeluTanh: f(std::integral_constant<int, kGeluTanh>{}); break;
+    case kRelu: f(std::integral_constant<int, kRelu>{}); break;
+    default: f(std::integral_constant<int, kSigmoid>{}); break;
     }
 }
 

@@ -48,14 +48,19 @@ __global__ void __launch_bounds__(256) gated_dz_kernel(const uint16_t* dH, const
         const uint4 u = reinterpret_cast<const uint4*>(Z)[g_at + nv];
         const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
         uint32_t a[4], b[4];
+        with_act(act, [&](auto which) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 hf = h16x2_to_float2<EK>(hw[j]), gf = h16x2_to_float2<EK>(gw[j]);
-            const float2 uf = h16x2_to_float2<EK>(uw[j]);
-            const float2 lo = gate_act_grad(act, gf.x), hi = gate_act_grad(act, gf.y);
-            a[j] = float2_to_h16x2<EK>(hf.x * uf.x * lo.y, hf.y * uf.y * hi.y);
-            b[j] = float2_to_h16x2<EK>(hf.x * lo.x, hf.y * hi.x);
-        }
+            for (int j = 0; j < 4; ++j) {
+                constexpr int A = decltype(which)::value;
+                const float2 hf = h16x2_to_float2<EK>(hw[j]), gf = h16x2_to_float2<EK>(gw[j]);
+                const float2 uf = h16x2_to_float2<EK>(uw[j]);
+                float2 av, dv;
+                gate_act_grad<A>(gf, av, dv);
+                const float2 dg = __fmul2_rn(__fmul2_rn(hf, uf), dv), du = __fmul2_rn(hf, av);
+                a[j] = float2_to_h16x2<EK>(dg.x, dg.y);
+                b[j] = float2_to_h16x2<EK>(du.x, du.y);
+            }
+        });
         uint4* out = reinterpret_cast<uint4*>(dZ) + g_at;
         if (store_ok(dZ, bytes, out, 16, status)) out[0] = make_uint4(a[0], a[1], a[2], a[3]);
         if (store_ok(dZ, bytes, out + nv, 16, status)) out[nv] = make_uint4(b[0], b[1], b[2], b[3]);

@@ -50,8 +50,7 @@ struct GatedLayout {
 template <int HN, bool ZK, bool F16>
 __global__ void __launch_bounds__(GatedLayout<HN, ZK>::kThreads, 1)
     gated_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                      const __grid_constant__ CUtensorMap map_h, const __grid_constant__ CUtensorMap map_z, int M,
-                      int C, int F, int act, int* status)
+                      const __grid_constant__ CUtensorMap map_h, uint16_t* Z, int M, int C, int F, int act, int* status)
 {
     pdl_wait();      // the previous kernel on the stream has finished
     pdl_trigger();   // the next one may start its set-up
@@ -96,7 +95,6 @@ __global__ void __launch_bounds__(GatedLayout<HN, ZK>::kThreads, 1)
         tma_prefetch_desc(&map_x);
         tma_prefetch_desc(&map_w);
         tma_prefetch_desc(&map_h);
-        if (ZK) tma_prefetch_desc(&map_z);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, L::kCols);
@@ -110,6 +108,7 @@ __global__ void __launch_bounds__(GatedLayout<HN, ZK>::kThreads, 1)
     if (warp == 0) {
         if (lane == 0) {
             const uint32_t full0 = leader_addr(&full[0]);
+            const uint64_t keep = policy_evict_last();   // both operands are read again by other tiles
             int stage = 0;
             uint32_t phase = 0;
             long long issued = 0;
@@ -125,8 +124,8 @@ __global__ void __launch_bounds__(GatedLayout<HN, ZK>::kThreads, 1)
                     if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * L::kStage);
                     uint8_t* a_tile = smem + stage * L::kStage;
                     const uint32_t fb = full0 + static_cast<uint32_t>(stage * 8);
-                    tma_load_2d_pair(a_tile, &map_x, fb, kb * kBK, m0);
-                    tma_load_2d_pair(a_tile + 16384, &map_w, fb, kb * kBK, w0);
+                    tma_load_2d_pair_hint(a_tile, &map_x, fb, kb * kBK, m0, keep);
+                    tma_load_2d_pair_hint(a_tile + 16384, &map_w, fb, kb * kBK, w0, keep);
                     ++issued;
                     if (++stage == S) {
                         stage = 0;
@@ -224,39 +223,52 @@ __global__ void __launch_bounds__(GatedLayout<HN, ZK>::kThreads, 1)
                     tc_fence_before();
                     mbar_arrive_cluster(tempty0 + static_cast<uint32_t>(acc * 8));
                 }
+                with_act(act, [&](auto which) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int at = row * 128 + (((half * 4 + j) ^ (row & 7)) << 4);
-                    uint32_t h[4];
+                    for (int j = 0; j < 4; ++j) {
+                        const int at = row * 128 + (((half * 4 + j) ^ (row & 7)) << 4);
+                        uint32_t h[4], gz[4], uz[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int e = 8 * j + 2 * i;
-                        const float g0 = __uint_as_float(g[e]), g1 = __uint_as_float(g[e + 1]);
-                        const float u0 = __uint_as_float(u[e]), u1 = __uint_as_float(u[e + 1]);
-                        h[i] = float2_to_h16x2<EK>(gate_act(act, g0) * u0, gate_act(act, g1) * u1);
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = 8 * j + 2 * i;
+                            const float g0 = __uint_as_float(g[e]), g1 = __uint_as_float(g[e + 1]);
+                            const float u0 = __uint_as_float(u[e]), u1 = __uint_as_float(u[e + 1]);
+                            constexpr int A = decltype(which)::value;
+                            const float2 v = __fmul2_rn(gate_act<A>(make_float2(g0, g1)), make_float2(u0, u1));
+                            h[i] = float2_to_h16x2<EK>(v.x, v.y);
+                            gz[i] = float2_to_h16x2<EK>(g0, g1);
+                            uz[i] = float2_to_h16x2<EK>(u0, u1);
+                        }
+                        *reinterpret_cast<uint4*>(stg + at) = make_uint4(h[0], h[1], h[2], h[3]);
                         if constexpr (ZK) {
-                            g[4 * j + i] = float2_to_h16x2<EK>(g0, g1);
-                            u[4 * j + i] = float2_to_h16x2<EK>(u0, u1);
+                            *reinterpret_cast<uint4*>(stg + 16384 + at) = make_uint4(gz[0], gz[1], gz[2], gz[3]);
+                            *reinterpret_cast<uint4*>(stg + 32768 + at) = make_uint4(uz[0], uz[1], uz[2], uz[3]);
                         }
                     }
-                    *reinterpret_cast<uint4*>(stg + at) = make_uint4(h[0], h[1], h[2], h[3]);
-                    if constexpr (ZK) {
-                        *reinterpret_cast<uint4*>(stg + 16384 + at) =
-                            make_uint4(g[4 * j], g[4 * j + 1], g[4 * j + 2], g[4 * j + 3]);
-                        *reinterpret_cast<uint4*>(stg + 32768 + at) =
-                            make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
-                    }
-                }
+                });
             }
             fence_proxy_async_smem();
             named_barrier_sync(1 + group, 128);
             if (issuer && n0 < F && m0 < M) {        // the maps clip the tails
                 tma_store_2d(&map_h, stg, n0, m0);
-                if constexpr (ZK) {
-                    tma_store_3d(&map_z, stg + 16384, n0, 0, m0);
-                    tma_store_3d(&map_z, stg + 32768, n0, 1, m0);
-                }
                 bulk_commit_group();
+            }
+            if constexpr (ZK) {
+                // Z by plain stores, a quarter warp per 128-byte row
+                const int chunk = lane & 7;
+                const int col = n0 + chunk * 8;
+#pragma unroll 2
+                for (int i = 0; i < 8; ++i) {
+                    const int r = quarter * 32 + i * 4 + (lane >> 3);
+                    const int at = r * 128 + ((chunk ^ (r & 7)) << 4);
+                    const uint4 zg = *reinterpret_cast<const uint4*>(stg + 16384 + at);
+                    const uint4 zu = *reinterpret_cast<const uint4*>(stg + 32768 + at);
+                    if (m0 + r < M && col < F) {
+                        uint16_t* z = Z + static_cast<long long>(m0 + r) * 2 * F + col;
+                        if (store_ok(Z, 4LL * M * F, z, 16, status)) __stcs(reinterpret_cast<uint4*>(z), zg);
+                        if (store_ok(Z, 4LL * M * F, z + F, 16, status)) __stcs(reinterpret_cast<uint4*>(z + F), zu);
+                    }
+                }
             }
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
@@ -321,10 +333,14 @@ __global__ void __launch_bounds__(256) gated_rows_kernel(const void* X, const vo
             g[r] += __shfl_xor_sync(0xFFFFFFFFu, g[r], o);
             u[r] += __shfl_xor_sync(0xFFFFFFFFu, u[r], o);
         }
-        if (lane == r && r < M) {
+    }
+    with_act(act, [&](auto which) {
+#pragma unroll
+        for (int r = 0; r < MR; ++r) {
+            if (lane != r || r >= M) continue;
             const long long at = static_cast<long long>(r) * F + f;
-            if (store_ok(H, 2LL * M * F, H + at, 2, status))
-                H[at] = static_cast<uint16_t>(float2_to_h16x2<EK>(gate_act(act, g[r]) * u[r], 0.f));
+            const float h = gate_act<decltype(which)::value>(splat(g[r])).x * u[r];
+            if (store_ok(H, 2LL * M * F, H + at, 2, status)) H[at] = static_cast<uint16_t>(float2_to_h16x2<EK>(h, 0.f));
             if (Z) {
                 uint16_t* z = Z + 2LL * r * F + f;
                 if (store_ok(Z, 4LL * M * F, z, 2, status)) z[0] = static_cast<uint16_t>(float2_to_h16x2<EK>(g[r], 0.f));
@@ -332,7 +348,7 @@ __global__ void __launch_bounds__(256) gated_rows_kernel(const void* X, const vo
                     z[F] = static_cast<uint16_t>(float2_to_h16x2<EK>(u[r], 0.f));
             }
         }
-    }
+    });
 }
 
 template <int HN, bool ZK, bool F16>
@@ -342,26 +358,20 @@ cudaError_t run_pair(const GatedArgs& a, cudaStream_t stream)
     static_assert(L::kAlloc <= 232448, "shared memory budget");
     const CUtensorMapDataType t = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const uint64_t M = static_cast<uint64_t>(a.M), C = static_cast<uint64_t>(a.C), F = static_cast<uint64_t>(a.F);
-    CUtensorMap mx, mw, mh, mz;
+    CUtensorMap mx, mw, mh;
     const uint64_t dx[2] = {C, M}, sx[1] = {2 * C}, dw[2] = {C, 2 * F}, dh[2] = {F, M}, sh[1] = {2 * F};
-    const uint64_t dz[3] = {F, 2, M}, sz[2] = {2 * F, 4 * F};
-    const uint32_t bx[2] = {64, 128}, bw[2] = {64, HN}, bz[3] = {64, 1, 128};
+    const uint32_t bx[2] = {64, 128}, bw[2] = {64, HN};
     if (!encode_map(&mx, t, 2, a.X, dx, sx, bx, true) || !encode_map(&mw, t, 2, a.W, dw, sx, bw, true) ||
         !encode_map(&mh, t, 2, a.H, dh, sh, bx, true))
         return cudaErrorInvalidValue;
-    if (ZK) {
-        if (!encode_map(&mz, t, 3, a.Z, dz, sz, bz, true)) return cudaErrorInvalidValue;
-    } else {
-        mz = mh;   // not used
-    }
     auto kern = gated_pair_kernel<HN, ZK, F16>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), L::kAlloc);
     if (e != cudaSuccess) return e;
     const int64_t tiles = ((a.M + 255) / 256) * ((a.F + HN - 1) / HN);
     const int64_t most = device_sm_count() / 2;
     const unsigned pairs = static_cast<unsigned>(tiles < most ? tiles : most);
-    return launch_kernel(kern, dim3(2 * pairs), dim3(L::kThreads), L::kAlloc, stream, 2, mx, mw, mh, mz,
-                         static_cast<int>(a.M), static_cast<int>(a.C), static_cast<int>(a.F), a.act, a.status);
+    return launch_kernel(kern, dim3(2 * pairs), dim3(L::kThreads), L::kAlloc, stream, 2, mx, mw, mh,
+                         static_cast<uint16_t*>(a.Z), static_cast<int>(a.M), static_cast<int>(a.C), static_cast<int>(a.F), a.act, a.status);
 }
 
 template <int MR, bool F16>
