@@ -50,7 +50,8 @@ struct GatedLayout {
 template <int HN, bool ZK, bool F16>
 __global__ void __launch_bounds__(GatedLayout<HN, ZK>::kThreads, 1)
     gated_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                      const __grid_constant__ CUtensorMap map_h, uint16_t* Z, int M, int C, int F, int act, int* status)
+                      const __grid_constant__ CUtensorMap map_h, const __grid_constant__ CUtensorMap map_z, int M,
+                      int C, int F, int act, int* status)
 {
     pdl_wait();      // the previous kernel on the stream has finished
     pdl_trigger();   // the next one may start its set-up
@@ -95,6 +96,7 @@ __global__ void __launch_bounds__(GatedLayout<HN, ZK>::kThreads, 1)
         tma_prefetch_desc(&map_x);
         tma_prefetch_desc(&map_w);
         tma_prefetch_desc(&map_h);
+        if (ZK) tma_prefetch_desc(&map_z);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, L::kCols);
@@ -200,6 +202,7 @@ __global__ void __launch_bounds__(GatedLayout<HN, ZK>::kThreads, 1)
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
         const bool issuer = ((warp - 2) & 3) == 0 && lane == 0;
         const uint32_t tempty0 = leader_addr(&tempty[0]);
+        const uint64_t once = policy_evict_first();                // Z is next read in the backward pass
         uint8_t* stg = smem + L::kEpi + group * L::kStgPerGroup;   // H, then Z's gate and other half
         int acc = 0;
         uint32_t acc_phase = 0;
@@ -212,63 +215,58 @@ __global__ void __launch_bounds__(GatedLayout<HN, ZK>::kThreads, 1)
             ok = named_barrier_and(1 + group, 128, ok);   // the group leaves together or not at all
             if (!ok) break;
             tc_fence_after();
+            // 16 columns at a time, the next ones on their way from tensor memory meanwhile
+            const uint32_t col = tmem_base + lane_addr + static_cast<uint32_t>(acc * 2 * HN + group * 64);
+            uint32_t g[2][16], u[2][16];
+            tmem_ld_32x32b_x16(col, g[0]);
+            tmem_ld_32x32b_x16(col + HN, u[0]);
+            with_act(act, [&](auto which) {
+                constexpr int A = decltype(which)::value;
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                uint32_t g[32], u[32];
-                const uint32_t col = tmem_base + lane_addr + static_cast<uint32_t>(acc * 2 * HN + group * 64 + half * 32);
-                tmem_ld_32x32b_x32(col, g);
-                tmem_ld_32x32b_x32(col + HN, u);
-                tmem_wait_ld();
-                if (half == 1) {                     // the accumulator is in registers: free it
-                    tc_fence_before();
-                    mbar_arrive_cluster(tempty0 + static_cast<uint32_t>(acc * 8));
-                }
-                with_act(act, [&](auto which) {
+                for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int at = row * 128 + (((half * 4 + j) ^ (row & 7)) << 4);
-                        uint32_t h[4], gz[4], uz[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int e = 8 * j + 2 * i;
-                            const float g0 = __uint_as_float(g[e]), g1 = __uint_as_float(g[e + 1]);
-                            const float u0 = __uint_as_float(u[e]), u1 = __uint_as_float(u[e + 1]);
-                            constexpr int A = decltype(which)::value;
-                            const float2 v = __fmul2_rn(gate_act<A>(make_float2(g0, g1)), make_float2(u0, u1));
-                            h[i] = float2_to_h16x2<EK>(v.x, v.y);
-                            gz[i] = float2_to_h16x2<EK>(g0, g1);
-                            uz[i] = float2_to_h16x2<EK>(u0, u1);
+                    for (int q = 0; q < 2; ++q) {
+                        tmem_wait_ld();
+                        if (half == 0 || q == 0) {
+                            const uint32_t next = col + static_cast<uint32_t>(half * 32 + q * 16 + 16);
+                            tmem_ld_32x32b_x16(next, g[q ^ 1]);
+                            tmem_ld_32x32b_x16(next + HN, u[q ^ 1]);
+                        } else {                 // the accumulator is in registers: free it
+                            tc_fence_before();
+                            mbar_arrive_cluster(tempty0 + static_cast<uint32_t>(acc * 8));
                         }
-                        *reinterpret_cast<uint4*>(stg + at) = make_uint4(h[0], h[1], h[2], h[3]);
-                        if constexpr (ZK) {
-                            *reinterpret_cast<uint4*>(stg + 16384 + at) = make_uint4(gz[0], gz[1], gz[2], gz[3]);
-                            *reinterpret_cast<uint4*>(stg + 32768 + at) = make_uint4(uz[0], uz[1], uz[2], uz[3]);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int at = row * 128 + (((half * 4 + q * 2 + j) ^ (row & 7)) << 4);
+                            uint32_t h[4], gz[4], uz[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int e = 8 * j + 2 * i;
+                                const float2 gf = make_float2(__uint_as_float(g[q][e]), __uint_as_float(g[q][e + 1]));
+                                const float2 uf = make_float2(__uint_as_float(u[q][e]), __uint_as_float(u[q][e + 1]));
+                                const float2 hf = __fmul2_rn(gate_act<A>(gf), uf);
+                                h[i] = float2_to_h16x2<EK>(hf.x, hf.y);
+                                gz[i] = float2_to_h16x2<EK>(gf.x, gf.y);
+                                uz[i] = float2_to_h16x2<EK>(uf.x, uf.y);
+                            }
+                            *reinterpret_cast<uint4*>(stg + at) = make_uint4(h[0], h[1], h[2], h[3]);
+                            if constexpr (ZK) {
+                                *reinterpret_cast<uint4*>(stg + 16384 + at) = make_uint4(gz[0], gz[1], gz[2], gz[3]);
+                                *reinterpret_cast<uint4*>(stg + 32768 + at) = make_uint4(uz[0], uz[1], uz[2], uz[3]);
+                            }
                         }
                     }
-                });
-            }
+                }
+            });
             fence_proxy_async_smem();
             named_barrier_sync(1 + group, 128);
             if (issuer && n0 < F && m0 < M) {        // the maps clip the tails
                 tma_store_2d(&map_h, stg, n0, m0);
-                bulk_commit_group();
-            }
-            if constexpr (ZK) {
-                // Z by plain stores, a quarter warp per 128-byte row
-                const int chunk = lane & 7;
-                const int col = n0 + chunk * 8;
-#pragma unroll 2
-                for (int i = 0; i < 8; ++i) {
-                    const int r = quarter * 32 + i * 4 + (lane >> 3);
-                    const int at = r * 128 + ((chunk ^ (r & 7)) << 4);
-                    const uint4 zg = *reinterpret_cast<const uint4*>(stg + 16384 + at);
-                    const uint4 zu = *reinterpret_cast<const uint4*>(stg + 32768 + at);
-                    if (m0 + r < M && col < F) {
-                        uint16_t* z = Z + static_cast<long long>(m0 + r) * 2 * F + col;
-                        if (store_ok(Z, 4LL * M * F, z, 16, status)) __stcs(reinterpret_cast<uint4*>(z), zg);
-                        if (store_ok(Z, 4LL * M * F, z + F, 16, status)) __stcs(reinterpret_cast<uint4*>(z + F), zu);
-                    }
+                if constexpr (ZK) {
+                    tma_store_3d_hint(&map_z, stg + 16384, n0, 0, m0, once);
+                    tma_store_3d_hint(&map_z, stg + 32768, n0, 1, m0, once);
                 }
+                bulk_commit_group();
             }
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
@@ -358,11 +356,16 @@ cudaError_t run_pair(const GatedArgs& a, cudaStream_t stream)
     static_assert(L::kAlloc <= 232448, "shared memory budget");
     const CUtensorMapDataType t = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const uint64_t M = static_cast<uint64_t>(a.M), C = static_cast<uint64_t>(a.C), F = static_cast<uint64_t>(a.F);
-    CUtensorMap mx, mw, mh;
+    CUtensorMap mx, mw, mh, mz;
+    const uint64_t dz[3] = {F, 2, M}, sz[2] = {2 * F, 4 * F};
     const uint64_t dx[2] = {C, M}, sx[1] = {2 * C}, dw[2] = {C, 2 * F}, dh[2] = {F, M}, sh[1] = {2 * F};
-    const uint32_t bx[2] = {64, 128}, bw[2] = {64, HN};
+    const uint32_t bx[2] = {64, 128}, bw[2] = {64, HN}, bz[3] = {64, 1, 128};
     if (!encode_map(&mx, t, 2, a.X, dx, sx, bx, true) || !encode_map(&mw, t, 2, a.W, dw, sx, bw, true) ||
         !encode_map(&mh, t, 2, a.H, dh, sh, bx, true))
+        return cudaErrorInvalidValue;
+    if (!ZK)
+        mz = mh;   // not used
+    else if (!encode_map(&mz, t, 3, a.Z, dz, sz, bz, true))
         return cudaErrorInvalidValue;
     auto kern = gated_pair_kernel<HN, ZK, F16>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), L::kAlloc);
@@ -370,8 +373,8 @@ cudaError_t run_pair(const GatedArgs& a, cudaStream_t stream)
     const int64_t tiles = ((a.M + 255) / 256) * ((a.F + HN - 1) / HN);
     const int64_t most = device_sm_count() / 2;
     const unsigned pairs = static_cast<unsigned>(tiles < most ? tiles : most);
-    return launch_kernel(kern, dim3(2 * pairs), dim3(L::kThreads), L::kAlloc, stream, 2, mx, mw, mh,
-                         static_cast<uint16_t*>(a.Z), static_cast<int>(a.M), static_cast<int>(a.C), static_cast<int>(a.F), a.act, a.status);
+    return launch_kernel(kern, dim3(2 * pairs), dim3(L::kThreads), L::kAlloc, stream, 2, mx, mw, mh, mz,
+                         static_cast<int>(a.M), static_cast<int>(a.C), static_cast<int>(a.F), a.act, a.status);
 }
 
 template <int MR, bool F16>
