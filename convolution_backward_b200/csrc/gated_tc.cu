@@ -13,9 +13,9 @@
 // and the epilogue's thread has both of its elements in its own TMEM lane.
 //   warp 0      TMA producer (X 128 rows x 64, W HN rows x 64 per k-block, both K-major)
 //   warp 1      TMEM allocation; the rank-0 CTA's lane 0 issues the pair MMAs
-//   warps 2..   groups of four epilogue warps, 64 columns of H each: TMEM loads, the
-//               activation in fp32, one rounding, a swizzled staging tile, one TMA store
-//               (H, and Z's two halves when the pre-activations are kept).
+//   warps 2..   eight epilogue warps for every 64 columns of H: TMEM loads 16 columns
+//               ahead, the activation in fp32, one rounding, a swizzled staging tile, one
+//               TMA store (H, and Z's two halves when the pre-activations are kept).
 // Two accumulators let a tile's epilogue run under the next tile's MMAs.
 //
 // gated_rows_kernel serves a handful of rows (single tokens): W is read once by plain
@@ -30,17 +30,18 @@ namespace {
 
 constexpr int kBK = 64;
 
-// HN = 128: two epilogue groups; HN = 64: one.  ZK: Z is kept.
+// Sixteen epilogue warps (HN = 128) rather than eight: at 256 channels, where the epilogue
+// bounds the tile, 32768 rows to 2048 took 80 us against 85.  ZK: Z is kept.
 template <int HN, bool ZK>
 struct GatedLayout {
-    static constexpr int kGroups = HN / 64;
-    static constexpr int kThreads = 64 + 128 * kGroups;
+    static constexpr int kBoxes = HN / 64;   // staging boxes of 64 columns, two warp groups each
+    static constexpr int kThreads = 64 + 256 * kBoxes;
     static constexpr int kBBytes = HN * kBK * 2;
     static constexpr int kStage = 16384 + kBBytes;
-    static constexpr int kStgPerGroup = (ZK ? 3 : 1) * 16384;
-    static constexpr int kStages = HN == 128 ? (ZK ? 4 : 6) : (ZK ? 7 : 8);
+    static constexpr int kStgPerBox = (ZK ? 3 : 2) * 16384;
+    static constexpr int kStages = HN == 128 ? (ZK ? 4 : 5) : (ZK ? 7 : 8);
     static constexpr int kEpi = kStages * kStage;
-    static constexpr int kBars = kEpi + kGroups * kStgPerGroup;
+    static constexpr int kBars = kEpi + kBoxes * kStgPerBox;
     static constexpr int kNumBars = 2 * kStages + 5;
     static constexpr int kBytes = kBars + kNumBars * 8 + 16;
     static constexpr int kAlloc = kBytes + 1024;   // slack to align the tiles to 1024 bytes
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(GatedLayout<HN, ZK>::kThreads, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull[a], 1);
-            mbar_init(&tempty[a], 2 * 128 * L::kGroups);
+            mbar_init(&tempty[a], 2 * 256 * L::kBoxes);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -196,78 +197,79 @@ __global__ void __launch_bounds__(GatedLayout<HN, ZK>::kThreads, 1)
             }
         }
     } else {
-        const int group = (warp - 2) >> 2;
+        const int box = (warp - 2) >> 3;
+        const int half = ((warp - 2) >> 2) & 1;   // columns [32 half, 32 half + 32) of the box
         const int quarter = warp & 3;             // TMEM lanes this warp may read
         const int row = quarter * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-        const bool issuer = ((warp - 2) & 3) == 0 && lane == 0;
+        const bool issuer = ((warp - 2) & 7) == 0 && lane == 0;
         const uint32_t tempty0 = leader_addr(&tempty[0]);
         const uint64_t once = policy_evict_first();                // Z is next read in the backward pass
-        uint8_t* stg = smem + L::kEpi + group * L::kStgPerGroup;   // H, then Z's gate and other half
+        uint8_t* const base = smem + L::kEpi + box * L::kStgPerBox;
+        uint8_t* stg = base;   // H, and with ZK Z's gate and other half behind it
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
         for (int t = pair; t < num_tiles; t += num_pairs) {
             const int m0 = (t / num_n) * 256 + rank * 128;
-            const int n0 = (t % num_n) * HN + group * 64;
+            const int n0 = (t % num_n) * HN + box * 64;
             ok = mbar_wait_cluster(&tfull[acc], acc_phase, abort_flag);
-            if (issuer) bulk_wait_group_read<0>();   // the previous tile's stores have read the staging
-            ok = named_barrier_and(1 + group, 128, ok);   // the group leaves together or not at all
+            // the stores that read this staging have read it: the previous tile's, or without Z (two
+            // boxes in turn) the one before
+            if (issuer) bulk_wait_group_read<ZK ? 0 : 1>();
+            ok = named_barrier_and(1 + box, 256, ok);   // the box's warps leave together or not at all
             if (!ok) break;
             tc_fence_after();
             // 16 columns at a time, the next ones on their way from tensor memory meanwhile
-            const uint32_t col = tmem_base + lane_addr + static_cast<uint32_t>(acc * 2 * HN + group * 64);
+            const uint32_t col = tmem_base + lane_addr + static_cast<uint32_t>(acc * 2 * HN + box * 64 + half * 32);
             uint32_t g[2][16], u[2][16];
             tmem_ld_32x32b_x16(col, g[0]);
             tmem_ld_32x32b_x16(col + HN, u[0]);
             with_act(act, [&](auto which) {
                 constexpr int A = decltype(which)::value;
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        tmem_wait_ld();
-                        if (half == 0 || q == 0) {
-                            const uint32_t next = col + static_cast<uint32_t>(half * 32 + q * 16 + 16);
-                            tmem_ld_32x32b_x16(next, g[q ^ 1]);
-                            tmem_ld_32x32b_x16(next + HN, u[q ^ 1]);
-                        } else {                 // the accumulator is in registers: free it
-                            tc_fence_before();
-                            mbar_arrive_cluster(tempty0 + static_cast<uint32_t>(acc * 8));
+                for (int q = 0; q < 2; ++q) {
+                    tmem_wait_ld();
+                    if (q == 0) {
+                        tmem_ld_32x32b_x16(col + 16, g[1]);
+                        tmem_ld_32x32b_x16(col + 16 + HN, u[1]);
+                    } else {                 // the accumulator is in registers: free it
+                        tc_fence_before();
+                        mbar_arrive_cluster(tempty0 + static_cast<uint32_t>(acc * 8));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int at = row * 128 + (((half * 4 + q * 2 + j) ^ (row & 7)) << 4);
+                        uint32_t h[4], gz[4], uz[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = 8 * j + 2 * i;
+                            const float2 gf = make_float2(__uint_as_float(g[q][e]), __uint_as_float(g[q][e + 1]));
+                            const float2 uf = make_float2(__uint_as_float(u[q][e]), __uint_as_float(u[q][e + 1]));
+                            const float2 hf = __fmul2_rn(gate_act<A>(gf), uf);
+                            h[i] = float2_to_h16x2<EK>(hf.x, hf.y);
+                            gz[i] = float2_to_h16x2<EK>(gf.x, gf.y);
+                            uz[i] = float2_to_h16x2<EK>(uf.x, uf.y);
                         }
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int at = row * 128 + (((half * 4 + q * 2 + j) ^ (row & 7)) << 4);
-                            uint32_t h[4], gz[4], uz[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int e = 8 * j + 2 * i;
-                                const float2 gf = make_float2(__uint_as_float(g[q][e]), __uint_as_float(g[q][e + 1]));
-                                const float2 uf = make_float2(__uint_as_float(u[q][e]), __uint_as_float(u[q][e + 1]));
-                                const float2 hf = __fmul2_rn(gate_act<A>(gf), uf);
-                                h[i] = float2_to_h16x2<EK>(hf.x, hf.y);
-                                gz[i] = float2_to_h16x2<EK>(gf.x, gf.y);
-                                uz[i] = float2_to_h16x2<EK>(uf.x, uf.y);
-                            }
-                            *reinterpret_cast<uint4*>(stg + at) = make_uint4(h[0], h[1], h[2], h[3]);
-                            if constexpr (ZK) {
-                                *reinterpret_cast<uint4*>(stg + 16384 + at) = make_uint4(gz[0], gz[1], gz[2], gz[3]);
-                                *reinterpret_cast<uint4*>(stg + 32768 + at) = make_uint4(uz[0], uz[1], uz[2], uz[3]);
-                            }
+                        *reinterpret_cast<uint4*>(stg + at) = make_uint4(h[0], h[1], h[2], h[3]);
+                        if constexpr (ZK) {
+                            *reinterpret_cast<uint4*>(stg + 16384 + at) = make_uint4(gz[0], gz[1], gz[2], gz[3]);
+                            *reinterpret_cast<uint4*>(stg + 32768 + at) = make_uint4(uz[0], uz[1], uz[2], uz[3]);
                         }
                     }
                 }
             });
             fence_proxy_async_smem();
-            named_barrier_sync(1 + group, 128);
+            named_barrier_sync(1 + box, 256);
             if (issuer && n0 < F && m0 < M) {        // the maps clip the tails
                 tma_store_2d(&map_h, stg, n0, m0);
                 if constexpr (ZK) {
                     tma_store_3d_hint(&map_z, stg + 16384, n0, 0, m0, once);
                     tma_store_3d_hint(&map_z, stg + 32768, n0, 1, m0, once);
                 }
-                bulk_commit_group();
             }
+            if (issuer) bulk_commit_group();
+            if constexpr (!ZK) stg = base + (acc ^ 1) * 16384;
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }

@@ -1033,6 +1033,7 @@ __global__ void __launch_bounds__(256)
     if (i >= MC) return;
     float4 a = *reinterpret_cast<const float4*>(ws + i);
     float4 b = *reinterpret_cast<const float4*>(ws + i + 4);
+#pragma unroll 8   // the loads of eight splits at a time, added in order
     for (int s = 1; s < S; ++s) {
         const float4 x = *reinterpret_cast<const float4*>(ws + s * MC + i);
         const float4 y = *reinterpret_cast<const float4*>(ws + s * MC + i + 4);
