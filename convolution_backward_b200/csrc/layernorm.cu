@@ -400,26 +400,24 @@ __global__ void __launch_bounds__(ln_block(MODE, false), ln_per_sm(MODE, VEC * N
             x.v[v].zero();
             if (live && v < mine) x.v[v].load(from, (lane + v * p.T) * VEC);
         }
+        float2 f[P::kUnits][kPer];   // widened once: x, then x - mean
         float2 s = make_float2(0.f, 0.f);
 #pragma unroll
         for (int u = 0; u < P::kUnits; ++u) {
-            float2 f[kPer];
-            x.unit(u, f);
+            x.unit(u, f[u]);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) s = __fadd2_rn(s, f[i]);
+            for (int i = 0; i < kPer; ++i) s = __fadd2_rn(s, f[u][i]);
         }
         const float mean = row_sum<MULTI, false>(s.x + s.y, 0.f, p.T, group, red, turn).x / fc;
         const float2 minus = make_float2(-mean, -mean);
         float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
         for (int u = 0; u < P::kUnits; ++u) {
-            float2 f[kPer];
-            x.unit(u, f);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) f[i] = __fadd2_rn(f[i], minus);
-            mask_unit<VEC>(u, mine, f);
+            for (int i = 0; i < kPer; ++i) f[u][i] = __fadd2_rn(f[u][i], minus);
+            mask_unit<VEC>(u, mine, f[u]);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) ss = ffma2(f[i], f[i], ss);
+            for (int i = 0; i < kPer; ++i) ss = ffma2(f[u][i], f[u][i], ss);
         }
         const float rstd = rsqrtf(row_sum<MULTI, false>(ss.x + ss.y, 0.f, p.T, group, red, turn).x / fc + p.eps);
         if (!live) return;
@@ -430,14 +428,13 @@ __global__ void __launch_bounds__(ln_block(MODE, false), ln_per_sm(MODE, VEC * N
         const float2 r2 = make_float2(rstd, rstd);
 #pragma unroll
         for (int u = 0; u < P::kUnits; ++u) {
-            float2 f[kPer], g[kPer], b[kPer];
+            float2 g[kPer], b[kPer];
             if (VEC > 1 && u >= mine) continue;
-            x.unit(u, f);
             gamma.unit(u, p.C, p.T, lane, g);
             beta.unit(u, p.C, p.T, lane, b);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) f[i] = ffma2(__fmul2_rn(__fadd2_rn(f[i], minus), r2), g[i], b[i]);
-            x.set_unit(u, f);
+            for (int i = 0; i < kPer; ++i) f[u][i] = ffma2(__fmul2_rn(f[u][i], r2), g[i], b[i]);
+            x.set_unit(u, f[u]);
         }
         char* out = static_cast<char*>(p.y) + m * p.C * es;
 #pragma unroll
