@@ -16,6 +16,7 @@ fp32 accumulate).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -487,9 +488,16 @@ def _allocator(device, stream):
     return None if stream == current else _Allocator(stream, current)
 
 
+def _torch():
+    import torch
+    return torch
+
+
 def _empty(al, like, shape, dtype):
     if al is not None:
         return al.empty(like, shape, dtype)
+    if dtype == like.dtype and shape == like.shape:
+        return _torch().empty_like(like)   # half the host time of the general form
     return like.new_empty(shape, dtype=dtype)
 
 
@@ -498,9 +506,6 @@ def _out(al, out, like, shape):
     if out is not None:
         _like(out, shape, like.dtype, "out")
         return out
-    if al is None and shape == like.shape:
-        import torch
-        return torch.empty_like(like)
     return _empty(al, like, shape, like.dtype)
 
 
@@ -526,8 +531,10 @@ def layernorm_forward(X, gamma=None, beta=None, eps=1e-5, stats=False, out=None,
             _like(t, (C,), X.dtype, what)
     al = _allocator(dev, stream)
     out = _out(al, out, X, X.shape)
-    mean = _empty(al, X, X.shape[:-1], torch.float32) if stats else None
-    rstd = _empty(al, X, X.shape[:-1], torch.float32) if stats else None
+    mean = rstd = None
+    if stats:
+        mean = _empty(al, X, X.shape[:-1], torch.float32)
+        rstd = _empty(al, mean, mean.shape, torch.float32)
     if al is not None:
         al.uses(X, *given)
     _call(dev, "dgrad_layernorm_forward", lib().dgrad_layernorm_forward, M, C, code, float(eps), X.data_ptr(),
@@ -535,12 +542,16 @@ def layernorm_forward(X, gamma=None, beta=None, eps=1e-5, stats=False, out=None,
     return (out, mean, rstd) if stats else out
 
 
+@functools.lru_cache(maxsize=256)
+def _ln_workspace(M, C, code) -> int:
+    nb = ctypes.c_size_t()
+    _check(lib().dgrad_layernorm_backward_workspace(M, C, code, ctypes.byref(nb)), "dgrad_layernorm_backward_workspace")
+    return nb.value
+
+
 def layernorm_backward_workspace_bytes(M, C, dtype) -> int:
     """Workspace bytes layernorm_backward needs for M rows of C elements of a torch dtype (host only)."""
-    nb = ctypes.c_size_t()
-    _check(lib().dgrad_layernorm_backward_workspace(int(M), int(C), _code_of(dtype), ctypes.byref(nb)),
-           "dgrad_layernorm_backward_workspace")
-    return nb.value
+    return _ln_workspace(int(M), int(C), _code_of(dtype))
 
 
 def layernorm_backward(dY, X, mean, rstd, gamma=None, param_grads=True, workspace=None, out=None, stream=None):
@@ -567,10 +578,13 @@ def layernorm_backward(dY, X, mean, rstd, gamma=None, param_grads=True, workspac
     dgamma = dbeta = None
     ws_bytes = 0
     if param_grads:
-        dgamma, dbeta = _empty(al, X, (C,), X.dtype), _empty(al, X, (C,), X.dtype)
+        dgamma = _empty(al, X if gamma is None else gamma, (C,), X.dtype)
+        dbeta = _empty(al, dgamma, (C,), X.dtype)
         if workspace is None:
-            workspace = _empty(al, X, (max(layernorm_backward_workspace_bytes(M, C, X.dtype), 16),), torch.uint8)
-        ws_bytes = workspace.numel() * workspace.element_size()
+            ws_bytes = max(_ln_workspace(M, C, code), 16)
+            workspace = _empty(al, X, (ws_bytes,), torch.uint8)
+        else:
+            ws_bytes = workspace.numel() * workspace.element_size()
     if al is not None:
         al.uses(dY, X, mean, rstd, *given)
     _call(dev, "dgrad_layernorm_backward", lib().dgrad_layernorm_backward, M, C, code, dY.data_ptr(), X.data_ptr(),
@@ -617,12 +631,16 @@ def gated_forward(X, W, act="silu", preact=False, out=None, stream=None):
     return (out, Z) if preact else out
 
 
+@functools.lru_cache(maxsize=256)
+def _gated_workspace(M, C, F) -> int:
+    nb = ctypes.c_size_t()
+    _check(lib().dgrad_gated_backward_workspace(M, C, F, ctypes.byref(nb)), "dgrad_gated_backward_workspace")
+    return nb.value
+
+
 def gated_backward_workspace_bytes(M, C, F) -> int:
     """Workspace bytes gated_backward needs (host only)."""
-    nb = ctypes.c_size_t()
-    _check(lib().dgrad_gated_backward_workspace(int(M), int(C), int(F), ctypes.byref(nb)),
-           "dgrad_gated_backward_workspace")
-    return nb.value
+    return _gated_workspace(int(M), int(C), int(F))
 
 
 def gated_backward(dH, X, Z, W, act="silu", input_grad=True, weight_grad=True, workspace=None, stream=None):
@@ -649,7 +667,7 @@ def gated_backward(dH, X, Z, W, act="silu", input_grad=True, weight_grad=True, w
     dX = _out(al, None, X, X.shape) if input_grad else None
     dW = _out(al, None, W, W.shape) if weight_grad else None
     if workspace is None:
-        workspace = _empty(al, X, (max(gated_backward_workspace_bytes(M, C, F), 16),), torch.uint8)
+        workspace = _empty(al, X, (max(_gated_workspace(M, C, F), 16),), torch.uint8)
     if al is not None:
         al.uses(dH, X, Z, W, *given)
     _call(dev, "dgrad_gated_backward", lib().dgrad_gated_backward, M, C, F, code, acode, dH.data_ptr(), X.data_ptr(),
