@@ -22,6 +22,13 @@
 // memory with bulk copies, wherever their first byte lies (a copy starts at the 16-byte
 // boundary before it), and refills a stage one chunk after it was read.  Blocks with
 // one step load from global memory directly.
+//
+// Rows whose length is no multiple of 16 bytes start anywhere.  They too are read and
+// written in the 16-byte vectors that lie wholly inside them; the elements before the
+// first and behind the last (at most 14, fp32 6) go to one lane each.  A row's offset on
+// the 16-byte grid repeats every eight (fp32: four) rows, and the rows of a thread are a
+// multiple of that apart, so a thread keeps its columns, and with them its parameters and
+// its column sums, in registers from row to row.
 // All sums and statistics are fp32; results are rounded once.
 //
 // The parameter gradients are sums down the columns.  Each block keeps its rows'
@@ -69,61 +76,137 @@ __device__ __forceinline__ float2 row_sum(float a, float b, int T, int group, fl
     return make_float2(a, b);
 }
 
-// gamma or beta as fp32 in shared memory, for rows of at most a warp: vector v's quarters
-// (four elements each) lie n vectors apart, so that adjacent lanes' 16-byte reads are
-// adjacent.  A null pointer gives the constant.
-template <int EK, int VEC>
-__device__ __forceinline__ void spread_param(float* dst, const void* src, float constant, int C)
-{
-    const int n = C / VEC;
-    for (int c = threadIdx.x; c < C; c += blockDim.x) {
-        float f[1] = {constant};
-        if (src) {
-            RowVec<EK, 1> v;
-            v.load(src, c);
-            v.unpack(f);
-        }
-        const int at = VEC == 1 ? c : ((c % VEC / 4) * n + c / VEC) * 4 + c % 4;
-        dst[at] = f[0];
-    }
-}
+// One thread's part of a row of C elements.  The row's whole 16-byte vectors start at
+// column `head`; the thread holds those numbered lane, lane + T, .., `mine` of them.  SH (the
+// row starts off its 16-byte grid, so head may not be 0): also one of the columns outside
+// the vectors, `single`, or none (-1).
+template <int EK, bool SH>
+struct LnLane {
+    static constexpr int es = elem_bytes<EK>();
+    static constexpr int VEC = 16 / es;
+    using V = RowVec<EK, VEC>;
+    using S = RowVec<EK, 1>;
+    int lane, T, C, head, mine, single;
 
-// The pairs of unit u (RowPart) of a parameter: from shared memory (rows of at most a warp),
-// or from the thread's registers.
-template <int EK, int VEC, int NV, bool MULTI>
+    __device__ __forceinline__ LnLane(int lane_, int T_, int C_, long long row)
+        : lane(lane_), T(T_), C(C_), head(0), single(-1)
+    {
+        if constexpr (SH) {
+            head = static_cast<int>((VEC - row * C % VEC) % VEC);
+            if (head > C) head = C;
+        }
+        const int n = (C - head) / VEC;
+        mine = lane < n ? (n - lane + T - 1) / T : 0;
+        if constexpr (SH) {
+            if (lane < head)
+                single = lane;
+            else if (lane < C - n * VEC)
+                single = n * VEC + lane;
+        }
+    }
+    // Column of vector v's first element.
+    __device__ __forceinline__ int col(int v) const { return (SH ? head : 0) + (lane + v * T) * VEC; }
+
+    // Vector v, and the single column, of the row at p (zeros where there is none).
+    __device__ __forceinline__ void load(V& x, const void* p, int v) const
+    {
+        x.zero();
+        if (v < mine) x.load(p, col(v));
+    }
+    __device__ __forceinline__ float load_single(const void* p) const
+    {
+        float f[1] = {0.f};
+        if (single >= 0) {
+            S x;
+            x.load(p, single);
+            x.unpack(f);
+        }
+        return f[0];
+    }
+    __device__ __forceinline__ void store(const V& x, void* p, int v, const void* base, long long bytes, int* status) const
+    {
+        if (v < mine && store_ok(base, bytes, static_cast<char*>(p) + col(v) * es, 16, status)) x.store(p, col(v));
+    }
+    __device__ __forceinline__ void store_single(float f, void* p, const void* base, long long bytes, int* status) const
+    {
+        if (single < 0 || !store_ok(base, bytes, static_cast<char*>(p) + single * es, es, status)) return;
+        S x;
+        const float a[1] = {f};
+        x.pack(a);
+        x.store(p, single);
+    }
+    // Zero what vector v holds when it is none of the thread's.
+    __device__ __forceinline__ void mask(int v, float2 (&f)[VEC / 2]) const
+    {
+        if (v >= mine) {
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) f[i] = make_float2(0.f, 0.f);
+        }
+    }
+};
+
+// gamma or beta.  REG: in the thread's registers, at its columns.  Else as fp32 in shared
+// memory (rows on the 16-byte grid, at most a warp each): vector v's quarters (four
+// elements each) lie n vectors apart, so that adjacent lanes' 16-byte reads are adjacent.
+// A null pointer gives the constant.
+template <int EK, int NV, bool REG, bool SH>
 struct LnParam {
-    using P = RowPart<EK, VEC, NV>;
-    P reg;
+    using L = LnLane<EK, SH>;
+    static constexpr int VEC = L::VEC;
+    typename L::V reg[NV];
+    float single;
     const float* sm;
 
-    __device__ __forceinline__ void init(float* smem, const void* src, float constant, int C, int T, int lane)
+    __device__ __forceinline__ void init(const L& l, float* smem, const void* src, float constant)
     {
-        if constexpr (MULTI) {
+        if constexpr (REG) {
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const int c = (lane + v * T) * VEC;
                 if (constant != 0.f)
-                    reg.v[v].ones();
+                    reg[v].ones();
                 else
-                    reg.v[v].zero();
-                if (src && c < C) reg.v[v].load(src, c);
+                    reg[v].zero();
+                // a thread's columns lie anywhere on the parameter's own 16-byte grid
+                if (src && v < l.mine) {
+                    if constexpr (SH) {
+                        float f[VEC];
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) {
+                            RowVec<EK, 1> x;
+                            float e[1];
+                            x.load(src, l.col(v) + i);
+                            x.unpack(e);
+                            f[i] = e[0];
+                        }
+                        reg[v].pack(f);
+                    } else {
+                        l.load(reg[v], src, v);
+                    }
+                }
             }
+            single = src ? l.load_single(src) : constant;
         } else {
-            spread_param<EK, VEC>(smem, src, constant, C);
+            const int n = l.C / VEC;
+            for (int c = threadIdx.x; c < l.C; c += blockDim.x) {
+                float f[1] = {constant};
+                if (src) {
+                    RowVec<EK, 1> x;
+                    x.load(src, c);
+                    x.unpack(f);
+                }
+                smem[((c % VEC / 4) * n + c / VEC) * 4 + c % 4] = f[0];
+            }
             sm = smem;
         }
     }
 
-    __device__ __forceinline__ void unit(int u, int C, int T, int lane, float2 (&f)[P::kPer]) const
+    __device__ __forceinline__ void get(const L& l, int v, float2 (&f)[VEC / 2]) const
     {
-        if constexpr (MULTI) {
-            reg.unit(u, f);
-        } else if constexpr (VEC == 1) {
-            const int c = lane + 2 * u * T;
-            f[0] = make_float2(c < C ? sm[c] : 0.f, c + T < C ? sm[c + T] : 0.f);
+        if constexpr (REG) {
+            unpack_pairs(reg[v], f);
         } else {
-            const int n = C / VEC;
-            const float4* q = reinterpret_cast<const float4*>(sm) + lane + u * T;
+            const int n = l.C / VEC;
+            const float4* q = reinterpret_cast<const float4*>(sm) + l.lane + v * l.T;
 #pragma unroll
             for (int i = 0; i < VEC / 4; ++i) {
                 const float4 w = q[i * n];
@@ -134,29 +217,6 @@ struct LnParam {
     }
 };
 
-// Vectors (or elements) of a row that this lane holds: the first `mine` of its NV.
-template <int VEC>
-__device__ __forceinline__ int lane_vectors(int C, int T, int lane)
-{
-    const int n = C / VEC;
-    return lane < n ? (n - lane + T - 1) / T : 0;
-}
-
-// Zero the elements of unit u that lie behind the row's end (whole vectors, or either element).
-template <int VEC, int PER>
-__device__ __forceinline__ void mask_unit(int u, int mine, float2 (&f)[PER])
-{
-    if constexpr (VEC == 1) {
-        if (2 * u >= mine) f[0].x = 0.f;
-        if (2 * u + 1 >= mine) f[0].y = 0.f;
-    } else {
-        if (u >= mine) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) f[i] = make_float2(0.f, 0.f);
-        }
-    }
-}
-
 // How a row's threads meet: 0, within a warp; 1, whole warps of a block of several rows
 // (or of 256 threads); 2, a block of more than 256 threads.
 constexpr int ln_mode(int T) { return T <= 32 ? 0 : T <= kLnBlock ? 1 : 2; }
@@ -164,29 +224,36 @@ constexpr int ln_mode(int T) { return T <= 32 ? 0 : T <= kLnBlock ? 1 : 2; }
 // Threads of a block.  Where a warp needs no other (mode 0), the backward pass has many
 // instructions per chunk and few warps: with blocks of four warps a chunk waits for fewer
 // others (401408 x 96 bf16: 43.9 us, against 47.3 with eight; forward 21.4 against 21.0).
-constexpr int ln_block(int mode, bool backward) { return mode == 2 ? kLnMaxMulti : mode == 0 && backward ? 128 : kLnBlock; }
-
-// Blocks an SM holds, by the registers their elements take.
-constexpr int ln_per_sm(int mode, int elems, bool backward)
+// Rows off the 16-byte grid need eight rows at a time, and keep eight warps.
+constexpr int ln_block(int mode, bool backward, bool sh)
 {
-    return mode == 2 ? 1 : mode == 0 && backward ? 4 : mode == 0 && elems <= 16 ? 3 : 2;
+    return mode == 2 ? kLnMaxMulti : mode == 0 && backward && !sh ? 128 : kLnBlock;
 }
 
-// Shared memory for `count` parameters (rows of at most a warp).
-__host__ __device__ constexpr int ln_param_bytes(int mode, int C, int count)
+// Blocks an SM holds, by the registers their elements take.
+constexpr int ln_per_sm(int mode, int elems, bool backward, bool sh)
 {
-    return mode == 0 ? (count * C * 4 + 15) / 16 * 16 : 0;
+    return mode == 2 ? 1 : mode == 0 && backward && !sh ? 4 : mode == 0 && elems <= 16 && !backward && !sh ? 3 : 2;
+}
+
+// Rows on the 16-byte grid of at most a warp keep their parameters in shared memory.
+constexpr bool ln_param_regs(int mode, bool sh) { return mode > 0 || sh; }
+
+// Shared memory for `count` parameters.
+__host__ __device__ constexpr int ln_param_bytes(int mode, bool sh, int C, int count)
+{
+    return ln_param_regs(mode, sh) ? 0 : (count * C * 4 + 15) / 16 * 16;
 }
 
 // Elements per thread that fit its registers without spills.  Forward: 48 where the
 // parameters are in shared memory, 24 or (one block per SM) 32 beside them.  Backward: the
-// column sums take two registers per element.  fp32 and element-wise loads take a register
-// for every element where 16-bit pairs take half.
-constexpr int ln_most(int mode, bool single, bool f32, bool backward)
+// column sums take two registers per element.  fp32 takes a register for every element
+// where 16-bit pairs take half.
+constexpr int ln_most(int mode, bool sh, bool f32, bool backward)
 {
-    if (single || (f32 && backward)) return 16;
-    if (backward) return 24;
-    return f32 ? (mode == 1 ? 16 : 24) : mode == 0 ? 48 : mode == 1 ? 24 : 32;
+    if (backward) return f32 ? 16 : 24;
+    if (!ln_param_regs(mode, sh)) return f32 ? 24 : 48;
+    return f32 ? (mode == 1 ? 16 : 24) : mode == 2 ? 32 : 24;
 }
 
 // --------------------------------------------------------------- ring of chunks
@@ -357,8 +424,8 @@ struct LnFwd {
     int* status;
 };
 
-template <int EK, int VEC, int NV, int MODE, bool RING>
-__global__ void __launch_bounds__(ln_block(MODE, false), ln_per_sm(MODE, VEC * NV, false))
+template <int EK, int NV, int MODE, bool RING, bool SH>
+__global__ void __launch_bounds__(ln_block(MODE, false, SH), ln_per_sm(MODE, 16 / elem_bytes<EK>() * NV, false, SH))
     ln_fwd_kernel(const LnFwd p)
 {
     constexpr int es = elem_bytes<EK>();
@@ -368,86 +435,89 @@ __global__ void __launch_bounds__(ln_block(MODE, false), ln_per_sm(MODE, VEC * N
     pdl_wait();      // the previous kernel on the stream has finished
     pdl_trigger();   // the next one may start its set-up
     constexpr bool MULTI = MODE > 0;
+    constexpr bool REG = ln_param_regs(MODE, SH);
     __shared__ float2 red[MULTI ? 128 : 1];
     __shared__ uint64_t bars[RING ? 2 * kMaxStages : 1];
     __shared__ int abort_flag;
     extern __shared__ __align__(16) uint8_t dyn[];
     float* params = reinterpret_cast<float*>(dyn);
-    uint8_t* ring = dyn + ln_param_bytes(MODE, p.C, 2);
+    uint8_t* ring = dyn + ln_param_bytes(MODE, SH, p.C, 2);
     uint64_t* full = bars;
     uint64_t* empty = bars + kMaxStages;
     if constexpr (RING)
         ln_start<1>(p.ring, src, nullptr, nullptr, p.M, row_bytes, ring, full, empty, &abort_flag);
     const int group = threadIdx.x / p.T;
-    const int lane = threadIdx.x - group * p.T;
     int turn = 0;
     const float fc = static_cast<float>(p.C);
-    const int mine = lane_vectors<VEC>(p.C, p.T, lane);
-
-    // gamma and beta: in registers where whole warps share a row; where a row takes at most a
-    // warp, every lane meets few of them often, and reads them widened from shared memory
-    using P = RowPart<EK, VEC, NV>;
-    constexpr int kPer = P::kPer;
-    LnParam<EK, VEC, NV, MULTI> gamma, beta;
-    gamma.init(params, p.gamma, 1.0f, p.C, p.T, lane);
-    beta.init(params + p.C, p.beta, 0.f, p.C, p.T, lane);
-    if constexpr (!MULTI) __syncthreads();
+    using L = LnLane<EK, SH>;
+    constexpr int H = L::VEC / 2;   // pairs of a vector
+    // every row of this thread starts where this one does on its 16-byte grid (ln_plan)
+    const L l(threadIdx.x - group * p.T, p.T, p.C, static_cast<long long>(blockIdx.x) * (RING ? p.ring.R : p.G) + group);
+    LnParam<EK, NV, REG, SH> gamma, beta;
+    gamma.init(l, params, p.gamma, 1.0f);
+    beta.init(l, params + p.C, p.beta, 0.f);
+    if constexpr (!REG) __syncthreads();
     // row m, read from `from`; every thread of the block takes part in each reduction
     auto one_row = [&](long long m, bool live, const void* from) {
-        P x;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            x.v[v].zero();
-            if (live && v < mine) x.v[v].load(from, (lane + v * p.T) * VEC);
-        }
-        float2 f[P::kUnits][kPer];   // widened once: x, then x - mean
+        float2 f[NV][H];   // widened once: x, then x - mean
         float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int u = 0; u < P::kUnits; ++u) {
-            x.unit(u, f[u]);
+        for (int v = 0; v < NV; ++v) {
+            typename L::V x;
+            x.zero();
+            if (live) l.load(x, from, v);
+            unpack_pairs(x, f[v]);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) s = __fadd2_rn(s, f[u][i]);
+            for (int i = 0; i < H; ++i) s = __fadd2_rn(s, f[v][i]);
+        }
+        float one = 0.f;   // the single column
+        if constexpr (SH) {
+            if (live) one = l.load_single(from);
+            s.x += one;
         }
         const float mean = row_sum<MULTI, false>(s.x + s.y, 0.f, p.T, group, red, turn).x / fc;
         const float2 minus = make_float2(-mean, -mean);
         float2 ss = make_float2(0.f, 0.f);
+        if constexpr (SH) {
+            one = l.single < 0 ? 0.f : one - mean;
+            ss.x = one * one;
+        }
 #pragma unroll
-        for (int u = 0; u < P::kUnits; ++u) {
+        for (int v = 0; v < NV; ++v) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) f[u][i] = __fadd2_rn(f[u][i], minus);
-            mask_unit<VEC>(u, mine, f[u]);
+            for (int i = 0; i < H; ++i) f[v][i] = __fadd2_rn(f[v][i], minus);
+            l.mask(v, f[v]);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) ss = ffma2(f[u][i], f[u][i], ss);
+            for (int i = 0; i < H; ++i) ss = ffma2(f[v][i], f[v][i], ss);
         }
         const float rstd = rsqrtf(row_sum<MULTI, false>(ss.x + ss.y, 0.f, p.T, group, red, turn).x / fc + p.eps);
         if (!live) return;
-        if (lane == 0) {
+        if (l.lane == 0) {
             if (p.mean && store_ok(p.mean, p.M * 4, p.mean + m, 4, p.status)) p.mean[m] = mean;
             if (p.rstd && store_ok(p.rstd, p.M * 4, p.rstd + m, 4, p.status)) p.rstd[m] = rstd;
         }
         const float2 r2 = make_float2(rstd, rstd);
-#pragma unroll
-        for (int u = 0; u < P::kUnits; ++u) {
-            float2 g[kPer], b[kPer];
-            if (VEC > 1 && u >= mine) continue;
-            gamma.unit(u, p.C, p.T, lane, g);
-            beta.unit(u, p.C, p.T, lane, b);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) f[u][i] = ffma2(__fmul2_rn(f[u][i], r2), g[i], b[i]);
-            x.set_unit(u, f[u]);
-        }
         char* out = static_cast<char*>(p.y) + m * p.C * es;
+        if constexpr (SH) l.store_single(fmaf(one * rstd, gamma.single, beta.single), out, p.y, p.M * p.C * es, p.status);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = (lane + v * p.T) * VEC;
-            if (v < mine && store_ok(p.y, p.M * p.C * es, out + c * es, VEC * es, p.status)) x.v[v].store(out, c);
+            if (v >= l.mine) continue;
+            float2 g[H], b[H];
+            gamma.get(l, v, g);
+            beta.get(l, v, b);
+#pragma unroll
+            for (int i = 0; i < H; ++i) f[v][i] = ffma2(__fmul2_rn(f[v][i], r2), g[i], b[i]);
+            typename L::V y;
+            pack_pairs(y, f[v]);
+            l.store(y, out, v, p.y, p.M * p.C * es, p.status);
         }
     };
     if constexpr (!RING) {
         const long long m = static_cast<long long>(blockIdx.x) * p.G + group;
         one_row(m, m < p.M, static_cast<const char*>(p.x) + m * p.C * es);
     } else {
-        ln_chunks<1>(p.ring, src, nullptr, nullptr, p.M, row_bytes, ring, full, empty, &abort_flag, p.status, [&](long long first, const uint8_t* st) {
+        ln_chunks<1>(p.ring, src, nullptr, nullptr, p.M, row_bytes, ring, full, empty, &abort_flag, p.status,
+                     [&](long long first, const uint8_t* st) {
                          st += slot_shift(first * p.C * es);
                          for (int r = group; r < p.ring.R; r += p.G)
                              one_row(first + r, first + r < p.M, st + r * p.C * es);
@@ -534,8 +604,8 @@ struct LnBwd {
     int* status;
 };
 
-template <int EK, int VEC, int NV, int MODE, bool RING>
-__global__ void __launch_bounds__(ln_block(MODE, true), ln_per_sm(MODE, VEC * NV, true))
+template <int EK, int NV, int MODE, bool RING, bool SH>
+__global__ void __launch_bounds__(ln_block(MODE, true, SH), ln_per_sm(MODE, 16 / elem_bytes<EK>() * NV, true, SH))
     ln_bwd_kernel(const LnBwd p)
 {
     constexpr int es = elem_bytes<EK>();
@@ -545,63 +615,73 @@ __global__ void __launch_bounds__(ln_block(MODE, true), ln_per_sm(MODE, VEC * NV
     pdl_wait();
     pdl_trigger();
     constexpr bool MULTI = MODE > 0;
+    constexpr bool REG = ln_param_regs(MODE, SH);
     __shared__ float2 red[MULTI ? 128 : 1];
     __shared__ uint64_t bars[RING ? 2 * kMaxStages : 1];
     __shared__ int abort_flag;
     extern __shared__ __align__(16) uint8_t dyn[];
     float* params = reinterpret_cast<float*>(dyn);
-    uint8_t* ring = dyn + ln_param_bytes(MODE, p.C, 1);   // at the end column sums [warps or groups][2][C]
+    uint8_t* ring = dyn + ln_param_bytes(MODE, SH, p.C, 1);   // at the end column sums [warps or groups][2][C]
     uint64_t* full = bars;
     uint64_t* empty = bars + kMaxStages;
     if constexpr (RING) ln_start<2>(p.ring, src, p.mean, p.rstd, p.M, row_bytes, ring, full, empty, &abort_flag);
     const int group = threadIdx.x / p.T;
-    const int lane = threadIdx.x - group * p.T;
     int turn = 0;
     const float inv_c = 1.0f / static_cast<float>(p.C);
-    const int mine = lane_vectors<VEC>(p.C, p.T, lane);
-
-    using P = RowPart<EK, VEC, NV>;
-    constexpr int kPer = P::kPer;
-    LnParam<EK, VEC, NV, MULTI> gamma;   // as in the forward kernel
-    gamma.init(params, p.gamma, 1.0f, p.C, p.T, lane);
-    if constexpr (!MULTI) __syncthreads();
-    float2 dg[P::kUnits][kPer], db[P::kUnits][kPer];   // sums down the rows
+    using L = LnLane<EK, SH>;
+    constexpr int H = L::VEC / 2;
+    const L l(threadIdx.x - group * p.T, p.T, p.C, static_cast<long long>(blockIdx.x) * (RING ? p.ring.R : p.G) + group);
+    LnParam<EK, NV, REG, SH> gamma;   // as in the forward kernel
+    gamma.init(l, params, p.gamma, 1.0f);
+    if constexpr (!REG) __syncthreads();
+    float2 dg[NV][H], db[NV][H];   // sums down the rows
+    float dg1 = 0.f, db1 = 0.f;    // the single column's
 #pragma unroll
-    for (int u = 0; u < P::kUnits; ++u)
+    for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) dg[u][i] = db[u][i] = make_float2(0.f, 0.f);
+        for (int i = 0; i < H; ++i) dg[v][i] = db[v][i] = make_float2(0.f, 0.f);
     auto one_row = [&](long long m, bool live, const void* fx, const void* fd, float mean, float rstd) {
-        P x, dy;
+        typename L::V x[NV], dy[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = (lane + v * p.T) * VEC;
-            x.v[v].zero();
-            dy.v[v].zero();
-            if (live && v < mine) {
-                x.v[v].load(fx, c);
-                dy.v[v].load(fd, c);
+            x[v].zero();
+            dy[v].zero();
+            if (live) {
+                l.load(x[v], fx, v);
+                l.load(dy[v], fd, v);
             }
         }
         const float2 minus = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
         float2 sq = make_float2(0.f, 0.f), sqn = sq;
+        float x1 = 0.f, q1 = 0.f;   // the single column
+        if constexpr (SH) {
+            if (live && l.single >= 0) {
+                const float d = l.load_single(fd);
+                x1 = l.load_single(fx) - mean;
+                q1 = d * gamma.single;
+                sq.x = q1;
+                sqn.x = q1 * (x1 * rstd);
+                dg1 = fmaf(d, x1 * rstd, dg1);
+                db1 += d;
+            }
+        }
 #pragma unroll
-        for (int u = 0; u < P::kUnits; ++u) {
+        for (int v = 0; v < NV; ++v) {
             // a dead row or column must add exactly nothing, whatever mean and rstd hold
-            if (!live || (VEC > 1 && u >= mine)) continue;
-            float2 n[kPer], d[kPer], g[kPer];
-            x.unit(u, n);
-            dy.unit(u, d);
-            gamma.unit(u, p.C, p.T, lane, g);
+            if (!live || v >= l.mine) continue;
+            float2 n[H], d[H], g[H];
+            unpack_pairs(x[v], n);
+            unpack_pairs(dy[v], d);
+            gamma.get(l, v, g);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) n[i] = __fmul2_rn(__fadd2_rn(n[i], minus), r2);
-            mask_unit<VEC>(u, mine, n);
+            for (int i = 0; i < H; ++i) n[i] = __fmul2_rn(__fadd2_rn(n[i], minus), r2);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
+            for (int i = 0; i < H; ++i) {
                 const float2 q = __fmul2_rn(d[i], g[i]);
                 sq = __fadd2_rn(sq, q);
                 sqn = ffma2(q, n[i], sqn);
-                dg[u][i] = ffma2(d[i], n[i], dg[u][i]);
-                db[u][i] = __fadd2_rn(db[u][i], d[i]);
+                dg[v][i] = ffma2(d[i], n[i], dg[v][i]);
+                db[v][i] = __fadd2_rn(db[v][i], d[i]);
             }
         }
         const float2 t = row_sum<MULTI, true>(sq.x + sq.y, sqn.x + sqn.y, p.T, group, red, turn);
@@ -609,23 +689,20 @@ __global__ void __launch_bounds__(ln_block(MODE, true), ln_per_sm(MODE, VEC * NV
         // rstd (q - mq - n mqn) = q rstd + ((x - mean) (-rstd^2 mqn) - rstd mq)
         const float a = -rstd * rstd * (t.y * inv_c), b = -rstd * (t.x * inv_c);
         const float2 a2 = make_float2(a, a), b2 = make_float2(b, b);
-#pragma unroll
-        for (int u = 0; u < P::kUnits; ++u) {
-            if (VEC > 1 && u >= mine) continue;
-            float2 f[kPer], d[kPer], g[kPer];
-            x.unit(u, f);
-            dy.unit(u, d);
-            gamma.unit(u, p.C, p.T, lane, g);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                f[i] = ffma2(__fmul2_rn(d[i], g[i]), r2, ffma2(__fadd2_rn(f[i], minus), a2, b2));
-            x.set_unit(u, f);
-        }
         char* out = static_cast<char*>(p.dx) + m * p.C * es;
+        if constexpr (SH) l.store_single(fmaf(q1, rstd, fmaf(x1, a, b)), out, p.dx, p.M * p.C * es, p.status);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = (lane + v * p.T) * VEC;
-            if (v < mine && store_ok(p.dx, p.M * p.C * es, out + c * es, VEC * es, p.status)) x.v[v].store(out, c);
+            if (v >= l.mine) continue;
+            float2 f[H], d[H], g[H];
+            unpack_pairs(x[v], f);
+            unpack_pairs(dy[v], d);
+            gamma.get(l, v, g);
+#pragma unroll
+            for (int i = 0; i < H; ++i)
+                f[i] = ffma2(__fmul2_rn(d[i], g[i]), r2, ffma2(__fadd2_rn(f[i], minus), a2, b2));
+            pack_pairs(x[v], f);
+            l.store(x[v], out, v, p.dx, p.M * p.C * es, p.status);
         }
     };
     if constexpr (!RING) {
@@ -634,7 +711,8 @@ __global__ void __launch_bounds__(ln_block(MODE, true), ln_per_sm(MODE, VEC * NV
         one_row(m, live, static_cast<const char*>(p.x) + m * p.C * es, static_cast<const char*>(p.dy) + m * p.C * es,
                 live ? p.mean[m] : 0.f, live ? p.rstd[m] : 0.f);
     } else {
-        ln_chunks<2>(p.ring, src, p.mean, p.rstd, p.M, row_bytes, ring, full, empty, &abort_flag, p.status, [&](long long first, const uint8_t* st) {
+        ln_chunks<2>(p.ring, src, p.mean, p.rstd, p.M, row_bytes, ring, full, empty, &abort_flag, p.status,
+                     [&](long long first, const uint8_t* st) {
                          const float* sm = reinterpret_cast<const float*>(st + 2 * p.ring.pitch);
                          const int shift = slot_shift(first * p.C * es);
                          for (int r = group; r < p.ring.R; r += p.G) {
@@ -651,14 +729,18 @@ __global__ void __launch_bounds__(ln_block(MODE, true), ln_per_sm(MODE, VEC * NV
     // `put` gets every column this thread holds, with its two sums
     auto each = [&](auto put) {
 #pragma unroll
-        for (int u = 0; u < P::kUnits; ++u)
+        for (int v = 0; v < NV; ++v) {
+            if (v >= l.mine) continue;
+            const int c = l.col(v);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int c = VEC == 1 ? lane + 2 * u * p.T : (lane + u * p.T) * VEC + 2 * i;
-                const int c1 = VEC == 1 ? c + p.T : c + 1;
-                if (c < p.C) put(c, dg[u][i].x, db[u][i].x);
-                if (c1 < p.C) put(c1, dg[u][i].y, db[u][i].y);
+            for (int i = 0; i < H; ++i) {
+                put(c + 2 * i, dg[v][i].x, db[v][i].x);
+                put(c + 2 * i + 1, dg[v][i].y, db[v][i].y);
             }
+        }
+        if constexpr (SH) {
+            if (l.single >= 0) put(l.single, dg1, db1);
+        }
     };
     if (p.G == 1) {
         each([&](int c, float a, float b) {
@@ -667,29 +749,46 @@ __global__ void __launch_bounds__(ln_block(MODE, true), ln_per_sm(MODE, VEC * NV
         });
         return;
     }
-    // the rows of a warp, then the warps (or groups of warps) one after the other: a fixed order
-    if constexpr (!MULTI) {
-#pragma unroll
-        for (int u = 0; u < P::kUnits; ++u)
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                for (int o = p.T; o < 32; o <<= 1) {
-                    dg[u][i].x += __shfl_xor_sync(0xFFFFFFFFu, dg[u][i].x, o);
-                    dg[u][i].y += __shfl_xor_sync(0xFFFFFFFFu, dg[u][i].y, o);
-                    db[u][i].x += __shfl_xor_sync(0xFFFFFFFFu, db[u][i].x, o);
-                    db[u][i].y += __shfl_xor_sync(0xFFFFFFFFu, db[u][i].y, o);
-                }
-    }
     // every warp's (or group's) sums side by side, then a thread per column in a fixed order
     float* cols = reinterpret_cast<float*>(ring);
-    const int parts = MULTI ? p.G : ln_block(0, true) / 32;
+    const int parts = MULTI ? p.G : static_cast<int>(blockDim.x >> 5);
     float* own = cols + (MULTI ? group : threadIdx.x >> 5) * 2 * p.C;
     __syncthreads();   // the ring has been read
-    if (MULTI || (threadIdx.x & 31) < p.T)
-        each([&](int c, float a, float b) {
-            own[c] = a;
-            own[p.C + c] = b;
-        });
+    auto keep = [&](int c, float a, float b) {
+        own[c] = a;
+        own[p.C + c] = b;
+    };
+    if constexpr (MULTI) {
+        each(keep);
+    } else if constexpr (!SH) {
+        // the rows of a warp hold the same columns in the same lanes
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 0; i < H; ++i)
+                for (int o = p.T; o < 32; o <<= 1) {
+                    dg[v][i].x += __shfl_xor_sync(0xFFFFFFFFu, dg[v][i].x, o);
+                    dg[v][i].y += __shfl_xor_sync(0xFFFFFFFFu, dg[v][i].y, o);
+                    db[v][i].x += __shfl_xor_sync(0xFFFFFFFFu, db[v][i].x, o);
+                    db[v][i].y += __shfl_xor_sync(0xFFFFFFFFu, db[v][i].y, o);
+                }
+        if ((threadIdx.x & 31) < p.T) each(keep);
+    } else {
+        // they do not where rows start at different offsets: one row's threads after the other
+        const int turns = 32 / p.T, mine = (threadIdx.x & 31) / p.T;
+        for (int k = 0; k < turns; ++k) {
+            if (mine == k) {
+                if (k == 0)
+                    each(keep);
+                else
+                    each([&](int c, float a, float b) {
+                        own[c] += a;
+                        own[p.C + c] += b;
+                    });
+            }
+            __syncwarp();
+        }
+    }
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * p.C; c += blockDim.x) {
         float a = cols[c];
@@ -824,88 +923,96 @@ __global__ void __launch_bounds__(1024) ln_params_kernel(const float* __restrict
     }
 }
 
-// How a row of C elements is spread: vec elements per load, T threads, nv vectors per
-// thread, G rows per block; nv = 0 means the row does not fit and the looped kernels run.
-// blocks: the grid; ring.stages 0: one step per block, loaded directly.
+// How a row of C elements is spread: T threads, nv 16-byte vectors per thread, G rows per
+// block; sh: rows off the 16-byte grid; nv = 0 means the row does not fit and the looped
+// kernels run.  blocks: the grid; ring.stages 0: one step per block, loaded directly.
 struct LnPlan {
-    int vec, T, nv, G, blocks;
+    bool sh;
+    int T, nv, G, blocks;
     LnRing ring;
 };
 
 constexpr int kSms = 148;   // a B200; the partial count must not depend on the device asked
 
-// T is the least that holds the row at no more than ln_most elements per thread.  Where the
-// rows are too few to give every SM 768 threads, T grows until a thread has one vector (or
-// eight elements): the rows' latency is then all there is.
-// per_sm blocks share an SM and its shared memory; tensors: how many a stage holds.
-LnPlan ln_plan(int64_t M, int C, int ek, int tensors)
+LnPlan ln_plan(int64_t M, int C, int ek, bool backward)
 {
     const int es = ek == kF32 ? 4 : 2;
-    const int wide = 16 / es;
+    const int vec = 16 / es;
+    const int tensors = backward ? 2 : 1;
     LnPlan p{};
-    p.vec = C % wide == 0 ? wide : 1;
-    const int n = C / p.vec;
-    // vectors per thread the kernels are compiled for
-    static const int wide_nv[] = {1, 2, 3, 4, 6}, one_nv[] = {4, 8, 16, 16, 16};
-    const int* nvs = p.vec == 1 ? one_nv : wide_nv;
-    auto fit = [&](int T) {   // the least compiled count that holds the row on T threads
+    p.sh = C % vec != 0;
+    const int n = C >= vec ? C / vec : 1;   // whole vectors of a row (at most, off the grid)
+    static const int nvs[] = {1, 2, 3, 4, 6};   // vectors per thread the kernels are compiled for
+    auto fit = [&](int T, int most) {   // the least compiled count that holds the row on T threads
         const int need = (n + T - 1) / T;
-        for (int i = 0; i < 5; ++i)
-            if (nvs[i] >= need)
-                return nvs[i] * p.vec <= ln_most(ln_mode(T), p.vec == 1, ek == kF32, tensors > 1) ? nvs[i] : 0;
+        for (int nv : nvs)
+            if (nv >= need) return nv * vec <= most ? nv : 0;
         return 0;
     };
-    const int least = p.vec == 1 ? 8 : 1;
-    for (int T = 1; T <= kLnMaxMulti; T = T < 32 ? T * 2 : T + 32) {
-        const int nv = fit(T);
-        if (!nv) continue;
-        p.T = T;
-        p.nv = nv;
-        if (nv <= least || T >= 256 || M * T >= static_cast<int64_t>(kSms) * 768) break;
-    }
-    if (!p.nv) {
-        const int64_t cap = tensors == 1 ? 4 * kSms : 64;
-        p.blocks = static_cast<int>(M < cap ? M : cap);
-        return p;
-    }
-    p.G = p.T <= kLnBlock ? ln_block(ln_mode(p.T), tensors > 1) / p.T : 1;
+    // T is the least that holds the row at no more than ln_most elements per thread (a larger one
+    // of at most 128 where that leaves an eighth fewer vectors empty), or at 16
+    // where whole warps share it and that takes no more than 256 threads (9765 x 2048 bf16 with
+    // 16: 20 us forward, 36 backward; with 24: 25 and 46).  Where the rows are too few to give
+    // every SM 768 threads, T grows until a thread has one vector: the rows' latency is then
+    // all there is.  Rows off the grid have up to 2 (vec - 1) columns outside their vectors, a
+    // lane each.
+    const int least = p.sh ? 2 * vec : 1;
+    for (int pass = 0; pass < 2 && !p.nv; ++pass)
+        for (int T = least; T <= (pass ? kLnMaxMulti : kLnBlock); T = T < 32 ? T * 2 : T + 32) {
+            const int mode = ln_mode(T);
+            int most = ln_most(mode, p.sh, ek == kF32, backward);
+            if (mode == 1 && pass == 0 && most > 16) most = 16;
+            const int nv = fit(T, most);
+            if (!nv) continue;
+            const bool few = M * p.T < static_cast<int64_t>(kSms) * 768;
+            if (!p.nv || few || (T <= 128 && 8 * T * nv <= 7 * p.T * p.nv)) {
+                p.T = T;
+                p.nv = nv;
+            }
+            if (nv == 1 || T >= 256) break;
+        }
+    auto looped = [&] {
+        const int64_t cap = backward ? 64 : 4 * kSms;
+        LnPlan q{};
+        q.sh = p.sh;
+        q.blocks = static_cast<int>(M < cap ? M : cap);
+        return q;
+    };
+    if (!p.nv) return looped();
+    const int mode = ln_mode(p.T);
+    p.G = p.T <= kLnBlock ? ln_block(mode, backward, p.sh) / p.T : 1;
     const int64_t steps = (M + p.G - 1) / p.G;
     const int64_t row = static_cast<int64_t>(C) * es;
-    // chunks of about 12 KB a tensor, stages for a third of an SM's shared memory (half where
-    // threads hold column sums), two at least
-    const int per_sm = ln_per_sm(ln_mode(p.T), p.nv * p.vec, tensors > 1);
-    int k = static_cast<int>((tensors == 1 ? 16384 : 12288) / (row * p.G));
-    if (k < 1) k = 1;
+    // Chunks of about 12 KB a tensor (16 KB forward), as many stages as the SM's blocks have
+    // shared memory for, two at least.
+    int k = static_cast<int>((backward ? 12288 : 16384) / (row * p.G));
+    if (k < 1 || (p.sh && p.G % vec)) k = 1;
     p.ring.R = p.G * k;
     p.ring.pitch = static_cast<int>((p.ring.R * row + 32 + 15) / 16 * 16);
-    p.ring.stage = tensors * p.ring.pitch + (tensors > 1 ? (8 * p.ring.R + 15) / 16 * 16 : 0);
-    int blocks_per_sm = per_sm;
+    p.ring.stage = tensors * p.ring.pitch + (backward ? (8 * p.ring.R + 15) / 16 * 16 : 0);
+    // mode 1: 128 registers a thread, blocks of G*T threads
+    int per_sm = mode == 1 ? 512 / (p.G * p.T) : ln_per_sm(mode, p.nv * vec, backward, p.sh);
     int stages = 0;
-    for (; blocks_per_sm >= 1; --blocks_per_sm) {
-        stages = (220 * 1024 / blocks_per_sm - 4096 - ln_param_bytes(ln_mode(p.T), C, 3 - tensors)) / p.ring.stage;
+    for (; per_sm >= 1; --per_sm) {
+        stages = (220 * 1024 / per_sm - 4096 - ln_param_bytes(mode, p.sh, C, backward ? 1 : 2)) / p.ring.stage;
         if (stages >= 2) break;
     }
-    if (blocks_per_sm < 1) {   // not two stages: the looped kernels
-        p = LnPlan{};
-        p.vec = C % wide == 0 ? wide : 1;
-        const int64_t cap = tensors == 1 ? 4 * kSms : 64;
-        p.blocks = static_cast<int>(M < cap ? M : cap);
-        return p;
-    }
-    const int64_t grid = static_cast<int64_t>(kSms) * blocks_per_sm;
-    if (steps <= (tensors == 1 ? 2 * grid : grid)) {
+    if (per_sm < 1) return looped();
+    int64_t grid = static_cast<int64_t>(kSms) * per_sm;
+    if (steps <= (backward ? grid : 2 * grid)) {
         p.blocks = static_cast<int>(steps);
         p.ring.stages = 0;
         return p;
     }
+    // rows off the grid: the rows of a thread lie a multiple of vec apart, which G rows at a
+    // time give when G is one, and else a grid whose rows are one
+    if (p.sh && p.G % vec)
+        while (grid * p.G % vec) --grid;
     const int64_t chunks = (M + p.ring.R - 1) / p.ring.R;
     p.blocks = static_cast<int>(chunks < grid ? chunks : grid);
     p.ring.stages = stages < kMaxStages ? stages : kMaxStages;
     return p;
 }
-
-LnPlan ln_fwd_plan(int64_t M, int C, int ek) { return ln_plan(M, C, ek, 1); }
-LnPlan ln_bwd_plan(int64_t M, int C, int ek) { return ln_plan(M, C, ek, 2); }
 
 template <typename A>
 cudaError_t run_ln(void (*kern)(A), const A& a, const LnPlan& p, size_t param_bytes, size_t least_smem, cudaStream_t st)
@@ -920,110 +1027,103 @@ cudaError_t run_ln(void (*kern)(A), const A& a, const LnPlan& p, size_t param_by
                          dim3(static_cast<unsigned>(p.G * p.T)), smem, st, 1, a);
 }
 
-template <int EK, int VEC, int NV, int MODE>
-cudaError_t run_modes_fwd(const LnFwd& a, const LnPlan& p, cudaStream_t st)
-{
-    if constexpr (MODE > 2) {
-        return cudaErrorInvalidValue;
-    } else if constexpr (VEC * NV > ln_most(MODE, VEC == 1, EK == kF32, false)) {
-        return run_modes_fwd<EK, VEC, NV, MODE + 1>(a, p, st);   // ln_plan does not choose it
-    } else {
-        if (ln_mode(p.T) != MODE) return run_modes_fwd<EK, VEC, NV, MODE + 1>(a, p, st);
-        const size_t params = ln_param_bytes(MODE, a.C, 2);
-        return p.ring.stages ? run_ln(ln_fwd_kernel<EK, VEC, NV, MODE, true>, a, p, params, 0, st)
-                             : run_ln(ln_fwd_kernel<EK, VEC, NV, MODE, false>, a, p, params, 0, st);
-    }
-}
-
-template <int EK, int VEC, int NV>
+// Finds the compiled kernel of a plan: mode, vectors per thread, grid or not.
+template <int EK, int NV, int MODE, bool SH>
 cudaError_t run_fwd(const LnFwd& a, const LnPlan& p, cudaStream_t st)
 {
-    return run_modes_fwd<EK, VEC, NV, 0>(a, p, st);
-}
-
-template <int EK, int VEC, int NV, int MODE>
-cudaError_t run_modes_bwd(const LnBwd& a, const LnPlan& p, size_t cols, cudaStream_t st)
-{
     if constexpr (MODE > 2) {
         return cudaErrorInvalidValue;
-    } else if constexpr (VEC * NV > ln_most(MODE, VEC == 1, EK == kF32, true)) {
-        return run_modes_bwd<EK, VEC, NV, MODE + 1>(a, p, cols, st);   // ln_plan does not choose it
     } else {
-        if (ln_mode(p.T) != MODE) return run_modes_bwd<EK, VEC, NV, MODE + 1>(a, p, cols, st);
-        const size_t params = ln_param_bytes(MODE, a.C, 1);
-        return p.ring.stages ? run_ln(ln_bwd_kernel<EK, VEC, NV, MODE, true>, a, p, params, cols, st)
-                             : run_ln(ln_bwd_kernel<EK, VEC, NV, MODE, false>, a, p, params, cols, st);
+        if constexpr (16 / elem_bytes<EK>() * NV <= ln_most(MODE, SH, EK == kF32, false)) {
+            if (ln_mode(p.T) == MODE) {
+                const size_t params = ln_param_bytes(MODE, SH, a.C, 2);
+                return p.ring.stages ? run_ln(ln_fwd_kernel<EK, NV, MODE, true, SH>, a, p, params, 0, st)
+                                     : run_ln(ln_fwd_kernel<EK, NV, MODE, false, SH>, a, p, params, 0, st);
+            }
+        }
+        return run_fwd<EK, NV, MODE + 1, SH>(a, p, st);
     }
 }
 
-template <int EK, int VEC, int NV>
-cudaError_t run_bwd(const LnBwd& a, const LnPlan& p, cudaStream_t st)
+template <int EK, bool SH>
+cudaError_t pick_fwd(const LnFwd& a, const LnPlan& p, cudaStream_t st)
 {
-    const size_t cols = p.G == 1 || !a.part ? 0 : static_cast<size_t>(a.C) * 8 * (p.T > 32 ? p.G : ln_block(0, true) / 32);
-    return run_modes_bwd<EK, VEC, NV, 0>(a, p, cols, st);
+    switch (p.nv) {
+    case 1: return run_fwd<EK, 1, 0, SH>(a, p, st);
+    case 2: return run_fwd<EK, 2, 0, SH>(a, p, st);
+    case 3: return run_fwd<EK, 3, 0, SH>(a, p, st);
+    case 4: return run_fwd<EK, 4, 0, SH>(a, p, st);
+    default: return run_fwd<EK, 6, 0, SH>(a, p, st);
+    }
+}
+
+// Finds the compiled kernel of a plan: mode, vectors per thread, grid or not.
+template <int EK, int NV, int MODE, bool SH>
+cudaError_t run_bwd(const LnBwd& a, const LnPlan& p, size_t cols, cudaStream_t st)
+{
+    if constexpr (MODE > 2) {
+        return cudaErrorInvalidValue;
+    } else {
+        if constexpr (16 / elem_bytes<EK>() * NV <= ln_most(MODE, SH, EK == kF32, true)) {
+            if (ln_mode(p.T) == MODE) {
+                const size_t params = ln_param_bytes(MODE, SH, a.C, 1);
+                return p.ring.stages ? run_ln(ln_bwd_kernel<EK, NV, MODE, true, SH>, a, p, params, cols, st)
+                                     : run_ln(ln_bwd_kernel<EK, NV, MODE, false, SH>, a, p, params, cols, st);
+            }
+        }
+        return run_bwd<EK, NV, MODE + 1, SH>(a, p, cols, st);
+    }
+}
+
+template <int EK, bool SH>
+cudaError_t pick_bwd(const LnBwd& a, const LnPlan& p, size_t cols, cudaStream_t st)
+{
+    switch (p.nv) {
+    case 1: return run_bwd<EK, 1, 0, SH>(a, p, cols, st);
+    case 2: return run_bwd<EK, 2, 0, SH>(a, p, cols, st);
+    case 3: return run_bwd<EK, 3, 0, SH>(a, p, cols, st);
+    case 4: return run_bwd<EK, 4, 0, SH>(a, p, cols, st);
+    default: return run_bwd<EK, 6, 0, SH>(a, p, cols, st);
+    }
 }
 
 template <int EK>
 cudaError_t dispatch_fwd(const LnFwd& a, const LnPlan& p, cudaStream_t st)
 {
-    constexpr int W = EK == kF32 ? 4 : 8;
     if (p.nv == 0) {
-        auto kern = p.vec == 1 ? ln_fwd_loop_kernel<EK, 1> : ln_fwd_loop_kernel<EK, W>;
+        auto kern = p.sh ? ln_fwd_loop_kernel<EK, 1> : ln_fwd_loop_kernel<EK, 16 / elem_bytes<EK>()>;
         return launch_kernel(kern, dim3(static_cast<unsigned>(p.blocks)), dim3(kLnLoopThreads), 0, st, 1, a);
     }
-    if (p.vec == 1) {
-        switch (p.nv) {
-        case 4: return run_fwd<EK, 1, 4>(a, p, st);
-        case 8: return run_fwd<EK, 1, 8>(a, p, st);
-        default: return run_fwd<EK, 1, 16>(a, p, st);
-        }
-    }
-    switch (p.nv) {
-    case 1: return run_fwd<EK, W, 1>(a, p, st);
-    case 2: return run_fwd<EK, W, 2>(a, p, st);
-    case 3: return run_fwd<EK, W, 3>(a, p, st);
-    case 4: return run_fwd<EK, W, 4>(a, p, st);
-    default: return run_fwd<EK, W, 6>(a, p, st);
-    }
+    return p.sh ? pick_fwd<EK, true>(a, p, st) : pick_fwd<EK, false>(a, p, st);
 }
 
 template <int EK>
 cudaError_t dispatch_bwd(const LnBwd& a, const LnPlan& p, cudaStream_t st)
 {
-    constexpr int W = EK == kF32 ? 4 : 8;
+    constexpr int W = 16 / elem_bytes<EK>();
     if (p.nv == 0) {
-        cudaError_t e = cudaSuccess;
         if (a.part) {
-            auto cols = p.vec == 1 ? ln_cols_kernel<EK, 1> : ln_cols_kernel<EK, W>;
-            const int n = a.C / p.vec;
-            e = launch_kernel(cols, dim3((n + 255) / 256, a.blocks), dim3(256), 0, st, 1, a);
+            auto cols = p.sh ? ln_cols_kernel<EK, 1> : ln_cols_kernel<EK, W>;
+            const int n = p.sh ? a.C : a.C / W;
+            const cudaError_t e = launch_kernel(cols, dim3((n + 255) / 256, a.blocks), dim3(256), 0, st, 1, a);
             if (e != cudaSuccess) return e;
         }
-        auto kern = p.vec == 1 ? ln_bwd_loop_kernel<EK, 1> : ln_bwd_loop_kernel<EK, W>;
+        auto kern = p.sh ? ln_bwd_loop_kernel<EK, 1> : ln_bwd_loop_kernel<EK, W>;
         const int64_t most = 4 * kSms;
         return launch_kernel(kern, dim3(static_cast<unsigned>(a.M < most ? a.M : most)), dim3(kLnLoopThreads), 0, st,
                              1, a);
     }
-    if (p.vec == 1) {
-        switch (p.nv) {
-        case 4: return run_bwd<EK, 1, 4>(a, p, st);
-        case 8: return run_bwd<EK, 1, 8>(a, p, st);
-        default: return run_bwd<EK, 1, 16>(a, p, st);
-        }
-    }
-    switch (p.nv) {
-    case 1: return run_bwd<EK, W, 1>(a, p, st);
-    case 2: return run_bwd<EK, W, 2>(a, p, st);
-    case 3: return run_bwd<EK, W, 3>(a, p, st);
-    default: return run_bwd<EK, W, 4>(a, p, st);
-    }
+    // the block's column sums, one after the chunks
+    const size_t parts = p.T > 32 ? p.G : ln_block(0, true, p.sh) / 32;
+    const size_t cols = p.G == 1 || !a.part ? 0 : static_cast<size_t>(a.C) * 8 * parts;
+    return p.sh ? pick_bwd<EK, true>(a, p, cols, st) : pick_bwd<EK, false>(a, p, cols, st);
 }
 
 }  // namespace
 
 cudaError_t launch_layernorm_forward(const LnFwdArgs& a, cudaStream_t stream)
 {
-    const LnPlan p = ln_fwd_plan(a.M, static_cast<int>(a.C), a.ek);
+    const LnPlan p = ln_plan(a.M, static_cast<int>(a.C), a.ek, false);
     const LnFwd k{a.X, a.gamma, a.beta, a.Y, a.mean, a.rstd, a.M, static_cast<int>(a.C), p.T, p.G, a.eps, p.ring,
                   a.status};
     return a.ek == kF32 ? dispatch_fwd<kF32>(k, p, stream)
@@ -1032,14 +1132,14 @@ cudaError_t launch_layernorm_forward(const LnFwdArgs& a, cudaStream_t stream)
 
 size_t layernorm_backward_workspace_bytes(int64_t M, int64_t C, int ek)
 {
-    const LnPlan p = ln_bwd_plan(M, static_cast<int>(C), ek);
+    const LnPlan p = ln_plan(M, static_cast<int>(C), ek, true);
     return static_cast<size_t>(p.blocks) * 2 * static_cast<size_t>(C) * sizeof(float);
 }
 
 cudaError_t launch_layernorm_backward(const LnBwdArgs& a, cudaStream_t stream)
 {
     const bool params = a.dgamma || a.dbeta;
-    const LnPlan p = ln_bwd_plan(a.M, static_cast<int>(a.C), a.ek);
+    const LnPlan p = ln_plan(a.M, static_cast<int>(a.C), a.ek, true);
     const LnBwd k{a.dY, a.X, a.gamma, a.mean, a.rstd, a.dX, params ? a.ws : nullptr, a.M, static_cast<int>(a.C), p.T,
                   p.G, p.blocks, p.ring, a.status};
     cudaError_t e = a.ek == kF32 ? dispatch_bwd<kF32>(k, p, stream)

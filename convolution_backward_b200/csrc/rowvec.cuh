@@ -90,49 +90,26 @@ struct RowVec {
     }
 };
 
-// A thread's NV vectors of a row as pairs of fp32 (packed FP32 instructions take two
-// at a time): the vectors' elements in order, or for VEC == 1 elements 2i and 2i + 1.
-template <int EK, int VEC, int NV>
-struct RowPart {
-    static constexpr int kPairs = VEC * NV / 2;
-    static_assert(VEC * NV % 2 == 0, "whole pairs");
-    RowVec<EK, VEC> v[NV];
-
-    // Pairs of vector (VEC > 1) or element pair (VEC == 1) `i`: pairs [first, first + n).
-    static constexpr int kPer = VEC > 1 ? VEC / 2 : 1;      // pairs per unit
-    static constexpr int kUnits = kPairs / kPer;
-
-    __device__ __forceinline__ void unit(int u, float2 (&f)[kPer]) const
-    {
-        if constexpr (VEC == 1) {
-            float a[1], b[1];
-            v[2 * u].unpack(a);
-            v[2 * u + 1].unpack(b);
-            f[0] = make_float2(a[0], b[0]);
-        } else {
-            float a[VEC];
-            v[u].unpack(a);
+// A 16-byte vector's elements as pairs of fp32 (packed FP32 instructions take two at a time).
+template <int EK, int VEC>
+__device__ __forceinline__ void unpack_pairs(const RowVec<EK, VEC>& v, float2 (&f)[VEC / 2])
+{
+    float a[VEC];
+    v.unpack(a);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) f[i] = make_float2(a[2 * i], a[2 * i + 1]);
-        }
-    }
+    for (int i = 0; i < VEC / 2; ++i) f[i] = make_float2(a[2 * i], a[2 * i + 1]);
+}
 
-    __device__ __forceinline__ void set_unit(int u, const float2 (&f)[kPer])
-    {
-        if constexpr (VEC == 1) {
-            const float a[1] = {f[0].x}, b[1] = {f[0].y};
-            v[2 * u].pack(a);
-            v[2 * u + 1].pack(b);
-        } else {
-            float a[VEC];
+template <int EK, int VEC>
+__device__ __forceinline__ void pack_pairs(RowVec<EK, VEC>& v, const float2 (&f)[VEC / 2])
+{
+    float a[VEC];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                a[2 * i] = f[i].x;
-                a[2 * i + 1] = f[i].y;
-            }
-            v[u].pack(a);
-        }
+    for (int i = 0; i < VEC / 2; ++i) {
+        a[2 * i] = f[i].x;
+        a[2 * i + 1] = f[i].y;
     }
-};
+    v.pack(a);
+}
 
 }  // namespace dgrad

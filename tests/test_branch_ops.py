@@ -233,14 +233,15 @@ def _check_fwd(x, g, b, eps, dtype, y, mean, rstd, what):
 
 
 # sub-warp, one-warp and multi-warp rows, aligned and not, and rows too long for registers
-LN_C = [1, 7, 8, 40, 96, 100, 384, 768, 1001, 1024, 1032, 2056, 5000, 12296, 20001, 32776]
+LN_C = [1, 3, 7, 8, 13, 40, 57, 96, 100, 201, 384, 521, 768, 770, 1001, 1024, 1032, 1999, 2056, 2500, 4095, 5000, 5618,
+        8197, 11111, 12296, 20001, 32776]
 
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("C", LN_C)
 def test_layernorm_forward(C, dtype):
-    for M in (1, 37, 530) if C < 2000 else (1, 5):
+    for M in (1, 37, 2530) if C < 2000 else (1, 5, 700):
         x, g, b, _ = _ln_inputs(M, C, dtype, seed=C + M)
         if C == 1:
             b = b + 1
@@ -303,7 +304,7 @@ def _check_bwd(dy, x, g, mean, rstd, dtype, got, what):
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("C", LN_C)
 def test_layernorm_backward(C, dtype):
-    for M in (1, 37, 1200) if C < 2000 else (1, 5, 70):
+    for M in (1, 37, 1200) if C < 2000 else (1, 5, 70, 700) if C < 6000 else (1, 5, 320):
         x, g, b, dy = _ln_inputs(M, C, dtype, seed=C + M)
         _, mean, rstd = cb.layernorm_forward(x, g, b, eps=1e-5, stats=True)
         got = cb.layernorm_backward(dy, x, mean, rstd, g)
