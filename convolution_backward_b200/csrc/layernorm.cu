@@ -107,11 +107,12 @@ struct LnLane {
     // Column of vector v's first element.
     __device__ __forceinline__ int col(int v) const { return (SH ? head : 0) + (lane + v * T) * VEC; }
 
-    // Vector v, and the single column, of the row at p (zeros where there is none).
-    __device__ __forceinline__ void load(V& x, const void* p, int v) const
+    // Vector v (one of the first `have`), and the single column, of the row at p; zeros where
+    // there is none.
+    __device__ __forceinline__ void load(V& x, const void* p, int v, int have) const
     {
         x.zero();
-        if (v < mine) x.load(p, col(v));
+        if (v < have) x.load(p, col(v));
     }
     __device__ __forceinline__ float load_single(const void* p) const
     {
@@ -180,7 +181,7 @@ struct LnParam {
                         }
                         reg[v].pack(f);
                     } else {
-                        l.load(reg[v], src, v);
+                        l.load(reg[v], src, v, l.mine);
                     }
                 }
             }
@@ -459,13 +460,13 @@ __global__ void __launch_bounds__(ln_block(MODE, false, SH), ln_per_sm(MODE, 16 
     if constexpr (!REG) __syncthreads();
     // row m, read from `from`; every thread of the block takes part in each reduction
     auto one_row = [&](long long m, bool live, const void* from) {
+        const int have = live ? l.mine : 0;
         float2 f[NV][H];   // widened once: x, then x - mean
         float2 s = make_float2(0.f, 0.f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             typename L::V x;
-            x.zero();
-            if (live) l.load(x, from, v);
+            l.load(x, from, v, have);
             unpack_pairs(x, f[v]);
 #pragma unroll
             for (int i = 0; i < H; ++i) s = __fadd2_rn(s, f[v][i]);
@@ -641,15 +642,12 @@ __global__ void __launch_bounds__(ln_block(MODE, true, SH), ln_per_sm(MODE, 16 /
 #pragma unroll
         for (int i = 0; i < H; ++i) dg[v][i] = db[v][i] = make_float2(0.f, 0.f);
     auto one_row = [&](long long m, bool live, const void* fx, const void* fd, float mean, float rstd) {
+        const int have = live ? l.mine : 0;
         typename L::V x[NV], dy[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            x[v].zero();
-            dy[v].zero();
-            if (live) {
-                l.load(x[v], fx, v);
-                l.load(dy[v], fd, v);
-            }
+            l.load(x[v], fx, v, have);
+            l.load(dy[v], fd, v, have);
         }
         const float2 minus = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
         float2 sq = make_float2(0.f, 0.f), sqn = sq;
@@ -668,7 +666,7 @@ __global__ void __launch_bounds__(ln_block(MODE, true, SH), ln_per_sm(MODE, 16 /
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             // a dead row or column must add exactly nothing, whatever mean and rstd hold
-            if (!live || v >= l.mine) continue;
+            if (v >= have) continue;
             float2 n[H], d[H], g[H];
             unpack_pairs(x[v], n);
             unpack_pairs(dy[v], d);
