@@ -252,7 +252,7 @@ __host__ __device__ constexpr int ln_param_bytes(int mode, bool sh, int C, int c
 // where 16-bit pairs take half.
 constexpr int ln_most(int mode, bool sh, bool f32, bool backward)
 {
-    if (backward) return f32 ? 16 : 24;
+    if (backward) return mode == 2 ? (f32 ? 24 : 32) : f32 ? 16 : 24;
     if (!ln_param_regs(mode, sh)) return f32 ? 24 : 48;
     return f32 ? (mode == 1 ? 16 : 24) : mode == 2 ? 32 : 24;
 }
