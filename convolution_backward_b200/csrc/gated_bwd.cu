@@ -340,16 +340,32 @@ WgPlan wgrad_plan(int64_t M, int64_t N2, int64_t C)
     return p;
 }
 
-// dX runs split-K when its tiles would leave most SMs idle; the count is fixed by the sizes.
+// Splits of dX's sums over K = 2F (1: the SM-pair kernel with tiles of 256 rows).  Few rows
+// leave most pairs idle through a long K; the split-K kernel's 128 x 128 tiles then fill the
+// SMs.  The count is that of least estimated time, in tensor cycles: a k-block costs a tile
+// 512 (256 x 256 on a pair), 256 (256 x 128) or, 128 x 128 on one
+// SM, 520 (its 32 KB come at about 64 bytes a cycle); splits add
+// their fp32 partials' traffic (24 bytes a cycle and SM) and a launch (4000).  The whole
+// backward pass of 1024 rows, 768 to 2048 channels, took 37 us with the pair kernel and 30
+// with 3 splits; of 2048 to 5600 channels 101 with the pair kernel and 107 with 2 or 8.
 int dx_splits(int64_t M, int64_t K, int64_t C)
 {
-    const int64_t tiles = ((M + 127) / 128) * ((C + 127) / 128);
-    if (tiles * 4 > kSms) return 1;
-    int64_t s = kSms / tiles;
     const int64_t num_kb = (K + kBK - 1) / kBK;
-    if (s > num_kb / 2) s = num_kb / 2;
-    if (s > 32) s = 32;
-    return s < 1 ? 1 : static_cast<int>(s);
+    const int64_t bn = C > 128 ? 256 : 128;
+    const int64_t pair_tiles = ((M + 255) / 256) * ((C + bn - 1) / bn);
+    const int64_t pairs = kSms / 2;
+    int64_t best = (pair_tiles + pairs - 1) / pairs * num_kb * (2 * bn);
+    int count = 1;
+    const int64_t tiles = ((M + 127) / 128) * ((C + 127) / 128);
+    for (int64_t s = 2; s <= 32 && s <= num_kb / 2; ++s) {
+        const int64_t t = (tiles * s + kSms - 1) / kSms * ((num_kb + s - 1) / s) * 520 +
+                          s * M * C * 8 / (24 * kSms) + 4000;
+        if (t < best) {
+            best = t;
+            count = static_cast<int>(s);
+        }
+    }
+    return count;
 }
 
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }

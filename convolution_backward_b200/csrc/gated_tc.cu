@@ -18,8 +18,8 @@
 //               TMA store (H, and Z's two halves when the pre-activations are kept).
 // Two accumulators let a tile's epilogue run under the next tile's MMAs.
 //
-// gated_rows_kernel serves a handful of rows (single tokens): W is read once by plain
-// 16-byte loads, a warp per column of H.
+// gated_row_kernel (one row) and gated_rows_kernel (up to 32) serve single tokens: W's
+// bytes bound them, so W is read once, by plain 16-byte loads straight to registers.
 #include "common.cuh"
 #include "gate_act.cuh"
 #include "host_util.h"
@@ -289,11 +289,28 @@ __global__ void __launch_bounds__(GatedLayout<HN, ZK>::kThreads, 1)
     }
 }
 
-// A few rows: warp w of a block owns column f of H and reads rows f and F + f of W,
-// 16 bytes per lane and load; X comes from L1.  MR rows at a time (M <= MR).
-template <int MR, bool F16>
-__global__ void __launch_bounds__(256) gated_rows_kernel(const void* X, const void* W, uint16_t* H, uint16_t* Z, int M,
-                                                         int C, int F, int act, int* status)
+// H and (when Z is not null) Z of one element from its two sums.
+template <bool F16>
+__device__ __forceinline__ void gated_out(float g, float u, long long m, int f, uint16_t* H, uint16_t* Z, int M, int F,
+                                          int act, int* status)
+{
+    constexpr int EK = F16 ? kF16 : kBF16;
+    with_act(act, [&](auto which) {
+        const float h = gate_act<decltype(which)::value>(splat(g)).x * u;
+        uint16_t* at = H + m * F + f;
+        if (store_ok(H, 2LL * M * F, at, 2, status)) *at = static_cast<uint16_t>(float2_to_h16x2<EK>(h, 0.f));
+    });
+    if (Z) {
+        uint16_t* z = Z + 2 * m * F + f;
+        if (store_ok(Z, 4LL * M * F, z, 2, status)) z[0] = static_cast<uint16_t>(float2_to_h16x2<EK>(g, 0.f));
+        if (store_ok(Z, 4LL * M * F, z + F, 2, status)) z[F] = static_cast<uint16_t>(float2_to_h16x2<EK>(u, 0.f));
+    }
+}
+
+// One row: a warp owns column f of H and reads rows f and F + f of W.
+template <bool F16>
+__global__ void __launch_bounds__(256) gated_row_kernel(const void* X, const void* W, uint16_t* H, uint16_t* Z, int C,
+                                                        int F, int act, int* status)
 {
     constexpr int EK = F16 ? kF16 : kBF16;
     const int lane = threadIdx.x & 31;
@@ -304,51 +321,103 @@ __global__ void __launch_bounds__(256) gated_rows_kernel(const void* X, const vo
     pdl_wait();      // the previous kernel on the stream has finished
     pdl_trigger();   // the next one may start its set-up
     if (f >= F) return;
-    float g[MR], u[MR];
-#pragma unroll
-    for (int r = 0; r < MR; ++r) g[r] = u[r] = 0.f;
+    float2 g = make_float2(0.f, 0.f), u = g;
 #pragma unroll 4
     for (int v = lane; v < nv; v += 32) {
-        const uint4 a = wg[v], b = wu[v];
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+        const uint4 a = wg[v], b = wu[v], x = static_cast<const uint4*>(X)[v];
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w}, xw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int r = 0; r < MR; ++r) {
-            if (r < M) {
-                const uint4 x = static_cast<const uint4*>(X)[static_cast<long long>(r) * nv + v];
-                const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 xf = h16x2_to_float2<EK>(xw[i]);
-                    const float2 af = h16x2_to_float2<EK>(aw[i]), bf = h16x2_to_float2<EK>(bw[i]);
-                    g[r] = fmaf(xf.y, af.y, fmaf(xf.x, af.x, g[r]));
-                    u[r] = fmaf(xf.y, bf.y, fmaf(xf.x, bf.x, u[r]));
-                }
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float2 xf = h16x2_to_float2<EK>(xw[i]);
+            g = ffma2(xf, h16x2_to_float2<EK>(aw[i]), g);
+            u = ffma2(xf, h16x2_to_float2<EK>(bw[i]), u);
         }
     }
+    float gs = g.x + g.y, us = u.x + u.y;
 #pragma unroll
-    for (int r = 0; r < MR; ++r) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            g[r] += __shfl_xor_sync(0xFFFFFFFFu, g[r], o);
-            u[r] += __shfl_xor_sync(0xFFFFFFFFu, u[r], o);
-        }
+    for (int o = 16; o > 0; o >>= 1) {
+        gs += __shfl_xor_sync(0xFFFFFFFFu, gs, o);
+        us += __shfl_xor_sync(0xFFFFFFFFu, us, o);
     }
-    with_act(act, [&](auto which) {
+    if (lane == 0) gated_out<F16>(gs, us, 0, f, H, Z, 1, F, act, status);
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1)
+{
+    if constexpr (F16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Up to 8 NT rows: a block owns 16 columns of H, its eight warps split C.  W's 16 gate rows
+// and 16 other rows are the left operand of small tensor-core products whose right operand
+// is X: the products' order along C is free, so lane (g, t) takes eight consecutive elements
+// of W's rows g and g + 8 and of X's row g, 16 bytes each, and feeds four of them at a time
+// to two MMAs.  The warps' sums meet in shared memory in a fixed order.  Multiply-adds on
+// CUDA cores took 10.5 us at 8 rows, 768 to 2048 channels; this takes 3.3.
+template <int NT, bool F16>
+__global__ void __launch_bounds__(256) gated_rows_kernel(const void* X, const void* W, uint16_t* H, uint16_t* Z, int M,
+                                                         int C, int F, int act, int* status)
+{
+    __shared__ float part[8][2][NT * 8][17];   // [warp][gate, other][row of X][column]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int f0 = blockIdx.x * 16;
+    const int nv = C >> 3;                     // 16-byte vectors of a row
+    const uint4* Wv = static_cast<const uint4*>(W);
+    const uint4* Xv = static_cast<const uint4*>(X);
+    pdl_wait();
+    pdl_trigger();
+    float d[2][NT][4] = {};
+    const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll 2
+    for (int v0 = warp * 4; v0 < nv; v0 += 32) {
+        const int v = v0 + t;
+        const bool in = v < nv;
+        uint4 a[2][2], x[NT];
 #pragma unroll
-        for (int r = 0; r < MR; ++r) {
-            if (lane != r || r >= M) continue;
-            const long long at = static_cast<long long>(r) * F + f;
-            const float h = gate_act<decltype(which)::value>(splat(g[r])).x * u[r];
-            if (store_ok(H, 2LL * M * F, H + at, 2, status)) H[at] = static_cast<uint16_t>(float2_to_h16x2<EK>(h, 0.f));
-            if (Z) {
-                uint16_t* z = Z + 2LL * r * F + f;
-                if (store_ok(Z, 4LL * M * F, z, 2, status)) z[0] = static_cast<uint16_t>(float2_to_h16x2<EK>(g[r], 0.f));
-                if (store_ok(Z, 4LL * M * F, z + F, 2, status))
-                    z[F] = static_cast<uint16_t>(float2_to_h16x2<EK>(u[r], 0.f));
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int f = f0 + g + 8 * r;
+                a[p][r] = in && f < F ? Wv[static_cast<long long>(p * F + f) * nv + v] : none;
             }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[n] = in && n * 8 + g < M ? Xv[static_cast<long long>(n * 8 + g) * nv + v] : none;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma_16x8x16<F16>(d[p][n], a[p][0].x, a[p][1].x, a[p][0].y, a[p][1].y, x[n].x, x[n].y);
+                mma_16x8x16<F16>(d[p][n], a[p][0].z, a[p][1].z, a[p][0].w, a[p][1].w, x[n].z, x[n].w);
+            }
+    }
+    // the product's element (column g or g + 8 of H, row 2t or 2t + 1 of X)
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) part[warp][p][n * 8 + 2 * t + (e & 1)][g + 8 * (e >> 1)] = d[p][n][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < NT * 8 * 16; i += 256) {
+        const int r = i >> 4, c = i & 15;
+        if (r >= M || f0 + c >= F) continue;
+        float gs = 0.f, us = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            gs += part[w][0][r][c];
+            us += part[w][1][r][c];
         }
-    });
+        gated_out<F16>(gs, us, r, f0 + c, H, Z, M, F, act, status);
+    }
 }
 
 template <int HN, bool ZK, bool F16>
@@ -379,10 +448,10 @@ cudaError_t run_pair(const GatedArgs& a, cudaStream_t stream)
                          static_cast<int>(a.M), static_cast<int>(a.C), static_cast<int>(a.F), a.act, a.status);
 }
 
-template <int MR, bool F16>
+template <int NT, bool F16>
 cudaError_t run_rows(const GatedArgs& a, cudaStream_t stream)
 {
-    return launch_kernel(gated_rows_kernel<MR, F16>, dim3(static_cast<unsigned>((a.F + 7) / 8)), dim3(256), 0, stream,
+    return launch_kernel(gated_rows_kernel<NT, F16>, dim3(static_cast<unsigned>((a.F + 15) / 16)), dim3(256), 0, stream,
                          1, a.X, a.W, static_cast<uint16_t*>(a.H), static_cast<uint16_t*>(a.Z), static_cast<int>(a.M),
                          static_cast<int>(a.C), static_cast<int>(a.F), a.act, a.status);
 }
@@ -390,9 +459,13 @@ cudaError_t run_rows(const GatedArgs& a, cudaStream_t stream)
 template <bool F16>
 cudaError_t dispatch(const GatedArgs& a, cudaStream_t stream)
 {
-    if (a.M <= 1) return run_rows<1, F16>(a, stream);
-    if (a.M <= 4) return run_rows<4, F16>(a, stream);
-    if (a.M <= 8) return run_rows<8, F16>(a, stream);
+    if (a.M <= 1)
+        return launch_kernel(gated_row_kernel<F16>, dim3(static_cast<unsigned>((a.F + 7) / 8)), dim3(256), 0, stream, 1,
+                             a.X, a.W, static_cast<uint16_t*>(a.H), static_cast<uint16_t*>(a.Z), static_cast<int>(a.C),
+                             static_cast<int>(a.F), a.act, a.status);
+    if (a.M <= 8) return run_rows<1, F16>(a, stream);
+    if (a.M <= 16) return run_rows<2, F16>(a, stream);
+    if (a.M <= 32) return run_rows<4, F16>(a, stream);
     const int64_t wide = ((a.M + 255) / 256) * ((a.F + 127) / 128);
     if (2 * wide <= device_sm_count() / 2)
         return a.Z ? run_pair<64, true, F16>(a, stream) : run_pair<64, false, F16>(a, stream);

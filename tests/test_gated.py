@@ -186,8 +186,9 @@ def _check_forward(x, w, act, dtype, h, z, what):
     within(h, rh, u * np.abs(rh) + (1 + u) * 1.01 * eh + eta, what + " h")
 
 
-# rows kernel (up to 8 rows), narrow and wide tiles, ragged everywhere, more tiles than pairs
-SHAPES = [(1, 8, 8), (1, 768, 264), (3, 72, 40), (8, 136, 72), (9, 8, 8), (37, 72, 1000), (128, 64, 64),
+# rows kernels (up to 32 rows), narrow and wide tiles, ragged everywhere, more tiles than pairs
+SHAPES = [(1, 8, 8), (1, 768, 264), (2, 264, 8), (3, 72, 40), (8, 136, 72), (9, 8, 8), (16, 520, 24), (25, 776, 104),
+          (32, 40, 16), (33, 64, 48), (37, 72, 1000), (128, 64, 64),
           (257, 328, 264), (700, 200, 136), (2600, 136, 520), (5900, 72, 600)]
 
 
