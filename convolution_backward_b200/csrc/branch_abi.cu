@@ -45,6 +45,7 @@ dgrad_status_t done(cudaError_t e)
 }
 
 constexpr int64_t kMaxRows = 0x7FFFFFFFLL;
+constexpr int64_t kMaxGatedRows = INT64_C(1) << 30;   // rows rounded up to a tile stay within 32 bits
 constexpr int64_t kMaxChannels = 65536;
 
 dgrad_status_t ln_shape(int64_t M, int64_t C, dgrad_dtype_t dtype)
@@ -57,7 +58,7 @@ dgrad_status_t ln_shape(int64_t M, int64_t C, dgrad_dtype_t dtype)
 dgrad_status_t gated_shape(int64_t M, int64_t C, int64_t F)
 {
     if (M < 0 || C < 1 || F < 1) return DGRAD_ERR_INVALID;
-    if (M > kMaxRows || C > kMaxChannels || F > kMaxChannels / 2) return DGRAD_ERR_UNSUPPORTED;
+    if (M > kMaxGatedRows || C > kMaxChannels || F > kMaxChannels / 2) return DGRAD_ERR_UNSUPPORTED;
     if (C % 8 || F % 8) return DGRAD_ERR_ALIGNMENT;
     return DGRAD_OK;
 }

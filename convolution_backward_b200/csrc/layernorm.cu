@@ -948,27 +948,35 @@ LnPlan ln_plan(int64_t M, int C, int ek, bool backward)
         return 0;
     };
     // T is the least that holds the row at no more than ln_most elements per thread (a larger one
-    // of at most 128 where that leaves an eighth fewer vectors empty), or at 16
-    // where whole warps share it and that takes no more than 256 threads (9765 x 2048 bf16 with
-    // 16: 20 us forward, 36 backward; with 24: 25 and 46).  Where the rows are too few to give
-    // every SM 768 threads, T grows until a thread has one vector: the rows' latency is then
-    // all there is.  Rows off the grid have up to 2 (vec - 1) columns outside their vectors, a
-    // lane each.
+    // of at most 128 where that leaves an eighth fewer vectors empty), or at 16 where whole
+    // warps share it and that takes no more than 256 threads (9765 x 2048 bf16 with 16: 20 us
+    // forward, 36 backward; with 24: 25 and 46).  Rows off the grid have up to 2 (vec - 1)
+    // columns outside their vectors, a lane each.
     const int least = p.sh ? 2 * vec : 1;
+    const auto next = [](int T) { return T < 32 ? T * 2 : T + 32; };
+    const auto held = [&](int T, bool wide) {
+        const int mode = ln_mode(T);
+        const int most = ln_most(mode, p.sh, ek == kF32, backward);
+        return fit(T, mode == 1 && !wide && most > 16 ? 16 : most);
+    };
     for (int pass = 0; pass < 2 && !p.nv; ++pass)
-        for (int T = least; T <= (pass ? kLnMaxMulti : kLnBlock); T = T < 32 ? T * 2 : T + 32) {
-            const int mode = ln_mode(T);
-            int most = ln_most(mode, p.sh, ek == kF32, backward);
-            if (mode == 1 && pass == 0 && most > 16) most = 16;
-            const int nv = fit(T, most);
-            if (!nv) continue;
-            const bool few = M * p.T < static_cast<int64_t>(kSms) * 768;
-            if (!p.nv || few || (T <= 128 && 8 * T * nv <= 7 * p.T * p.nv)) {
+        for (int T = least; T <= (pass ? kLnMaxMulti : kLnBlock); T = next(T)) {
+            const int nv = held(T, pass > 0);
+            if (nv && (!p.nv || (T <= 128 && 8 * T * nv <= 7 * p.T * p.nv))) {
                 p.T = T;
                 p.nv = nv;
             }
-            if (nv == 1 || T >= 256) break;
         }
+    // Rows too few to give every SM 512 threads take more threads each, down to one vector: their
+    // latency is then all there is (256 x 768 bf16: 2.6 us forward, 6.2 backward; without 3.9
+    // and 7.7).
+    for (int T = next(p.T); p.nv > 1 && T <= kLnBlock && M * p.T < static_cast<int64_t>(kSms) * 512; T = next(T)) {
+        const int nv = held(T, true);
+        if (nv && nv < p.nv) {
+            p.T = T;
+            p.nv = nv;
+        }
+    }
     auto looped = [&] {
         const int64_t cap = backward ? 64 : 4 * kSms;
         LnPlan q{};
@@ -996,6 +1004,8 @@ LnPlan ln_plan(int64_t M, int C, int ek, bool backward)
         if (stages >= 2) break;
     }
     if (per_sm < 1) return looped();
+    // One step per block (forward: two blocks' worth): direct loads (256 x 768 bf16: 2.6 us forward,
+    // 6.2 backward; through the ring 6.0 and 6.9).
     int64_t grid = static_cast<int64_t>(kSms) * per_sm;
     if (steps <= (backward ? grid : 2 * grid)) {
         p.blocks = static_cast<int>(steps);

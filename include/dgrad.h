@@ -267,7 +267,7 @@ typedef enum {
  * accumulators.  Z [M][2F], rounded to the element type, is what the backward pass
  * takes; null: not kept.  DGRAD_BF16 or DGRAD_F16 (else DGRAD_ERR_UNSUPPORTED) on the
  * tcgen05 tensor cores; up to 32 rows run on kernels that stream W once.  C and F
- * multiples of 8 (else DGRAD_ERR_ALIGNMENT); C <= 65536, F <= 32768, M < 2^31 (else
+ * multiples of 8 (else DGRAD_ERR_ALIGNMENT); C <= 65536, F <= 32768, M <= 2^30 (else
  * DGRAD_ERR_UNSUPPORTED).  H and Z overlap nothing. */
 dgrad_status_t dgrad_gated_forward(int64_t M, int64_t C, int64_t F, dgrad_dtype_t dtype, dgrad_act_t act,
                                    const void* X, const void* W, void* H, void* Z, void* stream);

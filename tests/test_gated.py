@@ -90,7 +90,7 @@ def test_forward_refusals():
     assert _fwd(C=0) == INVALID
     assert _fwd(C=65544) == UNSUPPORTED
     assert _fwd(F=32776) == UNSUPPORTED
-    assert _fwd(M=1 << 31) == UNSUPPORTED
+    assert _fwd(M=(1 << 30) + 1) == UNSUPPORTED
     assert _fwd(C=60) == ALIGNMENT
     assert _fwd(F=36) == ALIGNMENT
     for name in ("X", "W", "H"):
