@@ -35,6 +35,8 @@
 // column sums in registers, writes them once as fp32 partials [block][2][C], and
 // a second kernel adds the partials of a column in a fixed order: no atomics, so
 // results repeat bit for bit.
+#include <type_traits>
+
 #include "common.cuh"
 #include "host_util.h"
 #include "launchers.h"
@@ -724,27 +726,46 @@ __global__ void __launch_bounds__(ln_block(MODE, true, SH), ln_per_sm(MODE, 16 /
     if (!p.part) return;
     float* out = p.part + static_cast<long long>(blockIdx.x) * 2 * p.C;
     const long long part_bytes = static_cast<long long>(p.blocks) * 2 * p.C * 4;
-    // `put` gets every column this thread holds, with its two sums
-    auto each = [&](auto put) {
+    // This thread's columns to dst [2][C]; ADD: added to what is there.  checked: the partials.
+    auto put = [&](float* dst, auto add, bool checked) {
+        constexpr bool ADD = decltype(add)::value;
+        auto one = [&](int c, float v) {
+            if (!checked || store_ok(p.part, part_bytes, dst + c, 4, p.status)) dst[c] = ADD ? dst[c] + v : v;
+        };
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             if (v >= l.mine) continue;
             const int c = l.col(v);
+            if constexpr (!SH && !ADD) {   // whole quarters, 16 bytes each
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                put(c + 2 * i, dg[v][i].x, db[v][i].x);
-                put(c + 2 * i + 1, dg[v][i].y, db[v][i].y);
+                for (int i = 0; i < H; i += 2) {
+                    float* at = dst + c + 2 * i;
+                    if (checked && !(store_ok(p.part, part_bytes, at, 16, p.status) &&
+                                     store_ok(p.part, part_bytes, at + p.C, 16, p.status)))
+                        continue;
+                    *reinterpret_cast<float4*>(at) = make_float4(dg[v][i].x, dg[v][i].y, dg[v][i + 1].x, dg[v][i + 1].y);
+                    *reinterpret_cast<float4*>(at + p.C) =
+                        make_float4(db[v][i].x, db[v][i].y, db[v][i + 1].x, db[v][i + 1].y);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    one(c + 2 * i, dg[v][i].x);
+                    one(c + 2 * i + 1, dg[v][i].y);
+                    one(p.C + c + 2 * i, db[v][i].x);
+                    one(p.C + c + 2 * i + 1, db[v][i].y);
+                }
             }
         }
         if constexpr (SH) {
-            if (l.single >= 0) put(l.single, dg1, db1);
+            if (l.single >= 0) {
+                one(l.single, dg1);
+                one(p.C + l.single, db1);
+            }
         }
     };
-    if (p.G == 1) {
-        each([&](int c, float a, float b) {
-            if (store_ok(p.part, part_bytes, out + c, 4, p.status)) out[c] = a;
-            if (store_ok(p.part, part_bytes, out + p.C + c, 4, p.status)) out[p.C + c] = b;
-        });
+    if (!SH && p.G == 1) {   // (off the grid the columns go through shared memory, to leave in whole lines)
+        put(out, std::false_type{}, true);
         return;
     }
     // every warp's (or group's) sums side by side, then a thread per column in a fixed order
@@ -752,12 +773,8 @@ __global__ void __launch_bounds__(ln_block(MODE, true, SH), ln_per_sm(MODE, 16 /
     const int parts = MULTI ? p.G : static_cast<int>(blockDim.x >> 5);
     float* own = cols + (MULTI ? group : threadIdx.x >> 5) * 2 * p.C;
     __syncthreads();   // the ring has been read
-    auto keep = [&](int c, float a, float b) {
-        own[c] = a;
-        own[p.C + c] = b;
-    };
     if constexpr (MULTI) {
-        each(keep);
+        put(own, std::false_type{}, false);
     } else if constexpr (!SH) {
         // the rows of a warp hold the same columns in the same lanes
 #pragma unroll
@@ -770,19 +787,16 @@ __global__ void __launch_bounds__(ln_block(MODE, true, SH), ln_per_sm(MODE, 16 /
                     db[v][i].x += __shfl_xor_sync(0xFFFFFFFFu, db[v][i].x, o);
                     db[v][i].y += __shfl_xor_sync(0xFFFFFFFFu, db[v][i].y, o);
                 }
-        if ((threadIdx.x & 31) < p.T) each(keep);
+        if ((threadIdx.x & 31) < p.T) put(own, std::false_type{}, false);
     } else {
         // they do not where rows start at different offsets: one row's threads after the other
         const int turns = 32 / p.T, mine = (threadIdx.x & 31) / p.T;
         for (int k = 0; k < turns; ++k) {
             if (mine == k) {
                 if (k == 0)
-                    each(keep);
+                    put(own, std::false_type{}, false);
                 else
-                    each([&](int c, float a, float b) {
-                        own[c] += a;
-                        own[p.C + c] += b;
-                    });
+                    put(own, std::true_type{}, false);
             }
             __syncwarp();
         }
@@ -1123,7 +1137,7 @@ cudaError_t dispatch_bwd(const LnBwd& a, const LnPlan& p, cudaStream_t st)
     }
     // the block's column sums, one after the chunks
     const size_t parts = p.T > 32 ? p.G : ln_block(0, true, p.sh) / 32;
-    const size_t cols = p.G == 1 || !a.part ? 0 : static_cast<size_t>(a.C) * 8 * parts;
+    const size_t cols = (p.G == 1 && !p.sh) || !a.part ? 0 : static_cast<size_t>(a.C) * 8 * parts;
     return p.sh ? pick_bwd<EK, true>(a, p, cols, st) : pick_bwd<EK, false>(a, p, cols, st);
 }
 

@@ -403,3 +403,68 @@ def test_dropout_rate():
     for seed in range(4):
         kept = int((cb.dropout_forward(x, 0.3, seed) != 0).sum())
         assert abs(kept - 0.7 * n) < 5 * (n * 0.21) ** 0.5
+
+
+# ------------------------------------------------- the debug build, streams, graphs
+
+@pytest.fixture
+def debug_library(monkeypatch):
+    import os
+    path = os.path.join(os.path.dirname(cb.library_path()), "libdgrad_debug.so")
+    if not os.path.exists(path):
+        pytest.skip("libdgrad_debug.so not built")
+    monkeypatch.setattr(cb, "_LIB_PATH", path)
+    monkeypatch.setattr(cb, "_lib", None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", [(9, 13), (700, 96), (1500, 201), (1200, 770), (90, 4095), (3, 12296), (5, 32776)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_every_store_in_bounds(shape, dtype, debug_library):
+    """The debug build checks every hand-indexed store against its buffer."""
+    M, C = shape
+    x, g, b, dy = _ln_inputs(M, C, dtype, seed=C)
+    y, mean, rstd = cb.layernorm_forward(x, g, b, eps=1e-5, stats=True)
+    got = cb.layernorm_backward(dy, x, mean, rstd, g)
+    d = cb.dropout_forward(x, 0.3, 11, 2, residual=dy)
+    cb.check_status()
+    _check_fwd(x, g, b, 1e-5, dtype, y, mean, rstd, "debug")
+    _check_bwd(dy, x, g, mean, rstd, dtype, got, "debug")
+    _check_drop(x, dy, 0.3, 11, 2, dtype, d, "debug")
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once():
+    """The same operators on two streams at the same time, each with its own tensors."""
+    a, b = _ln_inputs(5000, 768, "bf16", 1), _ln_inputs(3000, 1001, "f32", 2)
+
+    def step(t, stream=None):
+        x, g, be, dy = t
+        y, m, r = cb.layernorm_forward(x, g, be, stats=True, stream=stream)
+        z = cb.dropout_forward(y, 0.1, 3, 4, residual=x, stream=stream)
+        return (z, *cb.layernorm_backward(dy, x, m, r, g, stream=stream))
+
+    want = [[t.clone() for t in step(k)] for k in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        got = [step(k, s) for k, s in zip((a, b), streams)]
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    for o, w in zip(got, want):
+        assert all(torch.equal(p, q) for p, q in zip(o, w))
+    cb.check_status()
+
+
+@pytest.mark.gpu
+def test_stream_of_another_device_is_refused():
+    class Other:
+        device = torch.device("cuda", 7)
+        cuda_stream = 0
+
+    with pytest.raises(ValueError, match="stream"):
+        cb.layernorm_forward(torch.zeros(4, 8, device="cuda"), stream=Other())
+    with pytest.raises(ValueError, match="stream"):
+        cb.dropout_backward(torch.zeros(4, 8, device="cuda"), 0.1, 1, stream=Other())

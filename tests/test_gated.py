@@ -375,3 +375,23 @@ def test_branch_on_another_stream_and_in_graphs():
     for o, wv in zip(outs, want):
         assert all(torch.equal(p, q) for p, q in zip(o, wv))
     cb.check_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", [(1, 72, 40), (7, 136, 72), (30, 264, 24), (300, 200, 136)], ids=lambda s: "x".join(map(str, s)))
+def test_every_store_in_bounds(shape, dtype, monkeypatch):
+    """The debug build checks every hand-indexed store against its buffer."""
+    import os
+    path = os.path.join(os.path.dirname(cb.library_path()), "libdgrad_debug.so")
+    if not os.path.exists(path):
+        pytest.skip("libdgrad_debug.so not built")
+    monkeypatch.setattr(cb, "_LIB_PATH", path)
+    monkeypatch.setattr(cb, "_lib", None)
+    M, C, F = shape
+    x, w, dh = _inputs(M, C, F, dtype, seed=M)
+    h, z = cb.gated_forward(x, w, preact=True)
+    dx, dw = cb.gated_backward(dh, x, z, w)
+    cb.check_status()
+    _check_forward(x, w, "silu", dtype, h, z, "debug")
+    _check_backward(dh, x, z, w, "silu", dtype, dx, dw, "debug")
