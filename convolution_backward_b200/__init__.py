@@ -10,8 +10,12 @@ calls raise ``DgradUnavailable``.
     dX = pointwise(dY, W)                          # dY (N,H,W,K), W (K,C) -> (N,H,W,C)
     dX = depthwise(dY, W, H=H, W=W_, stride=1, pad_h=1, pad_w=1)   # W (KH,KW,C)
 
-Tensors are NHWC and contiguous; float32 or bfloat16 (bf16 in, bf16 out,
-fp32 accumulate).
+    Y, mean, rstd = layernorm_forward(X, gamma, beta, stats=True)  # X (..., C)
+    H, Z = gated_forward(X, W, act="silu", preact=True)            # W (2F, C) -> (..., F), (..., 2F)
+    Y = dropout_forward(X, p, seed, offset, residual=R)
+
+and their ``_backward`` counterparts.  Tensors are NHWC (rows of channels) and contiguous;
+float32, bfloat16 or float16 (16-bit in, 16-bit out, fp32 accumulate).
 """
 from __future__ import annotations
 

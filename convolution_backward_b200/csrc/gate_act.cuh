@@ -13,10 +13,9 @@
 // polynomial of degree 8 fitted to log2(erfcx(|g|/sqrt 2)/(2t)) by weighted least squares
 // on Chebyshev nodes (relative error 1.5e-7; 8e-7 with fp32 rounding for |g| < 4).
 // ex2 and rcp are the hardware's approximations (about 2^-22), far below a 16-bit
-// result's half step.  An epilogue of 64 elements a thread spent more time in the
-// general-purpose exp, division and erfc than the tensor cores in the tile: 32768 rows,
-// 768 to 2048 channels, bf16 silu took 149 us with those and 126 us with these forms,
-// gelu 203 and 133 us.
+// result's half step.  With the general-purpose exp, division and erfc the epilogue took
+// longer than the tile's MMAs: 32768 rows, 768 to 2048 channels, bf16 silu 149 us, gelu
+// 203; with these forms 144 and 155.
 #pragma once
 
 #include <type_traits>

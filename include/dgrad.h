@@ -69,7 +69,8 @@ typedef struct {
  * every entry point: dgrad_pointwise, its split-K variants, dgrad_dense,
  * dgrad_grouped and dgrad_depthwise_tc run tcgen05 MMAs on f16 operands with
  * fp32 accumulation; dgrad_depthwise widens f16 to fp32 on load and uses fp32
- * FMAs.  DGRAD_F32 is served by dgrad_pointwise and dgrad_depthwise only. */
+ * FMAs.  DGRAD_F32 is served by dgrad_pointwise, dgrad_depthwise, layer norm and
+ * dropout only. */
 typedef enum { DGRAD_F32 = 0, DGRAD_BF16 = 1, DGRAD_F16 = 2 } dgrad_dtype_t;
 
 /* Depthwise kernel choice.  AUTO: rotated-filter for stride 1, row-streaming
