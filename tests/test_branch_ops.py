@@ -338,6 +338,50 @@ def test_layernorm_backward_variants(C, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", [(9000, 96), (7001, 201), (2500, 1001), (700, 4100)], ids=lambda s: "x".join(map(str, s)))
+def test_layernorm_in_place_many_rows(shape, dtype):
+    """Rows in flight for the next steps are not disturbed by results written over their tensor."""
+    M, C = shape
+    x, g, b, dy = _ln_inputs(M, C, dtype, seed=M)
+    want = cb.layernorm_forward(x, g, b, stats=True)
+    z = x.clone()
+    got = cb.layernorm_forward(z, g, b, stats=True, out=z)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    grads = cb.layernorm_backward(dy, x, want[1], want[2], g)
+    for which in (0, 1):
+        d, z = dy.clone(), x.clone()
+        got = cb.layernorm_backward(d, z, want[1], want[2], g, out=d if which == 0 else z)
+        assert all(torch.equal(p, q) for p, q in zip(got, grads))
+    cb.check_status()
+
+
+@pytest.mark.gpu
+def test_layernorm_gradient_by_differences():
+    """Central differences of the fp32 forward along a direction v, step h = 2^-5, against <dX, v>.
+    The step's own error is h^2/6 times the third derivative along v, below 40 in size here
+    (|v| = 1 per element, the row's spread near 1, three powers of it and constants up to 6
+    with sum(dY) weights of 1/sqrt(C)); the forward's rounding enters as 2e sqrt(M C)|y|/h."""
+    M, C = 64, 384
+    x, g, b, dy = _ln_inputs(M, C, "f32", seed=21, offset=0.0)
+    x = x / x.std()
+    v = torch.randn(M, C, generator=torch.Generator(device="cuda").manual_seed(5), device="cuda")
+    h = 2.0 ** -5
+    _, mean, rstd = cb.layernorm_forward(x, g, b, eps=1e-5, stats=True)
+    dx, dg, db = cb.layernorm_backward(dy, x, mean, rstd, g)
+    loss = lambda t, gg=g, bb=b: (cb.layernorm_forward(t, gg, bb, eps=1e-5).double() * dy.double()).sum()
+    scale = float((dx.double() * v.double()).norm())
+    assert abs(float((loss(x + h * v) - loss(x - h * v)) / (2 * h) - (dx.double() * v.double()).sum())) \
+        <= 40 / 6 * h * h * scale + 4 * E32 * (M * C) ** 0.5 * 8 / h
+    # the parameters enter linearly: only rounding is left
+    w = v[0].contiguous()
+    assert abs(float((loss(x, g + h * w) - loss(x, g - h * w)) / (2 * h) - (dg.double() * w.double()).sum())) \
+        <= 4 * E32 * (M * C) ** 0.5 * 8 / h
+    assert abs(float((loss(x, g, b + h * w) - loss(x, g, b - h * w)) / (2 * h) - (db.double() * w.double()).sum())) \
+        <= 4 * E32 * (M * C) ** 0.5 * 8 / h
+
+
+@pytest.mark.gpu
 def test_layernorm_empty_and_edges():
     x = torch.empty(0, 24, device="cuda")
     s = torch.empty(0, device="cuda")

@@ -292,6 +292,28 @@ def test_backward_workspace_and_empty():
     assert dx.shape == (0, 136) and dw.shape == w.shape and not dw.any()
 
 
+@pytest.mark.gpu
+def test_one_workspace_in_two_graphs():
+    """Two captured backward passes of different sizes that share a workspace, replayed in turn."""
+    cases = [_inputs(1500, 136, 264, "bf16", seed=1), _inputs(90, 264, 40, "f16", seed=2)]
+    zs = [cb.gated_forward(x, w, preact=True)[1] for x, w, _ in cases]
+    want = [[t.clone() for t in cb.gated_backward(dh, x, z, w)] for (x, w, dh), z in zip(cases, zs)]
+    nb = max(cb.gated_backward_workspace_bytes(x.shape[0], x.shape[1], w.shape[0] // 2) for x, w, _ in cases)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for (x, w, dh), z in zip(cases, zs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(cb.gated_backward(dh, x, z, w, workspace=ws))
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    for o, wv in zip(outs, want):
+        assert all(torch.equal(p, q) for p, q in zip(o, wv))
+    cb.check_status()
+
+
 # ------------------------------------------------------------- the whole branch
 
 class Branch:
