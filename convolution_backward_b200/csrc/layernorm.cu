@@ -233,10 +233,17 @@ constexpr int ln_block(int mode, bool backward, bool sh)
     return mode == 2 ? kLnMaxMulti : mode == 0 && backward && !sh ? 128 : kLnBlock;
 }
 
-// Blocks an SM holds, by the registers their elements take.
-constexpr int ln_per_sm(int mode, int elems, bool backward, bool sh)
+// Threads an SM holds (of ln_block a block), by the registers their elements take.  768 where
+// up to 16 elements, or 16-bit parameters beside them, leave 80 registers (9765 x 2048 bf16
+// forward: 20 us, with 512 threads 23); else 512, or one block of up to 384.
+constexpr int ln_threads(int mode, int elems, bool backward, bool sh, bool f32)
 {
-    return mode == 2 ? 1 : mode == 0 && backward && !sh ? 4 : mode == 0 && elems <= 16 && !backward && !sh ? 3 : 2;
+    if (mode == 2) return kLnMaxMulti;
+    return !backward && elems <= 16 && !sh && (mode == 0 || !f32) ? 768 : 512;
+}
+constexpr int ln_per_sm(int mode, int elems, bool backward, bool sh, bool f32)
+{
+    return ln_threads(mode, elems, backward, sh, f32) / ln_block(mode, backward, sh);
 }
 
 // Rows on the 16-byte grid of at most a warp keep their parameters in shared memory.
@@ -428,7 +435,7 @@ struct LnFwd {
 };
 
 template <int EK, int NV, int MODE, bool RING, bool SH>
-__global__ void __launch_bounds__(ln_block(MODE, false, SH), ln_per_sm(MODE, 16 / elem_bytes<EK>() * NV, false, SH))
+__global__ void __launch_bounds__(ln_block(MODE, false, SH), ln_per_sm(MODE, 16 / elem_bytes<EK>() * NV, false, SH, EK == kF32))
     ln_fwd_kernel(const LnFwd p)
 {
     constexpr int es = elem_bytes<EK>();
@@ -608,7 +615,7 @@ struct LnBwd {
 };
 
 template <int EK, int NV, int MODE, bool RING, bool SH>
-__global__ void __launch_bounds__(ln_block(MODE, true, SH), ln_per_sm(MODE, 16 / elem_bytes<EK>() * NV, true, SH))
+__global__ void __launch_bounds__(ln_block(MODE, true, SH), ln_per_sm(MODE, 16 / elem_bytes<EK>() * NV, true, SH, EK == kF32))
     ln_bwd_kernel(const LnBwd p)
 {
     constexpr int es = elem_bytes<EK>();
@@ -1010,8 +1017,7 @@ LnPlan ln_plan(int64_t M, int C, int ek, bool backward)
     p.ring.R = p.G * k;
     p.ring.pitch = static_cast<int>((p.ring.R * row + 32 + 15) / 16 * 16);
     p.ring.stage = tensors * p.ring.pitch + (backward ? (8 * p.ring.R + 15) / 16 * 16 : 0);
-    // mode 1: 128 registers a thread, blocks of G*T threads
-    int per_sm = mode == 1 ? 512 / (p.G * p.T) : ln_per_sm(mode, p.nv * vec, backward, p.sh);
+    int per_sm = mode == 2 ? 1 : ln_threads(mode, p.nv * vec, backward, p.sh, ek == kF32) / (p.G * p.T);
     int stages = 0;
     for (; per_sm >= 1; --per_sm) {
         stages = (220 * 1024 / per_sm - 4096 - ln_param_bytes(mode, p.sh, C, backward ? 1 : 2)) / p.ring.stage;
