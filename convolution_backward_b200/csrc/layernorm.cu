@@ -234,8 +234,8 @@ constexpr int ln_block(int mode, bool backward, bool sh)
 }
 
 // Threads an SM holds (of ln_block a block), by the registers their elements take.  768 where
-// up to 16 elements, or 16-bit parameters beside them, leave 80 registers (9765 x 2048 bf16
-// forward: 20 us, with 512 threads 23); else 512, or one block of up to 384.
+// up to 16 elements, with 16-bit parameters beside them or none, leave 80 registers (4882 x
+// 4096 bf16 forward: 22.3 us, with 512 threads 24.0); else 512, or one block of up to 384.
 constexpr int ln_threads(int mode, int elems, bool backward, bool sh, bool f32)
 {
     if (mode == 2) return kLnMaxMulti;
@@ -255,14 +255,14 @@ __host__ __device__ constexpr int ln_param_bytes(int mode, bool sh, int C, int c
     return ln_param_regs(mode, sh) ? 0 : (count * C * 4 + 15) / 16 * 16;
 }
 
-// Elements per thread that fit its registers without spills.  Forward: 48 where the
-// parameters are in shared memory, 24 or (one block per SM) 32 beside them.  Backward: the
+// Elements per thread that fit its registers without spills (but for a few words).  Forward: 64
+// where the parameters are in shared memory, 24 or (one block per SM) 32 beside them.  Backward: the
 // column sums take two registers per element.  fp32 takes a register for every element
 // where 16-bit pairs take half.
 constexpr int ln_most(int mode, bool sh, bool f32, bool backward)
 {
     if (backward) return mode == 2 ? (f32 ? 24 : 32) : f32 ? 16 : 24;
-    if (!ln_param_regs(mode, sh)) return f32 ? 24 : 48;
+    if (!ln_param_regs(mode, sh)) return f32 ? 32 : 64;
     return f32 ? (mode == 1 ? 16 : 24) : mode == 2 ? 32 : 24;
 }
 
@@ -961,7 +961,7 @@ LnPlan ln_plan(int64_t M, int C, int ek, bool backward)
     LnPlan p{};
     p.sh = C % vec != 0;
     const int n = C >= vec ? C / vec : 1;   // whole vectors of a row (at most, off the grid)
-    static const int nvs[] = {1, 2, 3, 4, 6};   // vectors per thread the kernels are compiled for
+    static const int nvs[] = {1, 2, 3, 4, 6, 8};   // vectors per thread the kernels are compiled for
     auto fit = [&](int T, int most) {   // the least compiled count that holds the row on T threads
         const int need = (n + T - 1) / T;
         for (int nv : nvs)
@@ -970,8 +970,8 @@ LnPlan ln_plan(int64_t M, int C, int ek, bool backward)
     };
     // T is the least that holds the row at no more than ln_most elements per thread (a larger one
     // of at most 128 where that leaves an eighth fewer vectors empty), or at 16 where whole
-    // warps share it and that takes no more than 256 threads (9765 x 2048 bf16 with 16: 20 us
-    // forward, 36 backward; with 24: 25 and 46).  Rows off the grid have up to 2 (vec - 1)
+    // warps share it and that takes no more than 256 threads (9765 x 2048 bf16 backward: 36 us
+    // with 16, 46 with 24).  Rows off the grid have up to 2 (vec - 1)
     // columns outside their vectors, a lane each.
     const int least = p.sh ? 2 * vec : 1;
     const auto next = [](int T) { return T < 32 ? T * 2 : T + 32; };
@@ -1081,7 +1081,8 @@ cudaError_t pick_fwd(const LnFwd& a, const LnPlan& p, cudaStream_t st)
     case 2: return run_fwd<EK, 2, 0, SH>(a, p, st);
     case 3: return run_fwd<EK, 3, 0, SH>(a, p, st);
     case 4: return run_fwd<EK, 4, 0, SH>(a, p, st);
-    default: return run_fwd<EK, 6, 0, SH>(a, p, st);
+    case 6: return run_fwd<EK, 6, 0, SH>(a, p, st);
+    default: return run_fwd<EK, 8, 0, SH>(a, p, st);
     }
 }
 

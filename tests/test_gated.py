@@ -114,7 +114,9 @@ def test_backward_refusals():
     assert size(16, 64, 32, None) == INVALID
     assert size(16, 60, 32, ctypes.byref(nb)) == ALIGNMENT
     assert size(0, 64, 32, ctypes.byref(nb)) == OK and nb.value == 0
-    assert size(16, 64, 32, ctypes.byref(nb)) == OK and nb.value >= 16 * 64 * 2
+    assert size(16, 64, 32, ctypes.byref(nb)) == OK and nb.value == 16 * 64 * 4        # few values: fp32 dZ
+    assert size(1600, 64, 32, ctypes.byref(nb)) == OK and nb.value >= 1600 * 64 * 2
+    assert size(16, 64, 32, ctypes.byref(nb)) == OK
     assert _bwd(dtype=0) == UNSUPPORTED
     assert _bwd(act=7) == INVALID
     assert _bwd(dX=0, dW=0) == INVALID
@@ -259,7 +261,8 @@ def _check_backward(dh, x, z, w, act, dtype, dx, dw, what):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(TYPES))
-@pytest.mark.parametrize("shape", SHAPES + [(300, 1096, 1208), (4000, 264, 40)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("shape", SHAPES + [(300, 1096, 1208), (4000, 264, 40), (1, 2048, 2048), (1, 520, 2056), (2, 72, 1024), (250, 200, 8), (256, 64, 8),
+                                            (257, 64, 8)], ids=lambda s: "x".join(map(str, s)))
 def test_backward(shape, dtype):
     M, C, F = shape
     x, w, dh = _inputs(M, C, F, dtype, seed=M + C + F + 1)
