@@ -17,9 +17,10 @@
 // workspace and a second kernel adds the splits in order and rounds once (no atomics:
 // results repeat).  With one split the tile is rounded and stored directly.
 //
-// Few values of dZ (few_kernels: M F <= 2048) have no sums to average their rounding out, and
-// the tensor cores nothing to do: dZ then stays fp32 and two kernels of fp32 multiply-adds
-// form dX and dW (8 rows, 64 to 64 channels: 6 us the backward pass, 11 through the GEMMs).
+// Few values of dZ (few_kernels: M F <= 4096) are too few for their rounding to average out
+// evenly over the results, and leave the tensor cores nothing to do: dZ then stays fp32 and
+// fp32 multiply-adds form dX and dW (8 rows, 64 to 64 channels: 7.9 us the backward pass,
+// 9.3 through the GEMMs; 1 row, 768 to 2048: 11.5 and 16.9; 64 rows, 64 to 64: 10.4 and 9.4).
 #include "common.cuh"
 #include "gate_act.cuh"
 #include "host_util.h"
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(256) gated_dz_kernel(const uint16_t* dH, const
 
 // ------------------------------------------------------- few values of dZ
 
-constexpr int64_t kFew = 2048;
+constexpr int64_t kFew = 4096;
 bool few_kernels(int64_t M, int64_t F) { return M * F <= kFew; }
 
 // dZ in fp32, eight columns per thread.
@@ -113,18 +114,19 @@ __device__ __forceinline__ uint4 round8(const float2 (&a)[4])
                       float2_to_h16x2<EK>(a[2].x, a[2].y), float2_to_h16x2<EK>(a[3].x, a[3].y));
 }
 
-// dX[m][c] = sum over j of dZ[m][j] W[j][c]: R rows and 64 columns per block, its 32 slices of
-// eight lanes take every 32nd j; the slices' sums are added in a fixed order.
-template <int R, bool F16>
-__global__ void __launch_bounds__(256) gated_dx_few_kernel(const float* dZ, const void* W, void* dX, int M, int N2, int C,
-                                                           int* status)
+// out[r][c] = sum over k of A[r ra + k ka] B[k][c], fp32 A, 16-bit B and out: R rows and 8 CV
+// columns per block, whose 256 / CV slices of CV lanes take the terms in turn; the slices' sums
+// are added in a fixed order.  dX: A = dZ, B = W; dW: A = dZ^T, B = X.
+template <int R, int CV, bool F16>
+__global__ void __launch_bounds__(256) few_product_kernel(const float* A, long long ra, long long ka, const void* B,
+                                                          void* out, int rows, int K, int C, int* status)
 {
     pdl_wait();
     pdl_trigger();
     constexpr int EK = F16 ? kF16 : kBF16;
-    __shared__ float2 part[8][R][8][4];   // [warp][row][column vector]
-    const int cv = threadIdx.x & 7, slice = threadIdx.x >> 3;
-    const int c = blockIdx.x * 64 + cv * 8, m0 = blockIdx.y * R;
+    __shared__ float2 part[8][R][CV][4];   // [warp][row][column vector]
+    const int cv = threadIdx.x % CV, slice = threadIdx.x / CV;
+    const int c = (blockIdx.x * CV + cv) * 8, r0 = blockIdx.y * R;
     float2 acc[R][4];
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -132,14 +134,14 @@ __global__ void __launch_bounds__(256) gated_dx_few_kernel(const float* dZ, cons
         for (int i = 0; i < 4; ++i) acc[r][i] = make_float2(0.f, 0.f);
     if (c < C) {
 #pragma unroll 4
-        for (int j = slice; j < N2; j += 32) {
-            const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(W) + static_cast<long long>(j) * C + c);
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        for (int k = slice; k < K; k += 256 / CV) {
+            const uint4 b = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(B) + static_cast<long long>(k) * C + c);
+            const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float d = m0 + r < M ? dZ[static_cast<long long>(m0 + r) * N2 + j] : 0.f;
+                const float2 a = splat(r0 + r < rows ? A[(r0 + r) * ra + k * ka] : 0.f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[r][i] = ffma2(splat(d), h16x2_to_float2<EK>(ww[i]), acc[r][i]);
+                for (int i = 0; i < 4; ++i) acc[r][i] = ffma2(a, h16x2_to_float2<EK>(bw[i]), acc[r][i]);
             }
         }
     }
@@ -148,15 +150,15 @@ __global__ void __launch_bounds__(256) gated_dx_few_kernel(const float* dZ, cons
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
-            for (int o = 8; o < 32; o <<= 1) {
+            for (int o = CV; o < 32; o <<= 1) {
                 acc[r][i].x += __shfl_xor_sync(0xFFFFFFFFu, acc[r][i].x, o);
                 acc[r][i].y += __shfl_xor_sync(0xFFFFFFFFu, acc[r][i].y, o);
             }
-            if ((threadIdx.x & 31) < 8) part[threadIdx.x >> 5][r][cv][i] = acc[r][i];
+            if ((threadIdx.x & 31) < CV) part[threadIdx.x >> 5][r][cv][i] = acc[r][i];
         }
     __syncthreads();
-    const int r = threadIdx.x >> 3;   // now a thread per row and column vector
-    if (r >= R || m0 + r >= M || c >= C) return;
+    const int r = threadIdx.x / CV;   // now a thread per row and column vector
+    if (r >= R || r0 + r >= rows || c >= C) return;
     float2 sum[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -164,35 +166,62 @@ __global__ void __launch_bounds__(256) gated_dx_few_kernel(const float* dZ, cons
 #pragma unroll
         for (int w = 1; w < 8; ++w) sum[i] = __fadd2_rn(sum[i], part[w][r][cv][i]);
     }
-    uint16_t* out = static_cast<uint16_t*>(dX) + static_cast<long long>(m0 + r) * C + c;
-    if (store_ok(dX, 2LL * M * C, out, 16, status)) *reinterpret_cast<uint4*>(out) = round8<EK>(sum);
+    uint16_t* at = static_cast<uint16_t*>(out) + static_cast<long long>(r0 + r) * C + c;
+    if (store_ok(out, 2LL * rows * C, at, 16, status)) *reinterpret_cast<uint4*>(at) = round8<EK>(sum);
 }
 
-// dW[j][c] = sum over the rows of dZ[m][j] X[m][c], eight columns per thread.
+// The same for a short K: eight columns of one row per thread, all of K.
 template <bool F16>
-__global__ void __launch_bounds__(256) gated_dw_few_kernel(const float* dZ, const void* X, void* dW, int M, int N2, int C,
-                                                           int* status)
+__global__ void __launch_bounds__(256) few_outer_kernel(const float* A, long long ra, long long ka, const void* B,
+                                                        void* out, int rows, int K, int C, int* status)
 {
     pdl_wait();
     pdl_trigger();
     constexpr int EK = F16 ? kF16 : kBF16;
     const int nv = C >> 3;
     const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= static_cast<long long>(N2) * nv) return;
-    const int j = static_cast<int>(i / nv), v = static_cast<int>(i - static_cast<long long>(j) * nv);
+    if (i >= static_cast<long long>(rows) * nv) return;
+    const int r = static_cast<int>(i / nv), v = static_cast<int>(i - static_cast<long long>(r) * nv);
     float2 acc[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
+    for (int q = 0; q < 4; ++q) acc[q] = make_float2(0.f, 0.f);
 #pragma unroll 4
-    for (int m = 0; m < M; ++m) {
-        const uint4 x = static_cast<const uint4*>(X)[static_cast<long long>(m) * nv + v];
-        const float2 d = splat(dZ[static_cast<long long>(m) * N2 + j]);
-        const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+    for (int k = 0; k < K; ++k) {
+        const uint4 b = static_cast<const uint4*>(B)[static_cast<long long>(k) * nv + v];
+        const float2 a = splat(A[r * ra + k * ka]);
+        const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[k] = ffma2(d, h16x2_to_float2<EK>(xw[k]), acc[k]);
+        for (int q = 0; q < 4; ++q) acc[q] = ffma2(a, h16x2_to_float2<EK>(bw[q]), acc[q]);
     }
-    uint4* out = static_cast<uint4*>(dW) + i;
-    if (store_ok(dW, 2LL * N2 * C, out, 16, status)) *out = round8<EK>(acc);
+    uint4* at = static_cast<uint4*>(out) + i;
+    if (store_ok(out, 2LL * rows * C, at, 16, status)) *at = round8<EK>(acc);
+}
+
+template <int CV, bool F16>
+cudaError_t few_slices(const float* A, long long ra, long long ka, const void* B, void* out, int rows, int K, int C,
+                       int* status, cudaStream_t stream)
+{
+    const int R = rows == 1 ? 1 : rows == 2 ? 2 : rows <= 4 ? 4 : 8;
+    auto kern = R == 1   ? few_product_kernel<1, CV, F16>
+                : R == 2 ? few_product_kernel<2, CV, F16>
+                : R == 4 ? few_product_kernel<4, CV, F16>
+                         : few_product_kernel<8, CV, F16>;
+    return launch_kernel(kern, dim3((C + 8 * CV - 1) / (8 * CV), (rows + R - 1) / R), dim3(256), 0, stream, 1, A, ra, ka, B,
+                         out, rows, K, C, status);
+}
+
+// Up to 16 terms a thread takes them all; up to 256 in 16 slices, more in 128.  Many slices of a
+// short sum idle, and their exchange costs more than the terms; one thread's long sum is all
+// latency (64 rows, 2048 to 64 channels, backward: 13 us; 50 with 128 slices, 37 with one).
+template <bool F16>
+cudaError_t few_product(const float* A, long long ra, long long ka, const void* B, void* out, int rows, int K, int C,
+                        int* status, cudaStream_t stream)
+{
+    if (K > 256) return few_slices<2, F16>(A, ra, ka, B, out, rows, K, C, status, stream);
+    if (K > 16) return few_slices<16, F16>(A, ra, ka, B, out, rows, K, C, status, stream);
+    const long long n = static_cast<long long>(rows) * (C / 8);
+    return launch_kernel(few_outer_kernel<F16>, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream, 1, A, ra,
+                         ka, B, out, rows, K, C, status);
 }
 
 template <bool F16>
@@ -206,16 +235,10 @@ cudaError_t run_few(const GatedBwdArgs& a, cudaStream_t stream)
                                   a.act, 4LL * M * N2, a.status);
     if (e != cudaSuccess) return e;
     if (a.dX) {
-        auto kern = M == 1 ? gated_dx_few_kernel<1, F16> : M <= 4 ? gated_dx_few_kernel<4, F16> : gated_dx_few_kernel<8, F16>;
-        const int rows = M == 1 ? 1 : M <= 4 ? 4 : 8;
-        e = launch_kernel(kern, dim3((C + 63) / 64, (M + rows - 1) / rows), dim3(256), 0, stream, 1, dZ, a.W, a.dX, M, N2, C,
-                          a.status);
+        e = few_product<F16>(dZ, N2, 1, a.W, a.dX, M, N2, C, a.status, stream);
         if (e != cudaSuccess) return e;
     }
-    if (!a.dW) return cudaSuccess;
-    const long long n = static_cast<long long>(N2) * (C / 8);
-    return launch_kernel(gated_dw_few_kernel<F16>, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream, 1, dZ,
-                         a.X, a.dW, M, N2, C, a.status);
+    return a.dW ? few_product<F16>(dZ, 1, N2, a.X, a.dW, N2, M, C, a.status, stream) : cudaSuccess;
 }
 
 // ------------------------------------------------------------------- dW

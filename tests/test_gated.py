@@ -262,7 +262,7 @@ def _check_backward(dh, x, z, w, act, dtype, dx, dw, what):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("shape", SHAPES + [(300, 1096, 1208), (4000, 264, 40), (1, 2048, 2048), (1, 520, 2056), (2, 72, 1024), (250, 200, 8), (256, 64, 8),
-                                            (257, 64, 8)], ids=lambda s: "x".join(map(str, s)))
+                                            (257, 64, 8), (512, 64, 8), (513, 64, 8)], ids=lambda s: "x".join(map(str, s)))
 def test_backward(shape, dtype):
     M, C, F = shape
     x, w, dh = _inputs(M, C, F, dtype, seed=M + C + F + 1)
