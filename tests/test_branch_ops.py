@@ -357,6 +357,29 @@ def test_layernorm_in_place_many_rows(shape, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("C", [96, 201, 4100, 20001])
+def test_layernorm_c_calls_with_null_parts(C):
+    """Either statistic and either parameter gradient alone."""
+    M = 700
+    x, g, b, dy = _ln_inputs(M, C, "bf16", seed=C)
+    y, mean, rstd = cb.layernorm_forward(x, g, b, stats=True)
+    dx, dg, db = cb.layernorm_backward(dy, x, mean, rstd, g)
+    st = torch.cuda.current_stream().cuda_stream
+    nb = cb.layernorm_backward_workspace_bytes(M, C, x.dtype)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    for which in (0, 1):
+        o, stat, gr = torch.empty_like(y), torch.full_like(mean, 9.0), torch.empty_like(dg)
+        p = [stat.data_ptr(), None] if which == 0 else [None, stat.data_ptr()]
+        assert cb.lib().dgrad_layernorm_forward(M, C, 1, 1e-5, x.data_ptr(), g.data_ptr(), b.data_ptr(), o.data_ptr(), *p,
+                                                st) == OK
+        assert torch.equal(o, y) and torch.equal(stat, (mean, rstd)[which])
+        p = [gr.data_ptr(), None] if which == 0 else [None, gr.data_ptr()]
+        assert cb.lib().dgrad_layernorm_backward(M, C, 1, dy.data_ptr(), x.data_ptr(), g.data_ptr(), mean.data_ptr(),
+                                                 rstd.data_ptr(), o.data_ptr(), *p, ws.data_ptr(), nb, st) == OK
+        assert torch.equal(o, dx) and torch.equal(gr, (dg, db)[which])
+
+
+@pytest.mark.gpu
 def test_layernorm_gradient_by_differences():
     """Central differences of the fp32 forward along a direction v, step h = 2^-5, against <dX, v>.
     The step's own error is h^2/6 times the third derivative along v, below 40 in size here

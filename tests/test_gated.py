@@ -296,6 +296,26 @@ def test_backward_workspace_and_empty():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(16, 72, 40), (900, 136, 72)], ids=lambda s: "x".join(map(str, s)))
+def test_c_calls_with_null_parts(shape):
+    """X may be null where dW is not wanted, W where dX is not."""
+    M, C, F = shape
+    x, w, dh = _inputs(M, C, F, "bf16", seed=3)
+    z = cb.gated_forward(x, w, preact=True)[1]
+    dx, dw = cb.gated_backward(dh, x, z, w)
+    nb = cb.gated_backward_workspace_bytes(M, C, F)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    gx, gw = torch.full_like(x, 7.0), torch.full_like(w, 7.0)
+    call = lambda X, W, dX, dW: cb.lib().dgrad_gated_backward(M, C, F, 1, 0, dh.data_ptr(), X, z.data_ptr(), W, dX, dW,
+                                                              ws.data_ptr(), nb, torch.cuda.current_stream().cuda_stream)
+    assert call(None, w.data_ptr(), gx.data_ptr(), None) == OK
+    assert call(x.data_ptr(), None, None, gw.data_ptr()) == OK
+    assert torch.equal(gx, dx) and torch.equal(gw, dw)
+    assert call(None, w.data_ptr(), gx.data_ptr(), gw.data_ptr()) == INVALID
+    assert call(x.data_ptr(), None, gx.data_ptr(), gw.data_ptr()) == INVALID
+
+
+@pytest.mark.gpu
 def test_one_workspace_in_two_graphs():
     """Two captured backward passes of different sizes that share a workspace, replayed in turn."""
     cases = [_inputs(1500, 136, 264, "bf16", seed=1), _inputs(90, 264, 40, "f16", seed=2)]
