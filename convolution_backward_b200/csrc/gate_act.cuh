@@ -7,9 +7,10 @@
 //   gelu_tanh  g s(2v), v = sqrt(2/pi)(g + 0.044715 g^3)   (the same as g(1 + tanh v)/2)
 //                                           s + 2 g s (1 - s) dv/dg
 //   relu       max(g, 0)                    g > 0
-//   sigmoid    s(g)                         s (1 - s)
+//   sigmoid    s(g)                         s(g) s(-g)
 // The forms keep their relative precision for large negative g, where 1 + tanh and
-// 1 + erf cancel.  P's tail is t 2^(p(t) - g^2/(2 ln 2)), t = 1/(1 + 0.29|g|), with p a
+// 1 + erf cancel, and sigmoid's derivative for large positive g, where 1 - s does (at
+// g = 12 s (1 - s) is off by 1%, from 17 on it is 0).  P's tail is t 2^(p(t) - g^2/(2 ln 2)), t = 1/(1 + 0.29|g|), with p a
 // polynomial of degree 8 fitted to log2(erfcx(|g|/sqrt 2)/(2t)) by weighted least squares
 // on Chebyshev nodes (relative error 1.5e-7; 8e-7 with fp32 rounding for |g| < 4).
 // ex2 and rcp are the hardware's approximations (about 2^-22), far below a 16-bit
@@ -115,8 +116,10 @@ __device__ __forceinline__ void gate_act_grad(float2 g, float2& a, float2& d)
         a = gate_act<kRelu>(g);
         d = make_float2(g.x > 0.f ? 1.0f : 0.f, g.y > 0.f ? 1.0f : 0.f);
     } else {
-        a = logistic2(__fmul2_rn(g, splat(-kLog2e)));
-        d = __fmul2_rn(a, ffma2(a, splat(-1.0f), splat(1.0f)));
+        const float2 x = ex2_pair(__fmul2_rn(make_float2(fabsf(g.x), fabsf(g.y)), splat(-kLog2e)));
+        const float2 r = rcp_pair(__fadd2_rn(x, splat(1.0f))), o = __fmul2_rn(x, r);   // s(|g|), s(-|g|)
+        a = make_float2(g.x > 0.f ? r.x : o.x, g.y > 0.f ? r.y : o.y);
+        d = __fmul2_rn(r, o);
     }
 }
 

@@ -1,0 +1,129 @@
+"""The residual branch's operators where they can go wrong: activations far out.  Against the
+definitions in 64 bits.
+
+Tolerances, elementwise (u, eta: the type's half step relative to the value and half its
+smallest subnormal; e = 2^-24), beyond those of test_branch_ops.py and test_gated.py:
+  act, act'   The exponential's argument t carries up to three roundings, so the exponential
+              is off relatively by 3 t e, and the approximate exponential, reciprocal and
+              products by less than 20 e more: rel = (20 + 4 t) e with t = |g| (silu,
+              sigmoid), g^2/2 (gelu; its fitted tail adds 2.5e-7 = 4.2 e), 2|v| (the tanh
+              form).  1 - s is off by 2 e absolutely where s < 1, which is for t < 18 only:
+              silu' by 2 e t s, the tanh form's by 2 e (2|g| dv/dg) s.  What lies below
+              2^-126 may be zero, and is multiplied by at most 90.
+  dZ          three products more.  On the tensor cores it is rounded once more: u |dz| and half
+              a subnormal step.
+"""
+import numpy as np
+import pytest
+
+import convolution_backward_b200 as cb
+import test_branch_ops as tb
+import test_gated as tg
+
+torch = pytest.importorskip("torch")
+
+E32 = 2.0 ** -24
+TYPES = tb.TYPES
+HALF = tg.TYPES
+TINY = 90 * 2.0 ** -126
+
+
+def act64(name, g):
+    """(act, act', rel, abs of act'): the activation in 64 bits and its fp32 evaluation's errors."""
+    if name == "relu":
+        return np.maximum(g, 0.0), (g > 0).astype(np.float64), 0 * g, 0 * g
+
+    def logistic(v):     # s(v), s(v) s(-v)
+        x = np.exp(-np.abs(v))
+        return np.where(v >= 0, 1.0, x) / (1 + x), x / (1 + x) ** 2
+
+    if name in ("silu", "sigmoid"):
+        t = np.abs(g)
+        s, p = logistic(g)
+        a, d, mag = (g * s, s + g * p, s + t * p) if name == "silu" else (s, p, p)
+        near = np.where(t < 18, 2 * E32 * t * s, 0.0) if name == "silu" else 0 * g
+    elif name == "gelu":
+        t = g * g / 2
+        cdf = 0.5 * torch.special.erfc(torch.from_numpy(-g / np.sqrt(2.0))).numpy()
+        phi = np.exp(-t) / np.sqrt(2 * np.pi)
+        a, d, mag, near = g * cdf, cdf + g * phi, cdf + np.abs(g) * phi, 0 * g
+    else:
+        k = np.sqrt(2 / np.pi)
+        v, dv = k * (g + 0.044715 * g ** 3), k * (1 + 3 * 0.044715 * g * g)
+        t = 2 * np.abs(v)
+        s, p = logistic(2 * v)
+        a, d, mag = g * s, s + 2 * g * p * dv, s + 2 * np.abs(g) * p * dv
+        near = np.where(t < 18, 4 * E32 * np.abs(g) * dv * s, 0.0)
+    rel = (25 + 4 * t) * E32
+    return a, d, rel, np.where(mag > 0, rel * mag, 0.0) + near
+
+
+def dz64(act, dh, z):
+    """(dZ, the fp32 evaluation's error)."""
+    F = dh.shape[1]
+    g, u = z[:, :F], z[:, F:]
+    a, d, rel, ed = act64(act, g)
+    dz = np.concatenate([dh * u * d, dh * a], axis=1)
+    with np.errstate(invalid="ignore"):
+        ea = np.where(a != 0, rel * np.abs(a), 0.0)
+    err = np.concatenate([np.abs(dh * u) * (ed + TINY), np.abs(dh) * (ea + TINY)], axis=1) + 4 * E32 * np.abs(dz)
+    return dz, err
+
+
+def tails(dtype):
+    """Gates from zero to the type's largest value, both signs: 64 of them."""
+    top = float(torch.finfo(HALF[dtype][0]).max)
+    g = [2.0 ** -20, 0.01, 0.1, 0.5, 0.75, 1.0, 1.28, 1.5, 2, 2.5, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 14, 16, 17, 20, 24, 30, 60,
+         80, 300, 1e4, 6e4]
+    return np.array([0.0, *g, *[-v for v in g], top if top > 1e5 else 5e4])
+
+
+# ----------------------------------------------------------- activations far out
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(HALF))
+@pytest.mark.parametrize("act", tg.ACTS)
+def test_activations_to_the_ends(act, dtype):
+    """X is the identity, so that the pre-activations are W's own values: H = act(g) u."""
+    t, u, eta = HALF[dtype]
+    g = torch.from_numpy(tails(dtype)).to(t)
+    other = torch.tensor([1.0, -0.5, 0.375, 1.0])
+    F = 72
+    w = torch.cat([g.expand(F, 64), other.repeat(18)[:, None].expand(F, 64).to(t)]).contiguous().cuda()
+    x = torch.eye(64, dtype=t, device="cuda")
+    for M in (64, 30, 7, 1):    # the pair kernel, the kernels of few rows
+        for lo in range(0, 64 if M > 1 else 0, M) or (0, 20, 50):
+            rows = x[lo:lo + M]
+            h, z = cb.gated_forward(rows, w, act=act, preact=True)
+            Z = w.t()[lo:lo + M]
+            assert torch.equal(z, Z)
+            Z = tg.to64(Z)
+            a, _, rel, _ = act64(act, Z[:, :F])
+            ref = a * Z[:, F:]
+            tg.within(h, ref, u * np.abs(ref) + 1.01 * (rel + 2 * E32) * np.abs(ref) + TINY + eta, f"M={M} from {lo}")
+    cb.check_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("F", [64, 72])      # dZ in fp32; rounded for the tensor cores
+@pytest.mark.parametrize("dtype", list(HALF))
+@pytest.mark.parametrize("act", [a for a in tg.ACTS if a != "gelu_tanh"])
+def test_derivatives_to_the_ends(act, dtype, F):
+    """X and the gate's rows of W are identities: dW is dZ^T, dX the gate's part of dZ."""
+    t, u, eta = HALF[dtype]
+    mk = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(t).cuda()
+    r = np.random.default_rng(7)
+    g = np.broadcast_to(tails(dtype)[:, None], (64, F))
+    other = np.broadcast_to(np.resize([1.0, -0.5, 768.0, 0.0], F), (64, F))
+    dh = mk(np.resize([1.0, -0.75, 0.5], (64, F)) * r.choice([-1.0, 1.0], size=(64, F)))
+    z = mk(np.concatenate([g, other], axis=1))
+    x = torch.eye(64, dtype=t, device="cuda")
+    w = torch.zeros(2 * F, 64, dtype=t, device="cuda")
+    w[:64] = x
+    dx, dw = cb.gated_backward(dh, x, z, w, act=act)
+    cb.check_status()
+    dz, err = dz64(act, tg.to64(dh), tg.to64(z))
+    bound = 2 * u * (1 + u) * np.abs(dz) + 1.01 * err + 2 * eta
+    tg.within(dw.t(), dz, bound, "dw")
+    tg.within(dx, dz[:, :64], bound[:, :64], "dx")
+
