@@ -107,11 +107,11 @@ __device__ __forceinline__ void gate_act_grad(float2 g, float2& a, float2& d)
     } else if constexpr (ACT == kGeluTanh) {
         const float2 g2 = __fmul2_rn(g, g);
         const float2 s = logistic2(__fmul2_rn(g, ffma2(g2, splat(-2.0f * kLog2e * kTanhB), splat(-2.0f * kLog2e * kTanhA))));
-        float2 dv = ffma2(g2, splat(3.0f * kTanhB), splat(kTanhA));
-        dv = make_float2(fminf(dv.x, 1e30f), fminf(dv.y, 1e30f));   // finite: s (1 - s) is 0 there
+        float2 dv2 = ffma2(g2, splat(6.0f * kTanhB), splat(2.0f * kTanhA));
+        dv2 = make_float2(fminf(dv2.x, 1e30f), fminf(dv2.y, 1e30f));   // finite: s (1 - s) is 0 there
         a = __fmul2_rn(g, s);
         const float2 rest = ffma2(s, splat(-1.0f), splat(1.0f));
-        d = ffma2(__fmul2_rn(__fmul2_rn(splat(2.0f), a), rest), dv, s);
+        d = ffma2(__fmul2_rn(a, rest), dv2, s);   // 2 a would pass fp32's largest value before rest is 0
     } else if constexpr (ACT == kRelu) {
         a = gate_act<kRelu>(g);
         d = make_float2(g.x > 0.f ? 1.0f : 0.f, g.y > 0.f ? 1.0f : 0.f);

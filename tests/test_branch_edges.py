@@ -107,7 +107,7 @@ def test_activations_to_the_ends(act, dtype):
 @pytest.mark.gpu
 @pytest.mark.parametrize("F", [64, 72])      # dZ in fp32; rounded for the tensor cores
 @pytest.mark.parametrize("dtype", list(HALF))
-@pytest.mark.parametrize("act", [a for a in tg.ACTS if a != "gelu_tanh"])
+@pytest.mark.parametrize("act", tg.ACTS)
 def test_derivatives_to_the_ends(act, dtype, F):
     """X and the gate's rows of W are identities: dW is dZ^T, dX the gate's part of dZ."""
     t, u, eta = HALF[dtype]
