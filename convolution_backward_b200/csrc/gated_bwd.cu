@@ -36,15 +36,27 @@ constexpr int kSms = 148;   // a B200; splits and workspaces must not depend on 
 
 // ------------------------------------------------------------------- dZ
 
-// Eight columns per thread: 16 bytes of dH, G and U in, 16 bytes of dG and dU out.
+// f16 holds less range than the fp32 values of dZ: products of gradients of some hundreds pass 65504, and
+// small ones fall among its subnormals.  So the pass that forms dZ also finds its largest finite
+// value, block by block, and where that lies beyond 65504 or below 2^-10 (there the subnormals'
+// half step, 2^-25, is more than 2^-15 of it) a second pass writes dZ again, times the power of two that
+// takes it to 2^14 .. 2^15.  The products' fp32 sums are multiplied by the inverse before they are
+// rounded.  What is then below 2^-29 of the largest value keeps an error of 2^-39 of that.  Where dZ
+// needs no scaling the second kernel only reads the blocks' values: f16, 300 rows, 136 to 264
+// channels 17.1 us (15.7 without), 25088 rows, 256 to 512 65 (60), 16384 rows, 1024 to 4096
+// 508 (505).  With two blocks per SM it reads them a microsecond faster, but scales at half the rate.  bf16 has fp32's range.
+constexpr int kDzBlocks = 64 * kSms;
+constexpr size_t kDzScaleBytes = 256 + (kDzBlocks * sizeof(float) + 255) / 256 * 256;   // the inverse, then the blocks' values
+
+// dZ's vectors of eight columns, times `by`: 16 bytes of dH, G and U in, 16 bytes of dG and dU out.
+// Returns (F16) the largest finite value this thread formed.
 template <bool F16>
-__global__ void __launch_bounds__(256) gated_dz_kernel(const uint16_t* dH, const uint16_t* Z, uint16_t* dZ,
-                                                       long long nvec, int nv, int act, long long bytes, int* status)
+__device__ __forceinline__ float dz_vectors(const uint16_t* dH, const uint16_t* Z, uint16_t* dZ, long long nvec, int nv,
+                                            int act, float by, long long bytes, int* status)
 {
-    pdl_wait();      // the previous kernel on the stream has finished
-    pdl_trigger();   // the next one may start its set-up
     constexpr int EK = F16 ? kF16 : kBF16;
     const long long stride = static_cast<long long>(gridDim.x) * 256;
+    float top = 0.f;
     for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < nvec; i += stride) {
         const long long m = i / nv;
         const long long g_at = m * 2 * nv + (i - m * nv);
@@ -61,7 +73,14 @@ __global__ void __launch_bounds__(256) gated_dz_kernel(const uint16_t* dH, const
                 const float2 uf = h16x2_to_float2<EK>(uw[j]);
                 float2 av, dv;
                 gate_act_grad<A>(gf, av, dv);
-                const float2 dg = __fmul2_rn(__fmul2_rn(hf, uf), dv), du = __fmul2_rn(hf, av);
+                float2 dg = __fmul2_rn(__fmul2_rn(hf, uf), dv), du = __fmul2_rn(hf, av);
+                if constexpr (F16) {
+                    const float v[4] = {fabsf(dg.x), fabsf(dg.y), fabsf(du.x), fabsf(du.y)};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) top = fmaxf(top, v[q] < 1e30f ? v[q] : 0.f);   // not infinities, NaN
+                    dg = __fmul2_rn(dg, splat(by));
+                    du = __fmul2_rn(du, splat(by));
+                }
                 a[j] = float2_to_h16x2<EK>(dg.x, dg.y);
                 b[j] = float2_to_h16x2<EK>(du.x, du.y);
             }
@@ -70,6 +89,57 @@ __global__ void __launch_bounds__(256) gated_dz_kernel(const uint16_t* dH, const
         if (store_ok(dZ, bytes, out, 16, status)) out[0] = make_uint4(a[0], a[1], a[2], a[3]);
         if (store_ok(dZ, bytes, out + nv, 16, status)) out[nv] = make_uint4(b[0], b[1], b[2], b[3]);
     }
+    return top;
+}
+
+// The largest of a block's 256 values, in thread 0.
+__device__ __forceinline__ float block_max(float v)
+{
+    __shared__ float s[8];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = s[0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) v = fmaxf(v, s[w]);
+    return v;
+}
+
+// top: the blocks' largest values, kDzBlocks of them (F16).
+template <bool F16>
+__global__ void __launch_bounds__(256) gated_dz_kernel(const uint16_t* dH, const uint16_t* Z, uint16_t* dZ,
+                                                       long long nvec, int nv, int act, float* top, long long bytes,
+                                                       int* status)
+{
+    pdl_wait();      // the previous kernel on the stream has finished
+    pdl_trigger();   // the next one may start its set-up
+    float most = dz_vectors<F16>(dH, Z, dZ, nvec, nv, act, 1.0f, bytes, status);
+    if constexpr (F16) {
+        most = block_max(most);
+        if (threadIdx.x == 0 && store_ok(top, kDzBlocks * 4LL, top + blockIdx.x, 4, status)) top[blockIdx.x] = most;
+    }
+}
+
+// Writes the inverse of dZ's scale, and dZ again where that is not 1.
+__global__ void __launch_bounds__(256) gated_dz_scale_kernel(const uint16_t* dH, const uint16_t* Z, uint16_t* dZ,
+                                                             long long nvec, int nv, int act, const float* top, int blocks,
+                                                             float* inverse, long long bytes, int* status)
+{
+    pdl_wait();
+    pdl_trigger();
+    float most = 0.f;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < blocks; i += 256) most = fmaxf(most, top[i]);
+    most = block_max(most);
+    int k = 0;   // the scale is 2^k
+    if (most > 65504.f || (most > 0.f && most < 0x1p-10f)) {
+        k = 14 + 127 - static_cast<int>(__float_as_uint(most) >> 23);
+        k = k < 100 ? k : 100;   // what 2^100 does not lift to f16's range gives zero in any product of f16 values
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0 && store_ok(inverse, 4, inverse, 4, status))
+        *inverse = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+    if (k != 0) dz_vectors<true>(dH, Z, dZ, nvec, nv, act, __uint_as_float(static_cast<uint32_t>(127 + k) << 23), bytes, status);
 }
 
 // ------------------------------------------------------- few values of dZ
@@ -265,7 +335,7 @@ template <int BN, bool PART, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
     wgrad_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                       const __grid_constant__ CUtensorMap map_d, int M, int N2, int C, int splits, int kb_per,
-                      int* status)
+                      const float* scale, int* status)
 {
     pdl_wait();      // the previous kernel on the stream has finished
     pdl_trigger();   // the next one may start its set-up
@@ -431,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
         const bool issuer = warp == 2 && lane == 0;
         const uint32_t tempty0 = leader_addr(&tempty[0]);
+        const float by = F16 && !PART ? *scale : 1.0f;   // (partials are multiplied when they are added)
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
@@ -453,6 +524,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld_32x32b_x32(tmem_base + lane_addr + static_cast<uint32_t>(acc * BN + chunk * kCols + q * 32),
                                        *reinterpret_cast<uint32_t(*)[32]>(&v[q * 32]));
                 tmem_wait_ld();
+                if constexpr (F16 && !PART) {
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * by);
+                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     uint4 o;
@@ -547,7 +622,8 @@ int dx_splits(int64_t M, int64_t K, int64_t C)
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 template <int BN, bool PART, bool F16>
-cudaError_t run_wgrad(const GatedBwdArgs& a, const void* dZ, void* dst, const WgPlan& p, cudaStream_t stream)
+cudaError_t run_wgrad(const GatedBwdArgs& a, const void* dZ, void* dst, const WgPlan& p, const float* scale,
+                      cudaStream_t stream)
 {
     using L = WgLayout<BN>;
     static_assert(L::kAlloc <= 232448, "shared memory budget");
@@ -570,7 +646,7 @@ cudaError_t run_wgrad(const GatedBwdArgs& a, const void* dZ, void* dst, const Wg
     const int64_t most = device_sm_count() / 2;
     const unsigned pairs = static_cast<unsigned>(units < most ? units : most);
     return launch_kernel(kern, dim3(2 * pairs), dim3(kThreads), L::kAlloc, stream, 2, ma, mb, md,
-                         static_cast<int>(a.M), static_cast<int>(N2), static_cast<int>(a.C), p.splits, p.kb_per,
+                         static_cast<int>(a.M), static_cast<int>(N2), static_cast<int>(a.C), p.splits, p.kb_per, scale,
                          a.status);
 }
 
@@ -580,18 +656,28 @@ cudaError_t run(const GatedBwdArgs& a, cudaStream_t stream)
     const int64_t N2 = 2 * a.F;
     uint16_t* dZ = static_cast<uint16_t*>(a.ws);
     const size_t dz_bytes = static_cast<size_t>(a.M) * N2 * 2;
+    char* rest = static_cast<char*>(a.ws) + align256(dz_bytes);
+    float* inverse = F16 ? reinterpret_cast<float*>(rest) : nullptr;
+    float* top = reinterpret_cast<float*>(rest + 256);
     // dX's and dW's partials share the rest: dX's are read before dW's kernel begins to write
-    float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + align256(dz_bytes));
+    float* part = reinterpret_cast<float*>(rest + kDzScaleBytes);
     const long long nvec = a.M * (a.F / 8);
-    const long long blocks = (nvec + 255) / 256, most = 64LL * kSms;
-    cudaError_t e = launch_kernel(gated_dz_kernel<F16>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
-                                  dim3(256), 0, stream, 1, static_cast<const uint16_t*>(a.dH),
-                                  static_cast<const uint16_t*>(a.Z), dZ, nvec, static_cast<int>(a.F / 8), a.act,
-                                  static_cast<long long>(dz_bytes), a.status);
+    const long long need = (nvec + 255) / 256;
+    const int blocks = static_cast<int>(need < kDzBlocks ? need : kDzBlocks), nv = static_cast<int>(a.F / 8);
+    const uint16_t* dH = static_cast<const uint16_t*>(a.dH);
+    const uint16_t* Z = static_cast<const uint16_t*>(a.Z);
+    cudaError_t e = launch_kernel(gated_dz_kernel<F16>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, 1, dH, Z,
+                                  dZ, nvec, nv, a.act, top, static_cast<long long>(dz_bytes), a.status);
     if (e != cudaSuccess) return e;
+    if (F16) {
+        const int few = blocks < 5 * kSms ? blocks : 5 * kSms;   // as many as are resident
+        e = launch_kernel(gated_dz_scale_kernel, dim3(static_cast<unsigned>(few)), dim3(256), 0, stream, 1, dH, Z, dZ, nvec, nv,
+                          a.act, top, blocks, inverse, static_cast<long long>(dz_bytes), a.status);
+        if (e != cudaSuccess) return e;
+    }
     if (a.dX) {
         const CUtensorMapDataType t = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-        const PwArgs g{a.M, N2, a.C, dZ, a.W, a.dX, a.status, F16};
+        const PwArgs g{a.M, N2, a.C, dZ, a.W, a.dX, a.status, F16, inverse};
         const uint64_t M = static_cast<uint64_t>(a.M), C = static_cast<uint64_t>(a.C), K = static_cast<uint64_t>(N2);
         const uint64_t da[2] = {K, M}, sa[1] = {2 * K}, db[2] = {C, K}, sb[1] = {2 * C}, dd[2] = {C, M};
         const uint32_t tall[2] = {64, 128}, sq[2] = {64, 64};
@@ -607,12 +693,12 @@ cudaError_t run(const GatedBwdArgs& a, cudaStream_t stream)
     if (!a.dW) return cudaSuccess;
     const WgPlan p = wgrad_plan(a.M, N2, a.C);
     if (p.splits == 1)
-        return p.bn == 256 ? run_wgrad<256, false, F16>(a, dZ, a.dW, p, stream)
-                           : run_wgrad<128, false, F16>(a, dZ, a.dW, p, stream);
-    e = p.bn == 256 ? run_wgrad<256, true, F16>(a, dZ, part, p, stream)
-                    : run_wgrad<128, true, F16>(a, dZ, part, p, stream);
+        return p.bn == 256 ? run_wgrad<256, false, F16>(a, dZ, a.dW, p, inverse, stream)
+                           : run_wgrad<128, false, F16>(a, dZ, a.dW, p, inverse, stream);
+    e = p.bn == 256 ? run_wgrad<256, true, F16>(a, dZ, part, p, inverse, stream)
+                    : run_wgrad<128, true, F16>(a, dZ, part, p, inverse, stream);
     if (e != cudaSuccess) return e;
-    return launch_splitk_reduce(part, a.dW, N2 * a.C, p.splits, F16, a.status, stream);
+    return launch_splitk_reduce(part, a.dW, N2 * a.C, p.splits, F16, inverse, a.status, stream);
 }
 
 }  // namespace
@@ -625,7 +711,7 @@ size_t gated_backward_workspace_bytes(int64_t M, int64_t C, int64_t F)
     const int s = dx_splits(M, N2, C);
     const size_t dw = p.splits > 1 ? static_cast<size_t>(p.splits) * N2 * C * 4 : 0;
     const size_t dx = s > 1 ? static_cast<size_t>(s) * M * C * 4 : 0;
-    return align256(static_cast<size_t>(M) * N2 * 2) + (dw > dx ? dw : dx);
+    return align256(static_cast<size_t>(M) * N2 * 2) + kDzScaleBytes + (dw > dx ? dw : dx);
 }
 
 cudaError_t launch_gated_backward(const GatedBwdArgs& a, cudaStream_t stream)

@@ -18,6 +18,7 @@ struct PwArgs {
     void* dX;
     int* status;  // device status word
     bool f16;     // 16-bit operands are f16 (split-K and pair kernels; bf16 otherwise)
+    const float* scale = nullptr;   // f16: the fp32 sums are multiplied by it (device memory; null: 1)
 };
 
 // fp32 in / fp32 out, fp32 FMA (no reduced-precision tensor-core path).
@@ -52,9 +53,9 @@ size_t pointwise_splitk_workspace_bytes(const PwArgs& a, int splits);
 cudaError_t launch_pointwise_tc_splitk(const PwArgs& a, const CUtensorMap& map_a, const CUtensorMap& map_b,
                                        int splits, float* ws, int num_sms, cudaStream_t stream);
 
-// out[i] = round(sum over s of ws[s][i]), s in increasing order; n a multiple of 8.
-cudaError_t launch_splitk_reduce(const float* ws, void* out, int64_t n, int splits, bool f16, int* status,
-                                 cudaStream_t stream);
+// out[i] = round(sum over s of ws[s][i]), s in increasing order; n a multiple of 8.  scale as in PwArgs.
+cudaError_t launch_splitk_reduce(const float* ws, void* out, int64_t n, int splits, bool f16, const float* scale,
+                                 int* status, cudaStream_t stream);
 
 // Dense or grouped KH x KW dgrad on tcgen05, by output phase (S*S sub-GEMMs),
 // bf16 or f16 (f16 = true).  G groups of Kg dY and Cg dX channels; W is

@@ -569,7 +569,8 @@ struct PwPairLayout {
 template <int BN, int STAGES, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
     pw_tc_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                      const __grid_constant__ CUtensorMap map_d, int M, int C, int K, int* status)
+                      const __grid_constant__ CUtensorMap map_d, int M, int C, int K, const float* scale,
+                      int* status)
 {
     using L = PwPairLayout<BN, STAGES>;
     constexpr int EK = F16 ? kF16 : kBF16;
@@ -748,6 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
         const bool issuer = warp == 2 && lane == 0;
         const uint32_t tempty0 = leader_addr(&tempty[0]);
+        const float by = F16 && scale ? *scale : 1.0f;
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
@@ -769,6 +771,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_32x32b_x32(tmem_base + lane_addr + static_cast<uint32_t>(acc * BN + chunk * 64 + 32),
                                    *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
                 tmem_wait_ld();
+                if constexpr (F16) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * by);
+                }
                 uint8_t* rowp = buf + row * 128;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -1025,7 +1031,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // to bf16 (or f16 when F16); 8 channels per thread.
 template <bool F16>
 __global__ void __launch_bounds__(256)
-    splitk_reduce_kernel(const float* __restrict__ ws, uint16_t* __restrict__ dX, long long MC, int S, int* status)
+    splitk_reduce_kernel(const float* __restrict__ ws, uint16_t* __restrict__ dX, long long MC, int S, const float* scale,
+                         int* status)
 {
     pdl_wait();      // the previous kernel on the stream has finished
     pdl_trigger();   // the next one may start its set-up
@@ -1041,6 +1048,11 @@ __global__ void __launch_bounds__(256)
         b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
     }
     constexpr int EK = F16 ? kF16 : kBF16;
+    if (F16 && scale) {
+        const float by = *scale;
+        a.x *= by; a.y *= by; a.z *= by; a.w *= by;
+        b.x *= by; b.y *= by; b.z *= by; b.w *= by;
+    }
     uint4 o;
     o.x = float2_to_h16x2<EK>(a.x, a.y);
     o.y = float2_to_h16x2<EK>(a.z, a.w);
@@ -1123,7 +1135,7 @@ cudaError_t launch_pair(const PwArgs& a, const CUtensorMap& map_a, const CUtenso
     }
     int pairs = max_clusters < num_tiles ? max_clusters : num_tiles;
     return launch_kernel(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), L::kAlloc, stream, 2, map_a,
-                         map_b, map_d, static_cast<int>(a.M), static_cast<int>(a.C), static_cast<int>(a.K), a.status);
+                         map_b, map_d, static_cast<int>(a.M), static_cast<int>(a.C), static_cast<int>(a.K), a.scale, a.status);
 }
 
 }  // namespace
@@ -1165,16 +1177,17 @@ cudaError_t launch_pointwise_tc_splitk(const PwArgs& a, const CUtensorMap& map_a
     }
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_splitk_reduce(ws, a.dX, a.M * a.C, S, a.f16, a.status, stream);
+    return launch_splitk_reduce(ws, a.dX, a.M * a.C, S, a.f16, a.scale, a.status, stream);
 }
 
-cudaError_t launch_splitk_reduce(const float* ws, void* out, int64_t n, int splits, bool f16, int* status,
-                                 cudaStream_t stream)
+cudaError_t launch_splitk_reduce(const float* ws, void* out, int64_t n, int splits, bool f16, const float* scale,
+                                 int* status, cudaStream_t stream)
 {
     const long long threads = (n + 7) / 8;
     auto reduce = f16 ? splitk_reduce_kernel<true> : splitk_reduce_kernel<false>;
     const cudaError_t e = launch_kernel(reduce, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, stream,
-                                        1, ws, static_cast<uint16_t*>(out), static_cast<long long>(n), splits, status);
+                                        1, ws, static_cast<uint16_t*>(out), static_cast<long long>(n), splits, scale,
+                                        status);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -277,7 +277,9 @@ dgrad_status_t dgrad_gated_forward(int64_t M, int64_t C, int64_t F, dgrad_dtype_
  *     dZ = [dH*U*act'(G) | dH*act(G)],   dX = dZ . W,   dW = dZ^T . X.
  * dX or dW null: not computed (X is then needed for dW only, W for dX only; both null:
  * DGRAD_ERR_INVALID).  dZ is computed in fp32 and rounded to the element type, the
- * operand type of both products (M*F <= 4096: it stays fp32).  Types and limits as dgrad_gated_forward.
+ * operand type of both products (M*F <= 4096: it stays fp32); in f16 times a power of
+ * two, undone in the fp32 sums, where its largest finite value lies beyond 65504 or below 2^-10
+ * (values under 2^-29 of that one are then held to 2^-39 of it).  Types and limits as dgrad_gated_forward.
  * workspace (16-byte aligned, at least dgrad_gated_backward_workspace bytes; contents
  * do not matter and are clobbered) holds dZ and fp32 partial sums; too small or null:
  * DGRAD_ERR_INVALID.  Two calls that may overlap need a workspace each.  dX, dW and

@@ -1,5 +1,5 @@
-"""The residual branch's operators where they can go wrong: activations far out.  Against the
-definitions in 64 bits.
+"""The residual branch's operators where they can go wrong: activations far out and the ends of the
+types' ranges.  Against the definitions in 64 bits.
 
 Tolerances, elementwise (u, eta: the type's half step relative to the value and half its
 smallest subnormal; e = 2^-24), beyond those of test_branch_ops.py and test_gated.py:
@@ -10,8 +10,8 @@ smallest subnormal; e = 2^-24), beyond those of test_branch_ops.py and test_gate
               form).  1 - s is off by 2 e absolutely where s < 1, which is for t < 18 only:
               silu' by 2 e t s, the tanh form's by 2 e (2|g| dv/dg) s.  What lies below
               2^-126 may be zero, and is multiplied by at most 90.
-  dZ          three products more.  On the tensor cores it is rounded once more: u |dz| and half
-              a subnormal step.
+  dZ          three products more.  On the tensor cores it is rounded once more: u |dz| and,
+              f16, half a subnormal step: 2^-25, or where dZ is scaled 2^-39 of its largest value.
 """
 import numpy as np
 import pytest
@@ -127,3 +127,86 @@ def test_derivatives_to_the_ends(act, dtype, F):
     tg.within(dw.t(), dz, bound, "dw")
     tg.within(dx, dz[:, :64], bound[:, :64], "dx")
 
+
+# ------------------------------------------- the gated gradients' range
+
+def _gpu64(*ts):
+    return [t.detach().double() for t in ts]
+
+
+def _within(got, ref, bound, what):
+    """As test_gated.within, on the GPU."""
+    bad = ~((got.double() - ref).abs() <= bound)
+    if bool(bad.any()):
+        i = int(torch.argmax(torch.where(bad, (got.double() - ref).abs() / bound, torch.zeros_like(ref)).flatten()))
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} off, worst at {i}: got {got.flatten()[i].item()!r}, "
+                             f"want {ref.flatten()[i].item()!r}, bound {bound.flatten()[i].item()!r}")
+
+
+def _check_gated_backward(dh, x, z, w, dtype, dx, dw, what):
+    """silu, on the GPU in 64 bits."""
+    _, u, eta = HALF[dtype]
+    DH, X, Z, W = _gpu64(dh, x, z, w)
+    F = DH.shape[1]
+    g, uu = Z[:, :F], Z[:, F:]
+    t = g.abs()
+    s, p = torch.sigmoid(g), torch.sigmoid(g) * torch.sigmoid(-g)
+    rel = (25 + 4 * t) * E32
+    dz = torch.cat([DH * uu * (s + g * p), DH * g * s], 1)
+    e = torch.cat([(DH * uu).abs() * (rel * (s + t * p) + 2 * E32 * t.clamp(max=18) * s), DH.abs() * t * s * rel], 1)
+    top = float(dz.abs().max())
+    least = 0.0 if dtype != "f16" else 2.0 ** -25 if 2.0 ** -10 <= top <= 65504 else top * 2.0 ** -39
+    e = u * dz.abs() + 1.01 * (e + 4 * E32 * dz.abs()) + least
+    for got, ref, err, terms in ((dx, dz @ W, e @ W.abs(), 2 * F * (dz.abs() @ W.abs())),
+                                 (dw, dz.t() @ X, e.t() @ X.abs(), X.shape[0] * (dz.abs().t() @ X.abs()))):
+        _within(got, ref, u * ref.abs() + (1 + u) * (err + 1.01 * E32 * terms) + eta, f"{what} {tuple(ref.shape)}")
+        # two roundings of at most u, evenly spread: in norm sqrt(2/3) u, a tenth for the rest
+        assert float((got.double() - ref).norm() / ref.norm()) <= 1.1 * (2 / 3) ** 0.5 * u, what
+
+
+# (few values), (pairs' tiles for dX, whole sums for dW), (dX's sums split), (dW's rows split)
+RANGE_SHAPES = [(16, 72, 40), (300, 136, 264), (300, 1096, 1208), (2600, 264, 72)]
+
+
+def _scaled(shape, dtype, seed, ks):
+    """x, w, dh, z with dH, U, X and W scaled by powers of two."""
+    x, w, dh = tg._inputs(*shape, dtype, seed)
+    z = cb.gated_forward(x, w, preact=True)[1]
+    a, b, c, d = (2.0 ** k for k in ks)
+    F = shape[2]
+    z = z.clone()
+    z[:, F:] *= b
+    return x * c, w * d, dh * a, z
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(HALF))
+@pytest.mark.parametrize("ks", [(9, 8, -12, -12), (-14, -6, 8, 8), (-8, -4, 4, 4)], ids=["large", "small", "middling"])
+@pytest.mark.parametrize("shape", RANGE_SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_gated_backward_over_the_range(shape, ks, dtype):
+    """dZ above f16's largest value and among its subnormals, between results that are neither."""
+    x, w, dh, z = _scaled(shape, dtype, 5, ks)
+    dx, dw = cb.gated_backward(dh, x, z, w)
+    cb.check_status()
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
+    _check_gated_backward(dh, x, z, w, dtype, dx, dw, str(ks))
+    for only in (dict(weight_grad=False), dict(input_grad=False)):
+        got = cb.gated_backward(dh, x, z, w, **only)
+        assert all(p is None or torch.equal(p, q) for p, q in zip(got, (dx, dw)))
+
+
+@pytest.mark.gpu
+def test_gated_backward_range_in_a_graph():
+    """One captured backward pass replayed with gradients of unlike size."""
+    cases = [_scaled((300, 136, 264), "f16", 5, ks) for ks in ((9, 8, -12, -12), (0, 0, 0, 0), (-14, -6, 8, 8))]
+    want = [[t.clone() for t in cb.gated_backward(dh, x, z, w)] for x, w, dh, z in cases]
+    x, w, dh, z = (t.clone() for t in cases[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = cb.gated_backward(dh, x, z, w)
+    for i in (0, 1, 2, 1, 0):
+        for into, of in zip((x, w, dh, z), cases[i]):
+            into.copy_(of)
+        g.replay()
+        assert all(torch.equal(p, q) for p, q in zip(out, want[i]))
+    cb.check_status()
