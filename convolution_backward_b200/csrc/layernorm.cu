@@ -693,11 +693,12 @@ __global__ void __launch_bounds__(ln_block(MODE, true, SH), ln_per_sm(MODE, 16 /
         }
         const float2 t = row_sum<MULTI, true>(sq.x + sq.y, sqn.x + sqn.y, p.T, group, red, turn);
         if (!live) return;
-        // rstd (q - mq - n mqn) = q rstd + ((x - mean) (-rstd^2 mqn) - rstd mq)
-        const float a = -rstd * rstd * (t.y * inv_c), b = -rstd * (t.x * inv_c);
+        // rstd (q - mq - n mqn) = q rstd + (n (-rstd mqn) - rstd mq), with n formed again: rstd^2
+        // lies outside fp32's range for rows whose spread is below 2^-64
+        const float a = -rstd * (t.y * inv_c), b = -rstd * (t.x * inv_c);
         const float2 a2 = make_float2(a, a), b2 = make_float2(b, b);
         char* out = static_cast<char*>(p.dx) + m * p.C * es;
-        if constexpr (SH) l.store_single(fmaf(q1, rstd, fmaf(x1, a, b)), out, p.dx, p.M * p.C * es, p.status);
+        if constexpr (SH) l.store_single(fmaf(q1, rstd, fmaf(x1 * rstd, a, b)), out, p.dx, p.M * p.C * es, p.status);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             if (v >= l.mine) continue;
@@ -707,7 +708,7 @@ __global__ void __launch_bounds__(ln_block(MODE, true, SH), ln_per_sm(MODE, 16 /
             gamma.get(l, v, g);
 #pragma unroll
             for (int i = 0; i < H; ++i)
-                f[i] = ffma2(__fmul2_rn(d[i], g[i]), r2, ffma2(__fadd2_rn(f[i], minus), a2, b2));
+                f[i] = ffma2(__fmul2_rn(d[i], g[i]), r2, ffma2(__fmul2_rn(__fadd2_rn(f[i], minus), r2), a2, b2));
             pack_pairs(x[v], f);
             l.store(x[v], out, v, p.dx, p.M * p.C * es, p.status);
         }

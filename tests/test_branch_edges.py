@@ -210,3 +210,47 @@ def test_gated_backward_range_in_a_graph():
         g.replay()
         assert all(torch.equal(p, q) for p, q in zip(out, want[i]))
     cb.check_status()
+
+
+# --------------------------------------------------- layer norm's gradient, far rows
+
+def _ln_bwd_check(dy, x, g, mean, rstd, dtype, got, what):
+    """test_branch_ops._check_bwd on the GPU."""
+    M, C = x.shape
+    _, u, eta = TYPES[dtype]
+    DY, X, G, m, r = _gpu64(dy, x, g, mean, rstd)
+    n, q = (X - m[:, None]) * r[:, None], DY * G
+    mq, mqn = q.mean(1, keepdim=True), (q * n).mean(1, keepdim=True)
+    K = tb.chain(C)
+    ref = r[:, None] * (q - mq - n * mqn)
+    ex = r[:, None] * E32 * (5 * q.abs() + (K + 6) * q.abs().mean(1, keepdim=True)
+                             + n.abs() * (K + 12) * (q * n).abs().mean(1, keepdim=True))
+    _within(got[0], ref, u * ref.abs() + (1 + u) * 1.01 * ex + eta, what + " dx")
+    k = (M + 64) * E32 * 1.01
+    for o, terms, more, name in ((got[1], DY * n, 3 * E32, "dgamma"), (got[2], DY, 0.0, "dbeta")):
+        ref = terms.sum(0)
+        _within(o, ref, u * ref.abs() + (1 + u) * (k + more) * terms.abs().sum(0) + eta, f"{what} {name}")
+
+
+def _ln_rows(M, C, dtype, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    t = TYPES[dtype][0]
+    x = (rnd(M, C) * (0.4 * rnd(C)).exp() + 0.5 * rnd(C)).to(t)
+    return x, (1 + 0.2 * rnd(C)).to(t), (0.2 * rnd(C)).to(t), rnd(M, C).to(t)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])      # f16 holds no such rows
+@pytest.mark.parametrize("k", [-66, 60], ids=["tiny", "huge"])
+@pytest.mark.parametrize("shape", [(9, 96), (40, 1001), (5, 768), (3, 20001)], ids=lambda s: "x".join(map(str, s)))
+def test_layernorm_backward_far_statistics(shape, k, dtype):
+    """Rows of 2^-66 and of 2^60: the gradient scales with 1/spread, whose square fp32 does not hold."""
+    x, g, b, dy = _ln_rows(*shape, dtype, seed=4)
+    x = (x.float() * 2.0 ** k).to(x.dtype)
+    X = x.double()
+    mean = X.mean(1).float()
+    rstd = (1 / (X.var(1, unbiased=False)).sqrt()).float()
+    got = cb.layernorm_backward(dy, x, mean, rstd, g)
+    cb.check_status()
+    _ln_bwd_check(dy, x, g, mean, rstd, dtype, got, f"2^{k}")
