@@ -53,9 +53,11 @@ __device__ __forceinline__ uint4 philox_block(const Drop& p, long long b)
     return make_uint4(c0, c1, c2, c3);
 }
 
+// Without a residual a kept zero keeps its sign, so that p = 0 changes nothing.
+template <bool RES>
 __device__ __forceinline__ float drop_one(float x, float r, uint32_t draw, const Drop& p)
 {
-    return draw >= p.thr ? fmaf(x, p.scale, r) : r;
+    return draw >= p.thr ? (RES ? fmaf(x, p.scale, r) : x * p.scale) : r;
 }
 
 template <int EK, bool RES>
@@ -88,7 +90,7 @@ __global__ void __launch_bounds__(kDropBlock) dropout_kernel(const Drop p)
             for (int i = 0; i < VEC; ++i) {
                 const int e = v * VEC + i;
                 const uint32_t draw = (e & 1) ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu;
-                f[i] = drop_one(f[i], RES ? rf[i] : 0.f, draw, p);
+                f[i] = drop_one<RES>(f[i], RES ? rf[i] : 0.f, draw, p);
             }
             V o;
             o.pack(f);
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(kDropBlock) dropout_kernel(const Drop p)
                 r.unpack(rf);
             }
             const uint32_t draw = (e & 1) ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu;
-            f[0] = drop_one(f[0], rf[0], draw, p);
+            f[0] = drop_one<RES>(f[0], rf[0], draw, p);
             x.pack(f);
             if (store_ok(p.y, p.n * es, static_cast<char*>(p.y) + i * es, es, p.status)) x.store(p.y, i);
         }

@@ -298,7 +298,7 @@ dgrad_status_t dgrad_gated_backward_workspace(int64_t M, int64_t C, int64_t F, s
  * (low word of seed, high word of seed): word (i % 8)/2, its low half for even i.  It
  * is kept where the draw is >= t = round(65536*p) (ties to even) and scale is
  * 65536/(65536 - t); 0 <= p <= 1 is thus rounded to a multiple of 2^-16, and p = 1
- * drops everything.  A dropped element does not enter the result (an infinity or NaN
+ * drops everything and p = 0 changes nothing.  A dropped element does not enter the result (an infinity or NaN
  * in X leaves no trace there).  Give every call its own (seed, offset); the backward
  * pass takes its forward's.  All element types; Y may be X or residual. n <= 2^48. */
 dgrad_status_t dgrad_dropout_forward(int64_t n, dgrad_dtype_t dtype, double p, uint64_t seed, uint64_t offset,

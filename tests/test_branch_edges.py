@@ -19,6 +19,7 @@ import pytest
 import convolution_backward_b200 as cb
 import test_branch_ops as tb
 import test_gated as tg
+from oracle import branch
 
 torch = pytest.importorskip("torch")
 
@@ -254,3 +255,16 @@ def test_layernorm_backward_far_statistics(shape, k, dtype):
     got = cb.layernorm_backward(dy, x, mean, rstd, g)
     cb.check_status()
     _ln_bwd_check(dy, x, g, mean, rstd, dtype, got, f"2^{k}")
+
+
+# ------------------------------------------------------------------------- dropout
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("n", [64, 100_003])
+def test_dropout_keeps_the_sign_of_zero(n, dtype):
+    x = torch.full((n,), -0.0, dtype=TYPES[dtype][0], device="cuda")
+    assert torch.signbit(cb.dropout_forward(x, 0.0, 3)).all()
+    keep = torch.from_numpy(branch.dropout_keep(n, 0.4, 3, 0)[0]).cuda()
+    assert torch.equal(torch.signbit(cb.dropout_backward(x, 0.4, 3)), keep)
+    assert torch.signbit(cb.dropout_forward(x, 0.0, 3, residual=x)).all()
