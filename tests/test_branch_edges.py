@@ -1,5 +1,5 @@
-"""The residual branch's operators where they can go wrong: activations far out and the ends of the
-types' ranges.  Against the definitions in 64 bits.
+"""The residual branch's operators where they can go wrong: activations far out, the ends of the
+types' ranges, layer norm's loops over many rows.  Against the definitions in 64 bits.
 
 Tolerances, elementwise (u, eta: the type's half step relative to the value and half its
 smallest subnormal; e = 2^-24), beyond those of test_branch_ops.py and test_gated.py:
@@ -13,6 +13,8 @@ smallest subnormal; e = 2^-24), beyond those of test_branch_ops.py and test_gate
   dZ          three products more.  On the tensor cores it is rounded once more: u |dz| and,
               f16, half a subnormal step: 2^-25, or where dZ is scaled 2^-39 of its largest value.
 """
+import os
+
 import numpy as np
 import pytest
 
@@ -213,7 +215,26 @@ def test_gated_backward_range_in_a_graph():
     cb.check_status()
 
 
-# --------------------------------------------------- layer norm's gradient, far rows
+# ------------------------------------------------------------------------ layer norm
+
+def _ln_fwd_check(x, g, b, eps, dtype, y, mean, rstd, what):
+    """test_branch_ops._check_fwd on the GPU."""
+    _, u, eta = TYPES[dtype]
+    X, G, B = _gpu64(x, g, b)
+    C = X.shape[1]
+    K = tb.chain(C)
+    rm = X.mean(1)
+    rr = 1 / torch.sqrt(((X - rm[:, None]) ** 2).mean(1) + eps)
+    em = (K + 1) * E32 * X.abs().mean(1) + E32 * rm.abs()
+    er = ((K / 2 + 4) * E32 + 0.5 * (em * rr) ** 2) * rr
+    _within(mean, rm, em, what + " mean")
+    _within(rstd, rr, er, what + " rstd")
+    n = (X - rm[:, None]) * rr[:, None]
+    ey = ((em * rr)[:, None] + n.abs() * ((K / 2 + 8) * E32 + 0.5 * (em * rr)[:, None] ** 2)) * G.abs() \
+        + 2 * E32 * ((n * G).abs() + B.abs())
+    ry = n * G + B
+    _within(y, ry, u * ry.abs() + (1 + u) * 1.01 * ey + eta, what + " y")
+
 
 def _ln_bwd_check(dy, x, g, mean, rstd, dtype, got, what):
     """test_branch_ops._check_bwd on the GPU."""
@@ -255,6 +276,74 @@ def test_layernorm_backward_far_statistics(shape, k, dtype):
     got = cb.layernorm_backward(dy, x, mean, rstd, g)
     cb.check_status()
     _ln_bwd_check(dy, x, g, mean, rstd, dtype, got, f"2^{k}")
+
+
+# Enough rows that every block takes several steps of them, the last one a part: within a warp and across warps, on
+# and off the 16-byte grid, rows shorter than a vector, vectors per thread from one to the most.
+MANY = [(40_009, 1), (40_009, 3), (40_009, 7), (40_009, 9), (30_011, 13), (30_011, 33), (30_011, 57), (30_011, 100),
+        (20_011, 201), (20_011, 385), (240_007, 8), (240_007, 16), (160_009, 64), (80_021, 96), (20_021, 384), (20_021, 640),
+        (9_001, 771), (9_001, 1536), (5_003, 2048), (3_001, 4104), (3_001, 4099), (1_801, 8200)]
+
+
+def _many(shape, dtype, edge):
+    M, C = shape
+    x, g, b, dy = _ln_rows(M, C, dtype, seed=M + C)
+    if C == 1:
+        b = b + 1
+    y, mean, rstd = cb.layernorm_forward(x, g, b, eps=1e-5, stats=True)
+    grads = cb.layernorm_backward(dy, x, mean, rstd, g)
+    cb.check_status()
+    _ln_fwd_check(x, g, b, 1e-5, dtype, y, mean, rstd, edge)
+    _ln_bwd_check(dy, x, g, mean, rstd, dtype, grads, edge)
+    return x, g, b, dy, (y, mean, rstd), grads
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", MANY, ids=lambda s: "x".join(map(str, s)))
+def test_layernorm_many_rows(shape, dtype):
+    x, g, b, dy, want, grads = _many(shape, dtype, "many rows")
+    z = x.clone()               # rows in flight are not disturbed by results written over their tensor
+    got = cb.layernorm_forward(z, g, b, eps=1e-5, stats=True, out=z)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    for which in (0, 1):
+        d, z = dy.clone(), x.clone()
+        got = cb.layernorm_backward(d, z, want[1], want[2], g, out=d if which == 0 else z)
+        assert all(torch.equal(p, q) for p, q in zip(got, grads))
+    cb.check_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", [(40_009, 3), (40_009, 9), (30_011, 57), (20_011, 201), (240_007, 8), (80_021, 96), (20_021, 640),
+                                   (9_001, 1536), (3_001, 4099)], ids=lambda s: "x".join(map(str, s)))
+def test_layernorm_many_rows_every_store_in_bounds(shape, dtype, monkeypatch):
+    path = os.path.join(os.path.dirname(cb.library_path()), "libdgrad_debug.so")
+    if not os.path.exists(path):
+        pytest.skip("libdgrad_debug.so not built")
+    monkeypatch.setattr(cb, "_LIB_PATH", path)
+    monkeypatch.setattr(cb, "_lib", None)
+    _many(shape, dtype, "debug")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("C", [1, 8, 9, 33, 64, 96, 100, 201, 384, 768, 1001, 2048])
+def test_layernorm_many_rows_take_every_sm(C, dtype):
+    """The workspace holds 8 C bytes per block: 20000 rows are a block's work for every SM."""
+    for i in range(200):
+        M = int(20000 * 1.02 ** i)
+        assert cb.layernorm_backward_workspace_bytes(M, C, dtype) // (8 * C) >= 140, M
+
+
+@pytest.mark.parametrize("case", [(torch.bfloat16, 9, 4736), (torch.bfloat16, 33, 4736), (torch.bfloat16, 100, 4736),
+                                  (torch.bfloat16, 64, 9472), (torch.bfloat16, 96, 18944), (torch.float32, 9, 4736),
+                                  (torch.float32, 100, 2368), (torch.float32, 64, 9472)], ids=lambda c: f"{c[0]}x{c[1]}")
+def test_layernorm_blocks_where_rows_pass_one_step(case):
+    """One row more than a step for every resident block: about as many blocks, not a few with many steps."""
+    dtype, C, M = case
+    blocks = lambda m: cb.layernorm_backward_workspace_bytes(m, C, dtype) // (8 * C)
+    for m in range(M, M + 3 * M // 2, 37):
+        assert 2 * blocks(m + 1) >= blocks(m), m
 
 
 # ------------------------------------------------------------------------- dropout
