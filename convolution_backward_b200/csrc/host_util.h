@@ -51,6 +51,31 @@ inline cudaError_t ensure_smem_limit(const void* kernel, int bytes)
     return cudaSuccess;
 }
 
+// Clusters of the launch `cfg` that can be resident at once, asked once per (kernel, device);
+// `fallback` where the question fails (asked again by the next call).
+inline int resident_clusters(const void* kernel, const cudaLaunchConfig_t& cfg, int fallback)
+{
+    struct Entry {
+        const void* k;
+        int dev;
+        int clusters;
+    };
+    static std::mutex mu;
+    static std::vector<Entry> known;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return fallback;
+    std::lock_guard<std::mutex> lk(mu);
+    for (const Entry& x : known)
+        if (x.k == kernel && x.dev == dev) return x.clusters;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();   // not the next launch's error
+        return fallback;
+    }
+    known.push_back({kernel, dev, n});
+    return n;
+}
+
 // Launch `kernel` on `stream` with programmatic stream serialisation (it may
 // begin while the previous kernel on the stream finishes; the kernel itself
 // waits for it with griddepcontrol.wait before touching global memory) and,

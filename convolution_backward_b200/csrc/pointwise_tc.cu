@@ -1126,14 +1126,9 @@ cudaError_t launch_pair(const PwArgs& a, const CUtensorMap& map_a, const CUtenso
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     // persistent: as many pairs as can be resident at once (at most one per tile)
-    static int max_clusters = 0;
-    if (max_clusters == 0) {
-        cfg.gridDim = dim3(static_cast<unsigned>(num_sms & ~1));
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) n = num_sms / 2;
-        max_clusters = n;
-    }
-    int pairs = max_clusters < num_tiles ? max_clusters : num_tiles;
+    cfg.gridDim = dim3(static_cast<unsigned>(num_sms & ~1));
+    const int max_clusters = resident_clusters(reinterpret_cast<const void*>(kern), cfg, num_sms / 2);
+    const int pairs = max_clusters < num_tiles ? max_clusters : num_tiles;
     return launch_kernel(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), L::kAlloc, stream, 2, map_a,
                          map_b, map_d, static_cast<int>(a.M), static_cast<int>(a.C), static_cast<int>(a.K), a.scale, a.status);
 }

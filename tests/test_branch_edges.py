@@ -14,6 +14,8 @@ smallest subnormal; e = 2^-24), beyond those of test_branch_ops.py and test_gate
               f16, half a subnormal step: 2^-25, or where dZ is scaled 2^-39 of its largest value.
 """
 import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -357,3 +359,37 @@ def test_dropout_keeps_the_sign_of_zero(n, dtype):
     keep = torch.from_numpy(branch.dropout_keep(n, 0.4, 3, 0)[0]).cuda()
     assert torch.equal(torch.signbit(cb.dropout_backward(x, 0.4, 3)), keep)
     assert torch.signbit(cb.dropout_forward(x, 0.0, 3, residual=x)).all()
+
+
+# --------------------------------------------------------------------- first calls
+
+FIRST = """
+import threading, torch, convolution_backward_b200 as cb
+cases = []
+for i in range(8):
+    g = torch.Generator(device="cuda").manual_seed(i)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").half()
+    M, C, F = 300 + 40 * i, 136, 264
+    cases.append((r(M, F), r(M, C), r(M, 2 * F), r(2 * F, C) / 8))
+torch.cuda.synchronize()
+got, start = [None] * 8, threading.Barrier(8)
+def work(i):
+    s = torch.cuda.Stream()
+    start.wait()
+    got[i] = cb.gated_backward(*cases[i], stream=s)
+    s.synchronize()
+ts = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+[t.start() for t in ts]; [t.join() for t in ts]
+for c, o in zip(cases, got):
+    assert all(torch.equal(p, q) for p, q in zip(cb.gated_backward(*c), o))
+cb.check_status()
+print("first calls agree")
+"""
+
+
+@pytest.mark.gpu
+def test_first_calls_from_many_threads():
+    """A process whose first calls come from eight threads at once."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "agree" in r.stdout, r.stdout + r.stderr
