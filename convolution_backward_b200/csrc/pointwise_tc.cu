@@ -1040,13 +1040,19 @@ __global__ void __launch_bounds__(256)
     if (i >= MC) return;
     float4 a = *reinterpret_cast<const float4*>(ws + i);
     float4 b = *reinterpret_cast<const float4*>(ws + i + 4);
-#pragma unroll 8   // the loads of eight splits at a time, added in order
-    for (int s = 1; s < S; ++s) {
+    auto add = [&](int s) {
         const float4 x = *reinterpret_cast<const float4*>(ws + s * MC + i);
         const float4 y = *reinterpret_cast<const float4*>(ws + s * MC + i + 4);
         a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
         b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
+    };
+    // added in order; the loads of eight splits at a time, then the rest as they come
+    int s = 1;
+    for (; s + 8 <= S; s += 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) add(s + j);
     }
+    for (; s < S; ++s) add(s);
     constexpr int EK = F16 ? kF16 : kBF16;
     if (F16 && scale) {
         const float by = *scale;

@@ -361,6 +361,26 @@ def test_dropout_keeps_the_sign_of_zero(n, dtype):
     assert torch.signbit(cb.dropout_forward(x, 0.0, 3, residual=x)).all()
 
 
+# ---------------------------------------------------------------- sums over splits
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(HALF))
+@pytest.mark.parametrize("splits", [1, 2, 3, 4, 8, 9, 10, 16, 17, 18, 25, 32])
+def test_every_split_is_added_once(splits, dtype):
+    """Whole numbers: every split's partial is exact, and so is their sum."""
+    gen = torch.Generator(device="cuda").manual_seed(splits)
+    ints = lambda *s: torch.randint(-1, 2, s, generator=gen, device="cuda").to(HALF[dtype][0])
+    dy, w = ints(1, 1, 37, 64 * 32), ints(64 * 32, 72)
+    dy[..., 64 * splits:] = 0      # (sums stay within 256, whole numbers in either type)
+    dy[..., 8:] *= (torch.arange(64 * 32 - 8, device="cuda") % 64 < 8).to(dy.dtype)
+    _, used = cb.splitk_workspace_bytes(1, 1, 37, 64 * 32, 72, splits)
+    got = cb.pointwise_splitk(dy, w, splits=splits)
+    cb.check_status()
+    assert used == splits
+    want = dy.double().view(37, -1) @ w.double()
+    assert float(want.abs().max()) <= 256 and torch.equal(got.double().view(37, 72), want)
+
+
 # --------------------------------------------------------------------- first calls
 
 FIRST = """
