@@ -1,5 +1,6 @@
 """The residual branch's operators where they can go wrong: activations far out, the ends of the
-types' ranges, layer norm's loops over many rows.  Against the definitions in 64 bits.
+types' ranges, infinities, layer norm's and the gated gradients' loops over many rows and tiles.
+Against the definitions in 64 bits.
 
 Tolerances, elementwise (u, eta: the type's half step relative to the value and half its
 smallest subnormal; e = 2^-24), beyond those of test_branch_ops.py and test_gated.py:
@@ -133,7 +134,7 @@ def test_derivatives_to_the_ends(act, dtype, F):
     tg.within(dx, dz[:, :64], bound[:, :64], "dx")
 
 
-# ------------------------------------------- the gated gradients' range
+# ------------------------------------------- the gated gradients' range and loops
 
 def _gpu64(*ts):
     return [t.detach().double() for t in ts]
@@ -214,6 +215,50 @@ def test_gated_backward_range_in_a_graph():
             into.copy_(of)
         g.replay()
         assert all(torch.equal(p, q) for p, q in zip(out, want[i]))
+    cb.check_status()
+
+
+# More units than the GPU has SM pairs: dX's tiles, dW's tiles, dW's narrow tiles
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(HALF))
+@pytest.mark.parametrize("shape", [(2600, 2056, 264), (12000, 264, 72), (300, 2056, 1160), (700, 3000, 1096), (130, 104, 9704),
+                                   (20000, 72, 24)], ids=lambda s: "x".join(map(str, s)))
+def test_gated_backward_more_tiles_than_pairs(shape, dtype):
+    x, w, dh = tg._inputs(*shape, dtype, seed=3)
+    z = cb.gated_forward(x, w, preact=True)[1]
+    dx, dw = cb.gated_backward(dh, x, z, w)
+    cb.check_status()
+    _check_gated_backward(dh, x, z, w, dtype, dx, dw, str(shape))
+    again = cb.gated_backward(dh, x, z, w)
+    assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(HALF))
+@pytest.mark.parametrize("shape", [(16, 72, 40), (300, 136, 264)], ids=lambda s: "x".join(map(str, s)))
+def test_gated_backward_infinities(shape, dtype):
+    """A NaN or an infinity spoils its own row of dX and its own column's rows of dW."""
+    M, C, F = shape
+    x, w, dh = tg._inputs(*shape, dtype, seed=3)
+    z = cb.gated_forward(x, w, preact=True)[1]
+    dh[5, 9] = 0
+    clean = cb.gated_backward(dh, x, z, w)
+    rows = [m for m in range(M) if m != 5]
+    outs = [j for j in range(2 * F) if j % F != 9]
+    for bad in (float("nan"), float("inf")):
+        d = dh.clone()
+        d[5, 9] = bad
+        dx, dw = cb.gated_backward(d, x, z, w)
+        assert torch.equal(dx[rows], clean[0][rows]) and torch.equal(dw[outs], clean[1][outs])
+        assert not torch.isfinite(dx[5]).any() and not torch.isfinite(dw[[9, F + 9]]).any()
+    for act in tg.ACTS:     # an overflowed pre-activation
+        d = dh.clone()
+        d[5, 9] = 1
+        zz = z.clone()
+        zz[5, 9] = float("-inf")
+        clean = cb.gated_backward(dh, x, z, w, act=act)
+        dx, dw = cb.gated_backward(d, x, zz, w, act=act)
+        assert torch.equal(dx[rows], clean[0][rows]) and torch.equal(dw[outs], clean[1][outs])
     cb.check_status()
 
 
@@ -348,6 +393,27 @@ def test_layernorm_blocks_where_rows_pass_one_step(case):
         assert 2 * blocks(m + 1) >= blocks(m), m
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", [(9, 96), (40, 201), (60, 1001), (5000, 96), (5, 20001)], ids=lambda s: "x".join(map(str, s)))
+def test_layernorm_backward_infinities(shape, dtype):
+    """A NaN or an infinity in dY spoils its own row of dX and its own columns of dgamma and dbeta."""
+    M, C = shape
+    x, g, b, dy = _ln_rows(M, C, dtype, seed=4)
+    _, mean, rstd = cb.layernorm_forward(x, g, b, stats=True)
+    dy[3, 11] = 0
+    clean = cb.layernorm_backward(dy, x, mean, rstd, g)
+    rows, cols = [m for m in range(M) if m != 3], [c for c in range(C) if c != 11]
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        d = dy.clone()
+        d[3, 11] = bad
+        dx, dg, db = cb.layernorm_backward(d, x, mean, rstd, g)
+        assert torch.equal(dx[rows], clean[0][rows])
+        assert torch.equal(dg[cols], clean[1][cols]) and torch.equal(db[cols], clean[2][cols])
+        assert not torch.isfinite(dx[3]).any() and not torch.isfinite(dg[11]) and not torch.isfinite(db[11])
+    cb.check_status()
+
+
 # ------------------------------------------------------------------------- dropout
 
 @pytest.mark.gpu
@@ -370,15 +436,15 @@ def test_every_split_is_added_once(splits, dtype):
     """Whole numbers: every split's partial is exact, and so is their sum."""
     gen = torch.Generator(device="cuda").manual_seed(splits)
     ints = lambda *s: torch.randint(-1, 2, s, generator=gen, device="cuda").to(HALF[dtype][0])
-    dy, w = ints(1, 1, 37, 64 * 32), ints(64 * 32, 72)
-    dy[..., 64 * splits:] = 0      # (sums stay within 256, whole numbers in either type)
-    dy[..., 8:] *= (torch.arange(64 * 32 - 8, device="cuda") % 64 < 8).to(dy.dtype)
-    _, used = cb.splitk_workspace_bytes(1, 1, 37, 64 * 32, 72, splits)
+    K = 128 * splits               # two k-blocks of 64 to a split
+    dy, w = ints(1, 1, 37, K), ints(K, 72)
+    dy *= (torch.arange(K, device="cuda") % 64 < 4).to(dy.dtype)   # sums within 256, whole numbers in either type
+    _, used = cb.splitk_workspace_bytes(1, 1, 37, K, 72, splits)
     got = cb.pointwise_splitk(dy, w, splits=splits)
     cb.check_status()
     assert used == splits
-    want = dy.double().view(37, -1) @ w.double()
-    assert float(want.abs().max()) <= 256 and torch.equal(got.double().view(37, 72), want)
+    want = dy.double().view(37, K) @ w.double()
+    assert torch.equal(got.double().view(37, 72), want)
 
 
 # --------------------------------------------------------------------- first calls
