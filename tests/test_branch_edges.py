@@ -165,6 +165,8 @@ def _check_gated_backward(dh, x, z, w, dtype, dx, dw, what):
     e = u * dz.abs() + 1.01 * (e + 4 * E32 * dz.abs()) + least
     for got, ref, err, terms in ((dx, dz @ W, e @ W.abs(), 2 * F * (dz.abs() @ W.abs())),
                                  (dw, dz.t() @ X, e.t() @ X.abs(), X.shape[0] * (dz.abs().t() @ X.abs()))):
+        if got is None:
+            continue
         _within(got, ref, u * ref.abs() + (1 + u) * (err + 1.01 * E32 * terms) + eta, f"{what} {tuple(ref.shape)}")
         # two roundings of at most u, evenly spread: in norm sqrt(2/3) u, a tenth for the rest
         assert float((got.double() - ref).norm() / ref.norm()) <= 1.1 * (2 / 3) ** 0.5 * u, what
@@ -297,6 +299,8 @@ def _ln_bwd_check(dy, x, g, mean, rstd, dtype, got, what):
     _within(got[0], ref, u * ref.abs() + (1 + u) * 1.01 * ex + eta, what + " dx")
     k = (M + 64) * E32 * 1.01
     for o, terms, more, name in ((got[1], DY * n, 3 * E32, "dgamma"), (got[2], DY, 0.0, "dbeta")):
+        if o is None:
+            continue
         ref = terms.sum(0)
         _within(o, ref, u * ref.abs() + (1 + u) * (k + more) * terms.abs().sum(0) + eta, f"{what} {name}")
 
@@ -425,6 +429,116 @@ def test_dropout_keeps_the_sign_of_zero(n, dtype):
     keep = torch.from_numpy(branch.dropout_keep(n, 0.4, 3, 0)[0]).cuda()
     assert torch.equal(torch.signbit(cb.dropout_backward(x, 0.4, 3)), keep)
     assert torch.signbit(cb.dropout_forward(x, 0.0, 3, residual=x)).all()
+
+
+# ------------------------------------------------------------ the sizes' ends, 32 bits
+
+def _tiles_agree(t, rows, what):
+    """Every block of `rows` rows holds the first one's bits."""
+    t = t.view(-1, rows, t.shape[-1])
+    for i in range(1, t.shape[0]):
+        assert torch.equal(t[i], t[0]), f"{what}, block {i}"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [96, 99])
+def test_layernorm_past_32_bits(C):
+    """More than 2^31 elements: the same 2^16 rows again and again."""
+    rows = 1 << 16
+    n = (1 << 31) // (rows * C) + 2
+    x, g, b, dy = _ln_rows(rows, C, "bf16", seed=C)
+    X, D = x.repeat(n, 1), dy.repeat(n, 1)
+    y, mean, rstd = cb.layernorm_forward(X, g, b, eps=1e-5, stats=True)
+    cb.check_status()
+    _ln_fwd_check(x, g, b, 1e-5, "bf16", y[:rows], mean[:rows], rstd[:rows], "first rows")
+    for t, what in ((y, "y"), (mean[:, None], "mean"), (rstd[:, None], "rstd")):
+        _tiles_agree(t, rows, what)
+    dx, dg, db = cb.layernorm_backward(D, X, mean, rstd, g, out=D)
+    cb.check_status()
+    _ln_bwd_check(dy, x, g, mean[:rows], rstd[:rows], "bf16", (dx[:rows], None, None), "first rows")
+    _tiles_agree(dx, rows, "dx")
+    DY, N = dy.double(), (x.double() - mean[:rows, None].double()) * rstd[:rows, None].double()
+    u = TYPES["bf16"][1]
+    for got, terms in ((dg, DY * N), (db, DY)):     # chains of n rows / (296 blocks of 16 rows or more), 64 more
+        chain = n * rows // (296 * 16) + 128
+        _within(got, n * terms.sum(0), u * n * terms.sum(0).abs() + 1.01 * chain * E32 * n * terms.abs().sum(0), "columns")
+
+
+@pytest.mark.gpu
+def test_dropout_past_32_bits():
+    """2^32 + 13 elements: their block numbers pass 2^29, their byte offsets 2^33."""
+    n, seed, offset = (1 << 32) + 13, 77, 1 << 40
+    x = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    y = cb.dropout_forward(x, 0.25, seed, offset, out=x)
+    cb.check_status()
+    for at in (0, (1 << 31) - 4096, (1 << 32) - 4096, (n - 4096) // 8 * 8):
+        m = min(8192, n - at)
+        blocks = np.arange(at // 8, (at + m + 7) // 8, dtype=np.uint64)
+        ctr = np.stack([blocks & np.uint64(0xFFFFFFFF), blocks >> np.uint64(32), np.full_like(blocks, offset & 0xFFFFFFFF),
+                        np.full_like(blocks, offset >> 32)], axis=1)
+        words = branch.philox(ctr, (seed, 0))
+        draws = np.stack([words & np.uint64(0xFFFF), words >> np.uint64(16)], axis=2).reshape(-1)[:m]
+        assert np.array_equal(tb.to64(y[at:at + m]) != 0, draws >= 16384), at
+
+
+@pytest.mark.gpu
+def test_gated_past_32_bits():
+    """Z of more than 2^31 elements: the same 4096 rows again and again."""
+    rows, n, C, F = 4096, 132, 8, 2048
+    x, w, dh = tg._inputs(rows, C, F, "bf16", seed=4)
+    X, D = x.repeat(n, 1), dh.repeat(n, 1)
+    h, z = cb.gated_forward(X, w, preact=True)
+    cb.check_status()
+    assert z.numel() > 1 << 31
+    tg._check_forward(x[:300], w, "silu", "bf16", h[:300], z[:300], "first rows")
+    _tiles_agree(h, rows, "h")
+    _tiles_agree(z, rows, "z")
+    dx, dw = cb.gated_backward(D, X, z, w)
+    cb.check_status()
+    _tiles_agree(dx, rows, "dx")
+    one = z[:rows].clone()
+    DW = _dw64(dh, x, one)
+    _check_gated_backward(dh, x, one, w, "bf16", dx[:rows], None, "first rows")
+    u = HALF["bf16"][1]
+    assert float((dw.double() - n * DW).norm() / (n * DW).norm()) <= 1.1 * (2 / 3) ** 0.5 * u
+
+
+def _dw64(dh, x, z):
+    DH, X, Z = _gpu64(dh, x, z)
+    F = DH.shape[1]
+    g, s = Z[:, :F], torch.sigmoid(Z[:, :F])
+    return torch.cat([DH * Z[:, F:] * s * (1 + g * (1 - s)), DH * g * s], 1).t() @ X
+
+
+# The widest blocks: C and F at their limits, on every kind of kernel.
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(HALF))
+@pytest.mark.parametrize("shape", [(1, 65536, 8), (20, 65536, 8), (40, 65536, 136), (1, 16, 32768), (20, 16, 32768), (40, 72, 32768)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_gated_widest(shape, dtype):
+    M, C, F = shape
+    gen = torch.Generator(device="cuda").manual_seed(C + F)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    t, u, eta = HALF[dtype]
+    x, w, dh = rnd(M, C).to(t), (1.5 * rnd(2 * F, C) / C ** 0.5).to(t), (0.3 * rnd(M, F)).to(t)
+    h, z = cb.gated_forward(x, w, preact=True)
+    cb.check_status()
+    X, W = _gpu64(x, w)
+    ref, d = X @ W.t(), C * E32 * (X.abs() @ W.abs().t())
+    _within(z, ref, u * ref.abs() + (1 + u) * d + eta, "z")
+    g, o, s = ref[:, :F], ref[:, F:], torch.sigmoid(ref[:, :F])
+    e = 1.2 * o.abs() * d[:, :F] + (g * s).abs() * d[:, F:] + (25 + 4 * g.abs()) * E32 * (g * s * o).abs()
+    _within(h, g * s * o, u * (g * s * o).abs() + (1 + u) * 1.01 * e + eta, "h")
+    dx, dw = cb.gated_backward(dh, x, z, w)
+    cb.check_status()
+    _check_gated_backward(dh, x, z, w, dtype, dx, dw, "widest")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", [(3, 65536), (700, 65535), (2, 65533)], ids=lambda s: "x".join(map(str, s)))
+def test_layernorm_widest(shape, dtype):
+    _many(shape, dtype, "widest")
 
 
 # ---------------------------------------------------------------- sums over splits
