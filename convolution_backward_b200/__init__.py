@@ -650,7 +650,9 @@ def gated_backward_workspace_bytes(M, C, F) -> int:
 def gated_backward(dH, X, Z, W, act="silu", input_grad=True, weight_grad=True, workspace=None, stream=None):
     """Gradients of gated_forward: (dX, dW) (bf16 or f16; dgrad_gated_backward).
 
-    Z: the pre-activations gated_forward kept.  Without ``input_grad`` dX, without
+    Z: the pre-activations gated_forward kept.  The gradient at Z is rounded to the element
+    type before the two products (fp32 up to 4096 values of dH); in f16 it is scaled where its
+    range needs that.  Without ``input_grad`` dX, without
     ``weight_grad`` dW is None and not computed.  workspace: a CUDA tensor of at least
     gated_backward_workspace_bytes(...) bytes, taken from torch when None."""
     import torch
@@ -691,8 +693,9 @@ def dropout_forward(X, p, seed, offset=0, residual=None, out=None, stream=None):
     """Dropout with probability p, plus ``residual`` when given (dgrad_dropout_forward).
 
     The mask is a function of (seed, offset) and the element's index, and is not stored:
-    give every call its own pair, and the backward pass its forward's.  ``out`` may be X
-    or residual."""
+    give every call its own pair, and the backward pass its forward's.  The pair is taken when
+    the call is made: a call captured into a CUDA graph repeats its mask in every replay.
+    p is rounded to a multiple of 2^-16.  ``out`` may be X or residual."""
     _need_cuda(X)
     code = _dtype_code(X)
     given = [t for t in (residual, out) if t is not None]

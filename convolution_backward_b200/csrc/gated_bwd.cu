@@ -6,8 +6,11 @@
 //
 // 8 M F C operations in two GEMMs of equal size; dZ is formed once, in fp32 from the
 // kept pre-activations, and rounded to the operands' 16 bits (the tensor cores take no
-// wider type at this rate; its rounding averages out over the sums) into the workspace,
-// from where both GEMMs read it.  dX is the pointwise dgrad GEMM with K = 2F.
+// wider type at this rate) into the workspace, from where both GEMMs read it.  That is a
+// second rounding: terms and their errors both grow with the root of their number, so the
+// gradients' error is about sqrt(2) times that of rounding the results alone, in norm, however
+// long the sums (against 64 bits: bf16 2.3e-3 and 1.7e-3, f16 2.9e-4 and 2.1e-4).  dX is the
+// pointwise dgrad GEMM with K = 2F.
 //
 // wgrad_pair_kernel: dW's tiles of 256 x BN on pairs of SMs.  The sums run over rows, so
 // both operands lie MN-major in memory (their columns contiguous) and go to the MMA as
@@ -17,10 +20,18 @@
 // workspace and a second kernel adds the splits in order and rounds once (no atomics:
 // results repeat).  With one split the tile is rounded and stored directly.
 //
-// Few values of dZ (few_kernels: M F <= 4096) are too few for their rounding to average out
-// evenly over the results, and leave the tensor cores nothing to do: dZ then stays fp32 and
-// fp32 multiply-adds form dX and dW (8 rows, 64 to 64 channels: 7.9 us the backward pass,
-// 9.3 through the GEMMs; 1 row, 768 to 2048: 11.5 and 16.9; 64 rows, 64 to 64: 10.4 and 9.4).
+// Few values of dZ (few_kernels: M F <= 4096) leave the tensor cores little to do: dZ then
+// stays fp32, with no second rounding, and fp32 multiply-adds form dX and dW.  At 4096 values
+// the two ways take about the same time, with fewer this one is faster.  The backward pass in bf16,
+// us, this way and through the GEMMs:
+//     rows, C to F          values                    rows, C to F          values
+//     1, 64 to 8                8    3.9   8.1        64, 768 to 64         4096  10.4  11.0
+//     8, 64 to 64             512    8.0   8.7        64, 2048 to 64        4096  13.1  11.4
+//     1, 768 to 2048         2048   10.9  15.8        128, 768 to 32        4096  10.2  11.1
+//     8, 768 to 512          4096    9.5  13.2        256, 768 to 16        4096  13.7  11.8
+//     32, 768 to 128         4096   15.3  12.0        512, 768 to 8         4096   9.0  14.1
+//     64, 64 to 64           4096    9.8   8.9        4, 768 to 2048        8192  20.0  16.7
+//     512, 64 to 8           4096    8.7  10.8        1, 2048 to 8192       8192  76    44
 #include "common.cuh"
 #include "gate_act.cuh"
 #include "host_util.h"

@@ -221,10 +221,12 @@ dgrad_status_t dgrad_depthwise_tc_workspace(const dgrad_problem_t* prob, size_t*
  * N*H*W positions of an NHWC tensor (or tokens): M rows of C channels, dense.
  * Base pointers 16-byte aligned (fp32 statistics: 4-byte); unlike the gradients
  * above, layer norm and dropout take any C or n >= 1: rows that do not start on
- * 16 bytes run on element-wide loads.  Ranges an output shares with another
+ * 16 bytes run on the 16-byte vectors inside them and single elements at their ends
+ * (rows too long for registers: on single elements).  Ranges an output shares with another
  * argument are refused (DGRAD_ERR_INVALID) except where one is named below.
  * Results repeat bit for bit: no atomics, sums in a fixed order, fp32 throughout
- * and one rounding to the element type at the end.  M (or n) of 0 is a no-op, and
+ * and one rounding to the element type at the end (the gated block's gradients: two, see
+ * there).  M (or n) of 0 is a no-op, and
  * sets gradients that are sums over rows to zero. ---- */
 
 /* Layer norm over C channels:
@@ -232,8 +234,8 @@ dgrad_status_t dgrad_depthwise_tc_workspace(const dgrad_problem_t* prob, size_t*
  *     Y = (x - mean)*rstd*gamma + beta.
  * All element types (gamma, beta and Y have X's).  gamma or beta null: ones, zeros.
  * mean, rstd (fp32, M each, either may be null) are what the backward pass needs.
- * Y may be X.  eps finite and >= 0 (a constant row at eps 0 gives NaN, as the
- * formula does).  C <= 65536, M < 2^31 (else DGRAD_ERR_UNSUPPORTED). */
+ * Y may be X.  eps finite and >= 0 (at eps 0 a constant row gives NaN, or what rounding
+ * leaves of its differences).  C <= 65536, M < 2^31 (else DGRAD_ERR_UNSUPPORTED). */
 dgrad_status_t dgrad_layernorm_forward(int64_t M, int64_t C, dgrad_dtype_t dtype, double eps, const void* X,
                                        const void* gamma, const void* beta, void* Y, float* mean, float* rstd,
                                        void* stream);
@@ -279,7 +281,10 @@ dgrad_status_t dgrad_gated_forward(int64_t M, int64_t C, int64_t F, dgrad_dtype_
  * DGRAD_ERR_INVALID).  dZ is computed in fp32 and rounded to the element type, the
  * operand type of both products (M*F <= 4096: it stays fp32); in f16 times a power of
  * two, undone in the fp32 sums, where its largest finite value lies beyond 65504 or below 2^-10
- * (values under 2^-29 of that one are then held to 2^-39 of it).  Types and limits as dgrad_gated_forward.
+ * (values under 2^-29 of that one are then held to 2^-39 of it).  The rounding of dZ makes the
+ * gradients' error about 1.4 times that of one rounding.  An infinite pre-activation (an f16 Z
+ * that overflowed) gives NaN where the formulas multiply it by zero, as silu and both gelus do:
+ * in its row of dX and its rows of dW.  Types and limits as dgrad_gated_forward.
  * workspace (16-byte aligned, at least dgrad_gated_backward_workspace bytes; contents
  * do not matter and are clobbered) holds dZ and fp32 partial sums; too small or null:
  * DGRAD_ERR_INVALID.  Two calls that may overlap need a workspace each.  dX, dW and
@@ -298,9 +303,10 @@ dgrad_status_t dgrad_gated_backward_workspace(int64_t M, int64_t C, int64_t F, s
  * (low word of seed, high word of seed): word (i % 8)/2, its low half for even i.  It
  * is kept where the draw is >= t = round(65536*p) (ties to even) and scale is
  * 65536/(65536 - t); 0 <= p <= 1 is thus rounded to a multiple of 2^-16, and p = 1
- * drops everything and p = 0 changes nothing.  A dropped element does not enter the result (an infinity or NaN
- * in X leaves no trace there).  Give every call its own (seed, offset); the backward
- * pass takes its forward's.  All element types; Y may be X or residual. n <= 2^48. */
+ * drops everything, p <= 2^-17 nothing.  A dropped element does not enter the result (an
+ * infinity or NaN in X leaves no trace there).  Give every call its own (seed, offset); the backward
+ * pass takes its forward's.  Both are taken when the call is made: a call captured into a graph
+ * draws the same mask in every replay.  All element types; Y may be X or residual. n <= 2^48. */
 dgrad_status_t dgrad_dropout_forward(int64_t n, dgrad_dtype_t dtype, double p, uint64_t seed, uint64_t offset,
                                      const void* X, const void* residual, void* Y, void* stream);
 

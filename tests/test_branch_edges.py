@@ -261,6 +261,10 @@ def test_gated_backward_infinities(shape, dtype):
         clean = cb.gated_backward(dh, x, z, w, act=act)
         dx, dw = cb.gated_backward(d, x, zz, w, act=act)
         assert torch.equal(dx[rows], clean[0][rows]) and torch.equal(dw[outs], clean[1][outs])
+        if act in ("relu", "sigmoid"):
+            assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
+        else:
+            assert torch.isnan(dx[5]).all() and torch.isnan(dw[[9, F + 9]]).all()
     cb.check_status()
 
 
