@@ -55,7 +55,8 @@ constexpr int kSms = 148;   // a B200; splits and workspaces must not depend on 
 // rounded.  What is then below 2^-29 of the largest value keeps an error of 2^-39 of that.  Where dZ
 // needs no scaling the second kernel only reads the blocks' values: f16, 300 rows, 136 to 264
 // channels 17.1 us (15.7 without), 25088 rows, 256 to 512 65 (60), 16384 rows, 1024 to 4096
-// 508 (505).  With two blocks per SM it reads them a microsecond faster, but scales at half the rate.  bf16 has fp32's range.
+// 508 (505).  With two blocks per SM it reads them a microsecond faster, but scales at half the
+// rate.  bf16 has fp32's range.
 constexpr int kDzBlocks = 64 * kSms;
 constexpr size_t kDzScaleBytes = 256 + (kDzBlocks * sizeof(float) + 255) / 256 * 256;   // the inverse, then the blocks' values
 
@@ -103,7 +104,7 @@ __device__ __forceinline__ float dz_vectors(const uint16_t* dH, const uint16_t* 
     return top;
 }
 
-// The largest of a block's 256 values, in thread 0.
+// The largest of a block's 256 values, in every thread (once per kernel: nothing is read again).
 __device__ __forceinline__ float block_max(float v)
 {
     __shared__ float s[8];
