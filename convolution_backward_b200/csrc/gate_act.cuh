@@ -11,8 +11,9 @@
 // The forms keep their relative precision for large negative g, where 1 + tanh and
 // 1 + erf cancel, and sigmoid's derivative for large positive g, where 1 - s does (at
 // g = 12 s (1 - s) is off by 1%, from 17 on it is 0).  P's tail is
-// t 2^(p(t) - g^2/(2 ln 2)), t = 1/(1 + 0.29|g|), with p a polynomial of degree 8 fitted to log2(erfcx(|g|/sqrt 2)/(2t)) by weighted least squares
-// on Chebyshev nodes (relative error 2.5e-7; 8e-7 with fp32 rounding for |g| < 4).
+// t 2^(p(t) - g^2/(2 ln 2)), t = 1/(1 + 0.29|g|), with p a polynomial of degree 8 fitted to
+// log2(erfcx(|g|/sqrt 2)/(2t)) by weighted least squares on Chebyshev nodes (relative error
+// 2.5e-7; 8e-7 with fp32 rounding for |g| < 4).
 // ex2 and rcp are the hardware's approximations (about 2^-22), far below a 16-bit
 // result's half step.  With the general-purpose exp, division and erfc the epilogue took
 // longer than the tile's MMAs: 32768 rows, 768 to 2048 channels, bf16 silu 149 us, gelu
