@@ -13,8 +13,14 @@ calls raise ``DgradUnavailable``.
     Y, mean, rstd = layernorm_forward(X, gamma, beta, stats=True)  # X (..., C)
     H, Z = gated_forward(X, W, act="silu", preact=True)            # W (2F, C) -> (..., F), (..., 2F)
     Y = dropout_forward(X, p, seed, offset, residual=R)
+    Y, mean, rstd = groupnorm_forward(X, groups, gamma, beta, act="silu", stats=True)   # X (N, ..., C)
 
-and their ``_backward`` counterparts.  Tensors are NHWC (rows of channels) and contiguous;
+and their ``_backward`` counterparts; and over all parameters at once
+
+    state = adamw_state(params, bits=8)             # or 32; master=True keeps fp32 copies
+    norm, scale = grad_norm(grads, max_norm=1.0)
+    adamw_step(state, grads, step, lr, grad_scale=scale)
+  Tensors are NHWC (rows of channels) and contiguous;
 float32, bfloat16 or float16 (16-bit in, 16-bit out, fp32 accumulate).
 """
 from __future__ import annotations
@@ -27,6 +33,8 @@ import threading
 __all__ = ["pointwise", "pointwise_splitk", "pointwise_splitk_noalloc", "depthwise_tc", "depthwise_tc_workspace_bytes", "dense", "grouped", "splitk_workspace_bytes", "depthwise", "out_dims", "check_status", "DgradError", "DgradUnavailable",
            "layernorm_forward", "layernorm_backward", "layernorm_backward_workspace_bytes", "dropout_forward", "dropout_backward",
            "gated_forward", "gated_backward", "gated_backward_workspace_bytes", "ACTIVATIONS",
+           "groupnorm_forward", "groupnorm_backward", "groupnorm_forward_workspace_bytes", "groupnorm_backward_workspace_bytes",
+           "AdamWState", "adamw_state", "adamw_step", "adamw_moments", "grad_norm", "grad_norm_workspace_bytes",
            "Problem", "lib", "library_path", "selftest_timeout", "fma_probe", "STATUS"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -41,6 +49,7 @@ STATUS = {0: "DGRAD_OK", 1: "DGRAD_ERR_INVALID", 2: "DGRAD_ERR_UNSUPPORTED", 3: 
           4: "DGRAD_ERR_CUDA", 5: "DGRAD_ERR_TIMEOUT", 6: "DGRAD_ERR_BOUNDS"}
 DW_MODES = {"auto": 0, "rotated": 1, "rowstream": 2}
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}   # dgrad_act_t
+_ACT_NONE = 5                    # DGRAD_ACT_NONE: group norm's act=None
 DTYPES = {"f32": 0, "bf16": 1, "f16": 2}
 SPLITK_SCRATCH_BYTES = 8 << 20   # DGRAD_SPLITK_SCRATCH_BYTES: the fixed per-device split-K buffer
 
@@ -57,6 +66,14 @@ class DgradError(RuntimeError):
         if status == 4:
             msg += f" (cudaError {cuda_error})"
         super().__init__(msg)
+
+
+class _AdamW(ctypes.Structure):
+    """dgrad_adamw_t."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64), ("lr_device", ctypes.c_void_p),
+                ("step_device", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p), ("state_bits", ctypes.c_int32),
+                ("stochastic", ctypes.c_int32), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
 
 
 class Problem(ctypes.Structure):
@@ -128,6 +145,15 @@ def lib():
                     "gated_forward": [i64, i64, i64, ci, ci, vp, vp, vp, vp, vp],
                     "gated_backward": [i64, i64, i64, ci, ci, vp, vp, vp, vp, vp, vp, vp, sz, vp],
                     "gated_backward_workspace": [i64, i64, i64, P(sz)],
+                    "groupnorm_forward": [i64, i64, i64, i64, ci, dbl, ci, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+                    "groupnorm_backward": [i64, i64, i64, i64, ci, ci, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+                    "groupnorm_forward_workspace": [i64, i64, i64, i64, ci, P(sz)],
+                    "groupnorm_backward_workspace": [i64, i64, i64, i64, ci, P(sz)],
+                    "adamw_step": [i64, vp, ci, ci, P(_AdamW), vp],
+                    "adamw_check": [i64, vp, ci, ci, ctypes.c_int32],
+                    "adamw_moments": [i64, vp, vp, vp, vp],
+                    "grad_norm": [i64, vp, vp, ci, dbl, vp, vp, sz, vp],
+                    "grad_norm_workspace": [i64, P(sz)],
                     "dropout_forward": [i64, ci, dbl, u64, u64, vp, vp, vp, vp],
                     "dropout_backward": [i64, ci, dbl, u64, u64, vp, vp, vp]}.items():
                 f = getattr(L, "dgrad_" + name)
@@ -597,6 +623,124 @@ def layernorm_backward(dY, X, mean, rstd, gamma=None, param_grads=True, workspac
     return out, dgamma, dbeta
 
 
+def _samples_of(X, groups):
+    """(N, S, C, G): samples, positions, channels and groups of X (N, ..., C)."""
+    if X.dim() < 2:
+        raise ValueError("expected samples of positions (N, ..., C)")
+    groups = int(groups)
+    C = X.shape[-1]
+    if groups < 1 or C < 1 or C % groups:
+        raise ValueError(f"groups must divide the {C} channels, got {groups}")
+    S = 1
+    for d in X.shape[1:-1]:
+        S *= d
+    return X.shape[0], S, C, groups
+
+
+def _norm_act(act):
+    return _ACT_NONE if act is None else _act_code(act)
+
+
+@functools.lru_cache(maxsize=256)
+def _gn_workspace(backward, N, S, C, G, code) -> int:
+    name = "dgrad_groupnorm_" + ("backward" if backward else "forward") + "_workspace"
+    nb = ctypes.c_size_t()
+    _check(getattr(lib(), name)(N, S, C, G, code, ctypes.byref(nb)), name)
+    return nb.value
+
+
+def groupnorm_forward_workspace_bytes(N, S, C, groups, dtype) -> int:
+    """Workspace bytes groupnorm_forward needs for N samples of S positions of C channels (host only)."""
+    return _gn_workspace(False, int(N), int(S), int(C), int(groups), _code_of(dtype))
+
+
+def groupnorm_backward_workspace_bytes(N, S, C, groups, dtype) -> int:
+    """Workspace bytes groupnorm_backward needs (host only)."""
+    return _gn_workspace(True, int(N), int(S), int(C), int(groups), _code_of(dtype))
+
+
+def _workspace(al, workspace, like, nbytes):
+    """(tensor, bytes): the given workspace, or one from torch."""
+    if workspace is not None:
+        return workspace, workspace.numel() * workspace.element_size()
+    nbytes = max(nbytes, 16)
+    return _empty(al, like, (nbytes,), _torch().uint8), nbytes
+
+
+def groupnorm_forward(X, groups, gamma=None, beta=None, eps=1e-5, act=None, stats=False, workspace=None, out=None,
+                      stream=None):
+    """Group norm of X (N, ..., C), channels last, with an activation (dgrad_groupnorm_forward).
+
+    Each of ``groups`` runs of C/groups adjacent channels is normalised over all positions of its
+    sample.  gamma, beta: (C,) of X's dtype, or None for ones and zeros; act: None or one of
+    ACTIVATIONS.  With ``stats`` the result is (Y, mean, rstd), the fp32 statistics (N, groups) that
+    groupnorm_backward takes.  ``out`` may be X.  workspace: a CUDA tensor of at least
+    groupnorm_forward_workspace_bytes(...) bytes, taken from torch when None."""
+    import torch
+    _need_cuda(X)
+    code = _dtype_code(X)
+    N, S, C, G = _samples_of(X, groups)
+    acode = _norm_act(act)
+    given = [t for t in (gamma, beta, workspace, out) if t is not None]
+    _need_cuda(*given)
+    dev = _device_of(X, *given)
+    for t, what in ((gamma, "gamma"), (beta, "beta")):
+        if t is not None:
+            _like(t, (C,), X.dtype, what)
+    al = _allocator(dev, stream)
+    out = _out(al, out, X, X.shape)
+    mean = rstd = None
+    if stats:
+        mean = _empty(al, X, (N, G), torch.float32)
+        rstd = _empty(al, mean, mean.shape, torch.float32)
+    workspace, ws_bytes = _workspace(al, workspace, X, _gn_workspace(False, N, S, C, G, code))
+    if al is not None:
+        al.uses(X, *given)
+    _call(dev, "dgrad_groupnorm_forward", lib().dgrad_groupnorm_forward, N, S, C, G, code, float(eps), acode,
+          X.data_ptr(), _ptr(gamma), _ptr(beta), out.data_ptr(), _ptr(mean), _ptr(rstd), workspace.data_ptr(), ws_bytes,
+          stream=stream)
+    return (out, mean, rstd) if stats else out
+
+
+def groupnorm_backward(dY, X, mean, rstd, gamma=None, beta=None, act=None, param_grads=True, workspace=None, out=None,
+                       stream=None):
+    """Gradients of groupnorm_forward: (dX, dgamma, dbeta) (dgrad_groupnorm_backward).
+
+    mean, rstd: the forward's statistics (N, groups); gamma, beta and act as in the forward pass.
+    dgamma and dbeta (C,) have X's dtype; without ``param_grads`` they are None and not computed.
+    ``out`` (dX) may be dY or X.  workspace: a CUDA tensor of at least
+    groupnorm_backward_workspace_bytes(...) bytes, taken from torch when None."""
+    import torch
+    _need_cuda(dY, X, mean, rstd)
+    code = _dtype_code(X)
+    if mean.dim() != 2:
+        raise ValueError(f"mean must have shape (N, groups), got {tuple(mean.shape)}")
+    N, S, C, G = _samples_of(X, mean.shape[1])
+    acode = _norm_act(act)
+    _like(dY, X.shape, X.dtype, "dY")
+    _like(mean, (N, G), torch.float32, "mean")
+    _like(rstd, (N, G), torch.float32, "rstd")
+    given = [t for t in (gamma, beta, workspace, out) if t is not None]
+    _need_cuda(*given)
+    dev = _device_of(dY, X, mean, rstd, *given)
+    for t, what in ((gamma, "gamma"), (beta, "beta")):
+        if t is not None:
+            _like(t, (C,), X.dtype, what)
+    al = _allocator(dev, stream)
+    out = _out(al, out, X, X.shape)
+    dgamma = dbeta = None
+    if param_grads:
+        dgamma = _empty(al, X if gamma is None else gamma, (C,), X.dtype)
+        dbeta = _empty(al, dgamma, (C,), X.dtype)
+    workspace, ws_bytes = _workspace(al, workspace, X, _gn_workspace(True, N, S, C, G, code))
+    if al is not None:
+        al.uses(dY, X, mean, rstd, *given)
+    _call(dev, "dgrad_groupnorm_backward", lib().dgrad_groupnorm_backward, N, S, C, G, code, acode, dY.data_ptr(),
+          X.data_ptr(), _ptr(gamma), _ptr(beta), mean.data_ptr(), rstd.data_ptr(), out.data_ptr(), _ptr(dgamma),
+          _ptr(dbeta), workspace.data_ptr(), ws_bytes, stream=stream)
+    return out, dgamma, dbeta
+
+
 def _act_code(act):
     if act not in ACTIVATIONS:
         raise ValueError(f"unknown activation {act!r}; use one of {', '.join(ACTIVATIONS)}")
@@ -728,6 +872,299 @@ def dropout_backward(dY, p, seed, offset=0, out=None, stream=None):
     _call(dev, "dgrad_dropout_backward", lib().dgrad_dropout_backward, dY.numel(), code, float(p),
           _counter(seed, "seed"), _counter(offset, "offset"), dY.data_ptr(), out.data_ptr(), stream=stream)
     return out
+
+
+# ------------------------------------------------ the optimizer's step over many tensors
+
+QUANT_BLOCK = 256   # elements of a tensor that share a maximum in 8-bit states
+
+_TABLE = [("param", "u8"), ("grad", "u8"), ("m", "u8"), ("v", "u8"), ("master", "u8"), ("m_max", "u8"), ("v_max", "u8"),
+          ("n", "i8")]   # dgrad_adamw_tensor_t
+
+
+def _same(ts, what):
+    """The one dtype and CUDA device of a list of contiguous tensors."""
+    if not ts:
+        raise ValueError(f"{what}: expected at least one tensor")
+    _need_cuda(*ts)
+    for t in ts:
+        if t.dtype != ts[0].dtype:
+            raise TypeError(f"{what} must have one dtype, got {ts[0].dtype} and {t.dtype}")
+    return ts[0].dtype, _device_of(*ts)
+
+
+class AdamWState:
+    """Parameters and optimizer states that adamw_step works on: lists of contiguous CUDA tensors of
+    one device, one tensor of each list per parameter.
+
+    params: one dtype.  32-bit states: m, v fp32 of the parameters' shapes.  8-bit states: m int8 and v
+    uint8 codes of the parameters' shapes, and m_max, v_max fp32 with an element for every 256 of a tensor.
+    master: fp32 copies of 16-bit parameters, which are then what is stepped.  No two tensors may
+    share memory.  The tensors stay the caller's (save and load them as they are); a parameter
+    whose storage is replaced later is refused by adamw_step."""
+
+    def __init__(self, params, m, v, master=None, m_max=None, v_max=None):
+        import numpy as np
+        import torch
+        self.params, self.m, self.v = list(params), list(m), list(v)
+        self.master = None if master is None else list(master)
+        dtype, self.device = _same(self.params, "params")
+        self._code = _code_of(dtype)
+        self.dtype = dtype
+        n = len(self.params)
+        self.bits = 8 if (self.m and self.m[0].dtype == torch.int8) else 32
+        if (self.bits == 8) != (m_max is not None) or (self.bits == 8) != (v_max is not None):
+            raise ValueError("m_max and v_max go with int8 m and uint8 v")
+        self.m_max = None if m_max is None else list(m_max)
+        self.v_max = None if v_max is None else list(v_max)
+        lists = [("m", self.m, torch.int8 if self.bits == 8 else torch.float32),
+                 ("v", self.v, torch.uint8 if self.bits == 8 else torch.float32), ("master", self.master, torch.float32)]
+        self.shapes = [tuple(p.shape) for p in self.params]
+        for what, ts, want in lists:
+            if ts is None:
+                continue
+            if len(ts) != n:
+                raise ValueError(f"{what}: expected {n} tensors, got {len(ts)}")
+            for t, shape in zip(ts, self.shapes):
+                _like(t, shape, want, what)
+        for what, ts in (("m_max", self.m_max), ("v_max", self.v_max)):
+            if ts is None:
+                continue
+            if len(ts) != n:
+                raise ValueError(f"{what}: expected {n} tensors, got {len(ts)}")
+            for t, p in zip(ts, self.params):
+                _like(t, (-(-p.numel() // QUANT_BLOCK),), torch.float32, what)
+        everything = [t for ts in (self.params, self.m, self.v, self.master, self.m_max, self.v_max) if ts for t in ts]
+        _need_cuda(*everything)
+        _device_of(*everything)
+        self._all = everything
+        self._table = np.zeros(n, dtype=_TABLE)
+        for name, ts in (("param", self.params), ("m", self.m), ("v", self.v), ("master", self.master),
+                         ("m_max", self.m_max), ("v_max", self.v_max)):
+            if ts is not None:
+                self._table[name] = [t.data_ptr() for t in ts]
+        self._table["n"] = [p.numel() for p in self.params]
+        self._address = self._table.ctypes.data
+        self._where = self._table["param"].tolist()
+        status = lib().dgrad_adamw_check(n, self._address, self._code, self._code, self.bits)
+        if status == 1:
+            raise ValueError("parameters and states must not share memory")
+        _check(status, "dgrad_adamw_check")
+        # the written ranges in order, for the gradients to be held against
+        lo = np.array([t.data_ptr() for t in everything if t.numel()], dtype=np.uint64)
+        size = np.array([t.numel() * t.element_size() for t in everything if t.numel()], dtype=np.uint64)
+        order = np.argsort(lo)
+        self._lo, self._hi = lo[order], (lo + size)[order]
+
+    def __len__(self):
+        return len(self.params)
+
+
+def adamw_state(params, bits=32, master=False):
+    """A fresh AdamWState for `params`: zero moments in 32 or in 8 bits, and with ``master`` fp32 copies of
+    16-bit parameters."""
+    import torch
+    params = list(params)
+    if bits not in (32, 8):
+        raise ValueError(f"bits must be 32 or 8, got {bits}")
+
+    def zeros(dtype):
+        return [torch.zeros(p.shape, dtype=dtype, device=p.device) for p in params]
+
+    def maxima():
+        return [torch.zeros(-(-p.numel() // QUANT_BLOCK), device=p.device) for p in params]
+
+    _same(params, "params")
+    more = {"master": [p.detach().float().clone() for p in params]} if master else {}
+    if bits == 32:
+        return AdamWState(params, zeros(torch.float32), zeros(torch.float32), **more)
+    return AdamWState(params, zeros(torch.int8), zeros(torch.uint8), m_max=maxima(), v_max=maxima(), **more)
+
+
+def _scalar(t, dtype, dev, what):
+    """The device pointer of a one-element tensor."""
+    _need_cuda(t)
+    if t.numel() != 1:
+        raise ValueError(f"{what} must have one element, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    _device_of(t, _On(dev))
+    return t.data_ptr()
+
+
+class _On:
+    """A device, for _device_of."""
+
+    def __init__(self, device):
+        self.device = device
+
+
+def adamw_step(state, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, grad_scale=None, seed=None,
+               offset=0, stream=None) -> None:
+    """One AdamW step over all tensors of `state`, in place (dgrad_adamw_step).
+
+    grads: one tensor per parameter, of its shape and of the parameters' dtype or float32 (one dtype
+    for the list), or None for a parameter that is left as it is.  step counts from 1.  step and lr
+    may be one-element CUDA tensors (int64, float32), which a captured step reads in every replay.
+    grad_scale: a one-element fp32 CUDA tensor that multiplies the gradients (grad_norm's factor); where
+    it is no finite number the step changes nothing.  seed (8-bit states): codes are
+    rounded stochastically by the bits of (seed, offset): give every step its own pair, and dropout others;
+    None: to the nearer value.  Moments and weights are fp32 within the step, and the weights
+    (master copies) are rounded once to the parameters' dtype."""
+    import numpy as np
+    import torch
+    n = len(state.params)
+    grads = list(grads)
+    if len(grads) != n:
+        raise ValueError(f"expected {n} gradients, got {len(grads)}")
+    dev = state.device
+    some = grads
+    shapes = state.shapes
+    if any(g is None for g in grads):
+        some = [g for g in grads if g is not None]
+        shapes = [s for g, s in zip(grads, shapes) if g is not None]
+    dtypes = {g.dtype for g in some}
+    if len(dtypes) > 1:
+        raise TypeError("gradients must have one dtype, got " + ", ".join(sorted(map(str, dtypes))))
+    gcode = _code_of(dtypes.pop()) if dtypes else state._code
+    if gcode != state._code and gcode != 0:
+        raise TypeError(f"gradients must be {state.dtype} or float32")
+    if [g.shape for g in some] != shapes:
+        raise ValueError("gradients must have their parameters' shapes")
+    if not all([g.is_cuda for g in some]):
+        raise ValueError("tensors must be CUDA tensors (no CPU path)")
+    if not all([g.is_contiguous() for g in some]):
+        raise ValueError("tensors must be contiguous")
+    if {g.get_device() for g in some} - {dev.index}:
+        raise ValueError("all tensors of one call must be on the same CUDA device")
+    if [p.data_ptr() for p in state.params] != state._where:
+        raise ValueError("a parameter's storage has changed since its AdamWState was made")
+    at = np.array([0 if g is None else g.data_ptr() for g in grads], dtype=np.uint64)
+    if len(state._lo):
+        size = state._table["n"].astype(np.uint64) * np.uint64(4 if gcode == 0 else 2)
+        k = np.searchsorted(state._hi, at, side="right")
+        if np.any((size > 0) & (at > 0) & (state._lo[np.minimum(k, len(state._lo) - 1)] < at + size) & (k < len(state._lo))):
+            raise ValueError("gradients must not share memory with parameters or states")
+    state._table["grad"] = at
+    h = _AdamW()
+    given = []
+    if isinstance(lr, torch.Tensor):
+        h.lr_device = _scalar(lr, torch.float32, dev, "lr")
+        given.append(lr)
+    else:
+        h.lr = float(lr)
+    if isinstance(step, torch.Tensor):
+        h.step_device = _scalar(step, torch.int64, dev, "step")
+        given.append(step)
+    else:
+        h.step = int(step)
+    if grad_scale is not None:
+        h.grad_scale = _scalar(grad_scale, torch.float32, dev, "grad_scale")
+        given.append(grad_scale)
+    h.beta1, h.beta2 = betas
+    h.eps, h.weight_decay, h.state_bits = eps, weight_decay, state.bits
+    if seed is not None:
+        if state.bits != 8:
+            raise ValueError("seed goes with 8-bit states")
+        h.stochastic, h.seed, h.offset = 1, _counter(seed, "seed"), _counter(offset, "offset")
+    al = _allocator(dev, stream)
+    if al is not None:
+        al.uses(*some, *given, *state._all)
+    _call(dev, "dgrad_adamw_step", lib().dgrad_adamw_step, n, state._address, state._code, gcode, ctypes.byref(h),
+          stream=stream)
+
+
+def adamw_moments(state, out=None, stream=None):
+    """(m, v): what a state's moments stand for, as lists of fp32 tensors (dgrad_adamw_moments): for
+    checkpoints, or to go on with 32-bit states.  32-bit states are returned as they are.  out: two lists of
+    fp32 tensors of the parameters' shapes to write to."""
+    import numpy as np
+    import torch
+    if state.bits == 32 and out is None:
+        return state.m, state.v
+    if state.bits == 32:
+        raise ValueError("32-bit moments are state.m and state.v")
+    dev = state.device
+    al = _allocator(dev, stream)
+    given = []
+    if out is None:
+        out = tuple([_empty(al, state.m_max[i], s, torch.float32) for i, s in enumerate(state.shapes)] for _ in range(2))
+    else:
+        out = tuple(list(ts) for ts in out)
+        if len(out) != 2:
+            raise ValueError("out: expected two lists of tensors")
+        for ts, what in zip(out, ("m", "v")):
+            if [t.shape for t in ts] != state.shapes:
+                raise ValueError(f"out: {what} must have the parameters' shapes")
+            if {t.dtype for t in ts} != {torch.float32}:
+                raise TypeError(f"out: {what} must be float32")
+            if not all([t.is_cuda and t.is_contiguous() for t in ts]):
+                raise ValueError("tensors must be contiguous CUDA tensors")
+            if {t.get_device() for t in ts} != {dev.index}:
+                raise ValueError("all tensors of one call must be on the same CUDA device")
+        given = out[0] + out[1]
+    to = np.array([[t.data_ptr() for t in ts] for ts in out], dtype=np.uint64)
+    size = state._table["n"].astype(np.uint64) * np.uint64(4)
+    if given:
+        lo = np.concatenate([state._lo, *[to[i][size > 0] for i in range(2)]])
+        hi = np.concatenate([state._hi, *[(to[i] + size)[size > 0] for i in range(2)]])
+        order = np.argsort(lo, kind="stable")
+        if np.any(lo[order][1:] < np.maximum.accumulate(hi[order])[:-1]):
+            raise ValueError("out must not share memory with itself or the state")
+    if al is not None:
+        al.uses(*given, *state._all)
+    _call(dev, "dgrad_adamw_moments", lib().dgrad_adamw_moments, len(state), state._address, to[0].ctypes.data,
+          to[1].ctypes.data, stream=stream)
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_workspace(count) -> int:
+    nb = ctypes.c_size_t()
+    _check(lib().dgrad_grad_norm_workspace(count, ctypes.byref(nb)), "dgrad_grad_norm_workspace")
+    return nb.value
+
+
+def grad_norm_workspace_bytes(count) -> int:
+    """Workspace bytes grad_norm needs for a list of `count` tensors (host only)."""
+    return _norm_workspace(int(count))
+
+
+def grad_norm(grads, max_norm=None, workspace=None, stream=None):
+    """The norm over all elements of `grads` (contiguous, one dtype and device), a fp32 CUDA scalar
+    (dgrad_grad_norm).  With max_norm: (norm, scale) with scale = min(1, max_norm/(norm + 1e-6)), the
+    grad_scale that clips an adamw_step; NaN where the norm is no finite number, which leaves that step
+    out.  Nothing waits for the GPU."""
+    import numpy as np
+    import torch
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads: expected at least one tensor")
+    first = grads[0]
+    if not all([g.is_cuda for g in grads]):
+        raise ValueError("tensors must be CUDA tensors (no CPU path)")
+    if not all([g.is_contiguous() for g in grads]):
+        raise ValueError("tensors must be contiguous")
+    if len({g.dtype for g in grads}) != 1:
+        raise TypeError("gradients must have one dtype")
+    code = _code_of(first.dtype)
+    dev = first.device
+    if {g.get_device() for g in grads} != {dev.index}:
+        raise ValueError("all tensors of one call must be on the same CUDA device")
+    limit = float("inf") if max_norm is None else float(max_norm)
+    given = [] if workspace is None else [workspace]
+    _need_cuda(*given)
+    _device_of(first, *given)
+    al = _allocator(dev, stream)
+    out = _empty(al, first, (2,), torch.float32)
+    workspace, ws_bytes = _workspace(al, workspace, first, _norm_workspace(len(grads)))
+    if al is not None:
+        al.uses(*grads, *given)
+    at = np.array([g.data_ptr() for g in grads], dtype=np.uint64)
+    n = np.array([g.numel() for g in grads], dtype=np.int64)
+    _call(dev, "dgrad_grad_norm", lib().dgrad_grad_norm, len(grads), at.ctypes.data, n.ctypes.data, code, limit,
+          out.data_ptr(), workspace.data_ptr(), ws_bytes, stream=stream)
+    return out[0] if max_norm is None else (out[0], out[1])
 
 
 def check_status(stream=None) -> None:

@@ -1,0 +1,737 @@
+// adamw.cu -- the AdamW step over many tensors at once (states in 32 or in 8 bits) and the
+// norm of many gradients.
+//
+// For each element, all in fp32, with g = scale * grad:
+//     m' = b1 m + (1 - b1) g,   v' = b2 v + (1 - b2) g g
+//     p' = p (1 - lr wd) - lr (m' / (1 - b1^t)) / (sqrt(v' / (1 - b2^t)) + eps)
+// A handful of operations for 22 to 28 bytes: HBM bounds it.  A launch takes a table of
+// tensors among its parameters (no copy to the device, nothing kept between calls, so a
+// captured step carries its own), and its blocks take equal runs of 1024-element chunks.
+//
+// 8-bit states.  Blocks of 256 elements of a tensor share the largest |m| and the largest v
+// (fp32, M and V).  Codes are linear in the square root of a gradient's magnitude:
+//     m = c|c| / 127^2 * M, c in -127 .. 127,    v = (c / 255)^4 * V, c in 0 .. 255
+// so that both reach down to 6e-5 (m) and 1.5e-5 (v's root) of a block's largest gradient with
+// steps of 2/c and 4/c of the value: 1.6% next to the largest, where a linear code's 0.4% of
+// the largest would be 100% of what lies 250 times below.  A v' above zero keeps a code above
+// zero: m / sqrt(0) would be a step of any size.
+// A code stands for the nearer of two values (the lower at a tie), or with a seed for the upper with
+// probability (w - low)/(high - low): what nearest rounding keeps losing, a v that moves by less
+// than half a step at a time, adds up on average.  The stored bits are defined by fp32
+// operations each rounded on its own (no fused multiply-add), given beside code_of, so that
+// a step's states can be reproduced exactly.  A warp holds a block: one reduction for M, one for V.
+//
+// Random bits: Philox-4x32-10 (J. Salmon, M. Moraes, R. Dror and D. Shaw, "Parallel random
+// numbers: as easy as 1, 2, 3", 2011) at counter (b, offset) and key seed; elements are counted
+// with every tensor rounded up to whole blocks of 256, element i takes word i % 4 of b = i / 4, its low
+// half for m, its high half for v.
+#include "common.cuh"
+#include "host_util.h"
+#include "launchers.h"
+#include "rowvec.cuh"
+
+namespace dgrad {
+namespace {
+
+constexpr int kOptBlock = 256;                  // threads
+constexpr int kQuant = 256;                     // elements that share M and V: a warp's
+constexpr int kOptChunk = kQuant * (kOptBlock / 32);   // elements a block takes at a time
+constexpr int kSteps = kQuant / (32 * 4);       // vectors of four a thread takes of it
+
+constexpr int kFewTensors = 24, kManyTensors = 380;   // tables; a launch's parameters hold 32764 bytes
+
+struct OptHyper {
+    float lr, b1, c1, b2, c2, eps, decay, wd, ibc1, ibc2, ln_b1, ln_b2;
+    const float* lr_dev;         // null: lr and decay above
+    const long long* step_dev;   // null: ibc1 and ibc2 above
+    const float* scale;          // null: 1
+    uint32_t seed_lo, seed_hi, off_lo, off_hi;
+    int* status;
+};
+
+struct AdamTensor {
+    void* p;
+    const void* g;
+    void* m;
+    void* v;
+    float* w;
+    float* m_max;
+    float* v_max;
+    long long n;
+    long long block0;   // quantisation blocks before it
+    int vec;            // every pointer is aligned for four elements
+};
+
+template <int CAP>
+struct OptTable {
+    OptHyper h;
+    int count;
+    unsigned chunks;              // of all tensors
+    unsigned first[CAP + 1];      // a tensor's first chunk
+    AdamTensor t[CAP];
+};
+
+// Four elements of kind EK at element i of p (16-byte vectors of fp32, 8-byte of 16 bits), or the
+// `have` that there are.
+template <int EK>
+__device__ __forceinline__ float4 load4(const void* p, long long i, int have, bool vec)
+{
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
+    if (have == 4 && vec) {
+        if constexpr (EK == kF32) {
+            return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+            const float2 a = h16x2_to_float2<EK>(u.x), b = h16x2_to_float2<EK>(u.y);
+            return make_float4(a.x, a.y, b.x, b.y);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (k < have) {
+            RowVec<EK, 1> v;
+            float e[1];
+            v.load(p, i + k);
+            v.unpack(e);
+            f[k] = e[0];
+        }
+    return make_float4(f[0], f[1], f[2], f[3]);
+}
+
+template <int EK>
+__device__ __forceinline__ void store4(void* p, long long i, int have, bool vec, float4 x, long long n, int* status)
+{
+    constexpr int es = elem_bytes<EK>();
+    char* at = static_cast<char*>(p) + i * es;
+    if (have == 4 && vec) {
+        if (!store_ok(p, n * es, at, 4 * es, status)) return;
+        if constexpr (EK == kF32)
+            *reinterpret_cast<float4*>(at) = x;
+        else
+            *reinterpret_cast<uint2*>(at) = make_uint2(float2_to_h16x2<EK>(x.x, x.y), float2_to_h16x2<EK>(x.z, x.w));
+        return;
+    }
+    const float f[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (k < have && store_ok(p, n * es, at + k * es, es, status)) {
+            RowVec<EK, 1> v;
+            const float e[1] = {f[k]};
+            v.pack(e);
+            v.store(p, i + k);
+        }
+}
+
+__device__ __forceinline__ uint32_t load_codes(const void* p, long long i, int have, bool vec)
+{
+    const uint8_t* c = static_cast<const uint8_t*>(p) + i;
+    if (have == 4 && vec) return *reinterpret_cast<const uint32_t*>(c);
+    uint32_t w = 0;
+    for (int k = 0; k < have; ++k) w |= static_cast<uint32_t>(c[k]) << (8 * k);
+    return w;
+}
+
+__device__ __forceinline__ void store_codes(void* p, long long i, int have, bool vec, uint32_t w, long long n, int* status)
+{
+    uint8_t* c = static_cast<uint8_t*>(p) + i;
+    if (have == 4 && vec) {
+        if (store_ok(p, n, c, 4, status)) *reinterpret_cast<uint32_t*>(c) = w;
+        return;
+    }
+    for (int k = 0; k < have; ++k)
+        if (store_ok(p, n, c + k, 1, status)) c[k] = static_cast<uint8_t>(w >> (8 * k));
+}
+
+__device__ __forceinline__ float elem(const float4& v, int k) { return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w; }
+
+__device__ __forceinline__ uint4 opt_philox(const OptHyper& h, unsigned long long b)
+{
+    uint32_t c0 = static_cast<uint32_t>(b), c1 = static_cast<uint32_t>(b >> 32), c2 = h.off_lo, c3 = h.off_hi;
+    uint32_t k0 = h.seed_lo, k1 = h.seed_hi;
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * c0;
+        const uint64_t p1 = static_cast<uint64_t>(0xCD9E8D57u) * c2;
+        c0 = static_cast<uint32_t>(p1 >> 32) ^ c1 ^ k0;
+        c1 = static_cast<uint32_t>(p1);
+        c2 = static_cast<uint32_t>(p0 >> 32) ^ c3 ^ k1;
+        c3 = static_cast<uint32_t>(p0);
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return make_uint4(c0, c1, c2, c3);
+}
+
+// Values that codes stand for, as multiples of 1/127^2 and 1/255^4 of the block's largest.
+template <bool FOURTH>
+__device__ __forceinline__ float code_value(float c)
+{
+    const float q = __fmul_rn(c, c);
+    return FOURTH ? __fmul_rn(q, q) : q;
+}
+constexpr float kMostM = 16129.0f, kMostV = 4228250625.0f;                 // value(127), value(255)
+constexpr float kUnitM = static_cast<float>(1.0 / 16129.0), kUnitV = static_cast<float>(1.0 / 4228250625.0);
+
+__device__ __forceinline__ float decode_m(int c, float top)
+{
+    const float f = static_cast<float>(c);
+    return __fmul_rn(__fmul_rn(__fmul_rn(f, fabsf(f)), kUnitM), top);
+}
+__device__ __forceinline__ float decode_v(uint32_t c, float top)
+{
+    return __fmul_rn(__fmul_rn(code_value<true>(static_cast<float>(c)), kUnitV), top);
+}
+
+// What a block's largest value scales the others by: w = (x k) inv, with k a power of two that
+// keeps inv = (1/(top k)) value(most) an ordinary number.  With a NaN for the largest value its whole
+// block stands for NaN, whatever the codes.
+struct CodeScale {
+    float k, inv;
+};
+template <bool FOURTH>
+__device__ __forceinline__ CodeScale code_scale(float top)
+{
+    CodeScale s;
+    s.k = top < 0x1p-60f ? 0x1p64f : top > 0x1p60f ? 0x1p-64f : 1.0f;
+    s.inv = top > 0.f ? __fmul_rn(__frcp_rn(__fmul_rn(top, s.k)), FOURTH ? kMostV : kMostM) : 0.f;
+    return s;
+}
+
+// The code of x >= 0: low is the largest c with value(c) <= w; the upper neighbour is taken where
+// (w - value(low)) 65536 > (value(low + 1) - value(low)) draw; nearest: draw = 32768.  The
+// approximate roots (2^-22) find low or, so lowered by 2^-10, the code below it.
+template <bool FOURTH>
+__device__ __forceinline__ int code_of(float x, const CodeScale& s, float draw)
+{
+    constexpr float kTop = FOURTH ? 255.0f : 127.0f;
+    const float w = __fmul_rn(__fmul_rn(x, s.k), s.inv);
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(w));
+    if constexpr (FOURTH) asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(r));
+    float low = fmaxf(rintf(r - (0.5f + 0x1p-10f)), 0.f);
+    float at = code_value<FOURTH>(low), up = code_value<FOURTH>(low + 1.f);
+    if (up <= w) {
+        low += 1.f;
+        at = up;
+        up = code_value<FOURTH>(low + 1.f);
+    }
+    if (__fmul_rn(__fsub_rn(w, at), 65536.f) > __fmul_rn(__fsub_rn(up, at), draw)) low += 1.f;
+    if (FOURTH && x > 0.f) low = fmaxf(low, 1.f);
+    return static_cast<int>(fminf(low, kTop));
+}
+
+// The largest of a warp's values >= 0 (the order of the bits is that of the values); NaN where
+// one is no finite number.
+__device__ __forceinline__ float warp_largest(float x)
+{
+    const uint32_t big = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x) & 0x7FFFFFFFu);
+    return __uint_as_float(big >= 0x7F800000u ? 0x7FC00000u : big);
+}
+
+// The step's scalars, once per block.
+struct OptStep {
+    float scale, nlr, decay, ibc1, ibc2;
+    bool skip;
+};
+__device__ __forceinline__ OptStep opt_step(const OptHyper& h)
+{
+    OptStep s{1.f, -h.lr, h.decay, h.ibc1, h.ibc2, false};
+    if (h.scale) {
+        s.scale = *h.scale;
+        s.skip = !isfinite(s.scale);
+    }
+    if (h.lr_dev) {
+        const float lr = *h.lr_dev;
+        s.nlr = -lr;
+        s.decay = fmaf(-lr, h.wd, 1.f);
+    }
+    if (h.step_dev) {
+        const float t = static_cast<float>(*h.step_dev);
+        s.ibc1 = -1.f / expm1f(t * h.ln_b1);
+        s.ibc2 = -1.f / expm1f(t * h.ln_b2);
+    }
+    return s;
+}
+
+__device__ __forceinline__ float new_weight(float w, float m, float v, const OptHyper& h, const OptStep& s)
+{
+    float root, inv;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v * s.ibc2));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(root + h.eps));
+    return fmaf(s.nlr, m * s.ibc1 * inv, w * s.decay);
+}
+
+__device__ __forceinline__ float new_m(float m, float g, const OptHyper& h)
+{
+    return __fadd_rn(__fmul_rn(m, h.b1), __fmul_rn(g, h.c1));
+}
+__device__ __forceinline__ float new_v(float v, float g, const OptHyper& h)
+{
+    return __fadd_rn(__fmul_rn(v, h.b2), __fmul_rn(__fmul_rn(g, h.c2), g));
+}
+
+// PK, GK: the parameters' and gradients' types; MASTER: an fp32 copy of the parameters is what is
+// stepped.  MODE 0: fp32 states; 1: 8 bits, nearest; 2: 8 bits, stochastic.
+template <int PK, int GK, bool MASTER, int MODE, int CAP>
+__global__ void __launch_bounds__(kOptBlock) adamw_kernel(const __grid_constant__ OptTable<CAP> tab)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // equal runs of chunks
+    const unsigned each = tab.chunks / gridDim.x, more = tab.chunks % gridDim.x;
+    unsigned c = blockIdx.x * each + min(blockIdx.x, more);
+    const unsigned end = c + each + (blockIdx.x < more ? 1 : 0);
+    int lo = 0, hi = tab.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tab.first[mid] <= c)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    pdl_wait();
+    pdl_trigger();
+    const OptHyper& h = tab.h;
+    const OptStep st = opt_step(h);
+    if (st.skip) return;
+    for (; c < end; ++c) {
+        while (tab.first[lo + 1] <= c) ++lo;
+        const AdamTensor& t = tab.t[lo];
+        const long long q = static_cast<long long>(c - tab.first[lo]) * (kOptBlock / 32) + warp;   // block of 256
+        const long long i0 = q * kQuant + lane * 4;
+        if (q * kQuant >= t.n) continue;
+        const bool vec = t.vec != 0;
+        float4 g[kSteps], w[kSteps], m[kSteps], v[kSteps];
+        uint32_t cm[kSteps], cv[kSteps];
+        float mtop = 0.f, vtop = 0.f;
+        if constexpr (MODE != 0) {
+            mtop = t.m_max[q];
+            vtop = t.v_max[q];
+        }
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+            const long long i = i0 + j * 128;
+            const int have = static_cast<int>(max(0LL, min(4LL, t.n - i)));
+            g[j] = load4<GK>(t.g, i, have, vec);
+            w[j] = MASTER ? load4<kF32>(t.w, i, have, vec) : load4<PK>(t.p, i, have, vec);
+            if constexpr (MODE == 0) {
+                m[j] = load4<kF32>(t.m, i, have, vec);
+                v[j] = load4<kF32>(t.v, i, have, vec);
+            } else {
+                cm[j] = load_codes(t.m, i, have, vec);
+                cv[j] = load_codes(t.v, i, have, vec);
+            }
+        }
+        float big_m = 0.f, big_v = 0.f;
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+            float mm[4], vv[4], ww[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float gs = __fmul_rn(elem(g[j], k), st.scale);
+                float om, ov;
+                if constexpr (MODE == 0) {
+                    om = elem(m[j], k);
+                    ov = elem(v[j], k);
+                } else {
+                    om = decode_m(static_cast<int8_t>(cm[j] >> (8 * k)), mtop);
+                    ov = decode_v((cv[j] >> (8 * k)) & 0xFFu, vtop);
+                }
+                mm[k] = new_m(om, gs, h);
+                vv[k] = new_v(ov, gs, h);
+                ww[k] = new_weight(elem(w[j], k), mm[k], vv[k], h, st);
+                if constexpr (MODE != 0) {
+                    // the order of the bits is that of the values, and a NaN's lie above
+                    big_m = __uint_as_float(max(__float_as_uint(big_m), __float_as_uint(mm[k]) & 0x7FFFFFFFu));
+                    big_v = __uint_as_float(max(__float_as_uint(big_v), __float_as_uint(vv[k]) & 0x7FFFFFFFu));
+                }
+            }
+            m[j] = make_float4(mm[0], mm[1], mm[2], mm[3]);
+            v[j] = make_float4(vv[0], vv[1], vv[2], vv[3]);
+            w[j] = make_float4(ww[0], ww[1], ww[2], ww[3]);
+        }
+        CodeScale sm, sv;
+        if constexpr (MODE != 0) {
+            big_m = warp_largest(big_m);
+            big_v = warp_largest(big_v);
+            sm = code_scale<false>(big_m);
+            sv = code_scale<true>(big_v);
+            const long long nq = (t.n + kQuant - 1) / kQuant;
+            if (lane == 0 && store_ok(t.m_max, nq * 4, t.m_max + q, 4, h.status)) t.m_max[q] = big_m;
+            if (lane == 0 && store_ok(t.v_max, nq * 4, t.v_max + q, 4, h.status)) t.v_max[q] = big_v;
+        }
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+            const long long i = i0 + j * 128;
+            const int have = static_cast<int>(max(0LL, min(4LL, t.n - i)));
+            if (MASTER) store4<kF32>(t.w, i, have, vec, w[j], t.n, h.status);
+            store4<PK>(t.p, i, have, vec, w[j], t.n, h.status);
+            if constexpr (MODE == 0) {
+                store4<kF32>(t.m, i, have, vec, m[j], t.n, h.status);
+                store4<kF32>(t.v, i, have, vec, v[j], t.n, h.status);
+            } else {
+                uint4 bits = make_uint4(0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u);
+                if constexpr (MODE == 2)
+                    bits = opt_philox(h, static_cast<unsigned long long>(t.block0 + q) * (kQuant / 4) + lane + j * 32);
+                const uint32_t word[4] = {bits.x, bits.y, bits.z, bits.w};
+                uint32_t om = 0, ov = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float x = elem(m[j], k);
+                    const int a = code_of<false>(fabsf(x), sm, static_cast<float>(word[k] & 0xFFFFu));
+                    const int b = code_of<true>(elem(v[j], k), sv, static_cast<float>(word[k] >> 16));
+                    om |= (static_cast<uint32_t>(x < 0.f ? -a : a) & 0xFFu) << (8 * k);
+                    ov |= static_cast<uint32_t>(b) << (8 * k);
+                }
+                store_codes(t.m, i, have, vec, om, t.n, h.status);
+                store_codes(t.v, i, have, vec, ov, t.n, h.status);
+            }
+        }
+    }
+}
+
+// ------------------------------------------- what 8-bit states stand for, as fp32
+
+struct MomentTensor {
+    const void* m;
+    const void* v;
+    const float* m_max;
+    const float* v_max;
+    float* m_out;
+    float* v_out;
+    long long n;
+    int vec;
+};
+
+template <int CAP>
+struct MomentTable {
+    int count;
+    unsigned chunks;
+    int* status;
+    unsigned first[CAP + 1];
+    MomentTensor t[CAP];
+};
+
+template <int CAP>
+__global__ void __launch_bounds__(kOptBlock) moments_kernel(const __grid_constant__ MomentTable<CAP> tab)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned each = tab.chunks / gridDim.x, more = tab.chunks % gridDim.x;
+    unsigned c = blockIdx.x * each + min(blockIdx.x, more);
+    const unsigned end = c + each + (blockIdx.x < more ? 1 : 0);
+    int lo = 0, hi = tab.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tab.first[mid] <= c)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    pdl_wait();
+    pdl_trigger();
+    for (; c < end; ++c) {
+        while (tab.first[lo + 1] <= c) ++lo;
+        const MomentTensor& t = tab.t[lo];
+        const long long q = static_cast<long long>(c - tab.first[lo]) * (kOptBlock / 32) + warp;
+        if (q * kQuant >= t.n) continue;
+        const bool vec = t.vec != 0;
+        const float mtop = t.m_max[q], vtop = t.v_max[q];
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+            const long long i = q * kQuant + lane * 4 + j * 128;
+            const int have = static_cast<int>(max(0LL, min(4LL, t.n - i)));
+            const uint32_t cm = load_codes(t.m, i, have, vec), cv = load_codes(t.v, i, have, vec);
+            float m[4], v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                m[k] = decode_m(static_cast<int8_t>(cm >> (8 * k)), mtop);
+                v[k] = decode_v((cv >> (8 * k)) & 0xFFu, vtop);
+            }
+            store4<kF32>(t.m_out, i, have, vec, make_float4(m[0], m[1], m[2], m[3]), t.n, tab.status);
+            store4<kF32>(t.v_out, i, have, vec, make_float4(v[0], v[1], v[2], v[3]), t.n, tab.status);
+        }
+    }
+}
+
+// ----------------------------------------------------------- the gradients' norm
+
+constexpr int kFewNorms = 64, kManyNorms = 1600;
+constexpr int kNormChunk = 4096;     // elements a block takes at a time: 16 a thread
+
+struct NormTensor {
+    const void* g;
+    long long n : 63;
+    unsigned long long vec : 1;   // on 16 bytes
+};
+
+template <int CAP>
+struct NormTable {
+    int count;
+    unsigned chunks;
+    double* part;                 // one sum per block of this launch
+    int* status;
+    unsigned first[CAP + 1];
+    NormTensor t[CAP];
+};
+
+// Squares of fp32 values are exact in 64 bits, and their sums need not fear overflow, order or
+// length.  The sum of a thread's 16 squares is formed first, so that its chain is short.
+template <int EK, int CAP>
+__global__ void __launch_bounds__(kOptBlock) norm_kernel(const __grid_constant__ NormTable<CAP> tab)
+{
+    __shared__ double warps[kOptBlock / 32];
+    const unsigned each = tab.chunks / gridDim.x, more = tab.chunks % gridDim.x;
+    unsigned c = blockIdx.x * each + min(blockIdx.x, more);
+    const unsigned end = c + each + (blockIdx.x < more ? 1 : 0);
+    int lo = 0, hi = tab.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tab.first[mid] <= c)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    pdl_wait();
+    pdl_trigger();
+    double sum = 0.0;
+    constexpr int VEC = 16 / elem_bytes<EK>();
+    constexpr int NV = kNormChunk / (kOptBlock * VEC);
+    for (; c < end; ++c) {
+        while (tab.first[lo + 1] <= c) ++lo;
+        const NormTensor& t = tab.t[lo];
+        const long long i0 = static_cast<long long>(c - tab.first[lo]) * kNormChunk;
+        if (t.vec && i0 + kNormChunk <= t.n) {
+            RowVec<EK, VEC> v[NV];
+#pragma unroll
+            for (int j = 0; j < NV; ++j) v[j].load(t.g, i0 + (j * kOptBlock + threadIdx.x) * VEC);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                float f[VEC];
+                v[j].unpack(f);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) sum = fma(static_cast<double>(f[k]), static_cast<double>(f[k]), sum);
+            }
+        } else {
+            const long long i1 = min(t.n, i0 + kNormChunk);
+            for (long long i = i0 + threadIdx.x; i < i1; i += kOptBlock) {
+                RowVec<EK, 1> v;
+                float f[1];
+                v.load(t.g, i);
+                v.unpack(f);
+                sum = fma(static_cast<double>(f[0]), static_cast<double>(f[0]), sum);
+            }
+        }
+    }
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kOptBlock / 32; ++w) sum += warps[w];
+        tab.part[blockIdx.x] = sum;
+    }
+}
+
+// out[0] = the root of the sum of n parts, out[1] = min(1, max_norm/(out[0] + 1e-6)), NaN where
+// the norm is no finite number.
+__global__ void __launch_bounds__(kOptBlock) norm_join_kernel(const double* part, int n, float max_norm, float* out, int* status)
+{
+    __shared__ double warps[kOptBlock / 32];
+    pdl_wait();
+    pdl_trigger();
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < n; i += kOptBlock) sum += part[i];
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0 && store_ok(out, 8, out, 8, status)) {
+        for (int w = 1; w < kOptBlock / 32; ++w) sum += warps[w];
+        const float norm = static_cast<float>(sqrt(sum));
+        out[0] = norm;
+        out[1] = isfinite(norm) ? fminf(max_norm / (norm + 1e-6f), 1.f) : __int_as_float(0x7FC00000);
+    }
+}
+
+template <int EK>
+bool on4(const void* p)   // aligned for four elements of kind EK
+{
+    return (reinterpret_cast<uintptr_t>(p) & (4 * elem_bytes<EK>() - 1)) == 0;
+}
+
+// Runs of at most CAP tensors; f(begin, end).
+template <typename F>
+cudaError_t in_runs(int64_t count, int cap, F f)
+{
+    for (int64_t i = 0; i < count; i += cap) {
+        const cudaError_t e = f(i, count - i < cap ? count : i + cap);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+unsigned opt_grid(unsigned chunks, int per_sm)
+{
+    const unsigned most = static_cast<unsigned>(device_sm_count() * per_sm);
+    return chunks < most ? chunks : most;
+}
+
+template <int PK, int GK, bool MASTER, int MODE, int CAP>
+cudaError_t adamw_run(const AdamWArgs& a, const OptHyper& h, int64_t begin, int64_t end, int64_t& block0, cudaStream_t stream)
+{
+    OptTable<CAP> tab;
+    tab.h = h;
+    tab.count = 0;
+    unsigned chunks = 0;
+    for (int64_t i = begin; i < end; ++i) {
+        const dgrad_adamw_tensor_t& s = a.t[i];
+        const int64_t at = block0;
+        block0 += (s.n + kQuant - 1) / kQuant;
+        if (!s.grad || s.n == 0) continue;
+        bool vec = on4<PK>(s.param) && on4<GK>(s.grad) && (!MASTER || on4<kF32>(s.master));
+        if (MODE == 0)
+            vec = vec && on4<kF32>(s.m) && on4<kF32>(s.v);
+        else
+            vec = vec && ((reinterpret_cast<uintptr_t>(s.m) | reinterpret_cast<uintptr_t>(s.v)) & 3) == 0;
+        tab.first[tab.count] = chunks;
+        tab.t[tab.count++] = {s.param, s.grad, s.m, s.v, s.master, s.m_max, s.v_max, s.n, at, vec};
+        chunks += static_cast<unsigned>((s.n + kOptChunk - 1) / kOptChunk);
+    }
+    tab.first[tab.count] = chunks;
+    tab.chunks = chunks;
+    if (chunks == 0) return cudaSuccess;
+    return launch_kernel(adamw_kernel<PK, GK, MASTER, MODE, CAP>, dim3(opt_grid(chunks, 8)), dim3(kOptBlock), 0, stream, 1, tab);
+}
+
+template <int PK, int GK, bool MASTER, int MODE>
+cudaError_t adamw_all(const AdamWArgs& a, const OptHyper& h, cudaStream_t stream)
+{
+    const int cap = a.count <= kFewTensors ? kFewTensors : kManyTensors;
+    int64_t block0 = 0;
+    return in_runs(a.count, cap, [&](int64_t b, int64_t e) {
+        return cap == kFewTensors ? adamw_run<PK, GK, MASTER, MODE, kFewTensors>(a, h, b, e, block0, stream)
+                                  : adamw_run<PK, GK, MASTER, MODE, kManyTensors>(a, h, b, e, block0, stream);
+    });
+}
+
+template <int PK, int GK, bool MASTER>
+cudaError_t adamw_mode(const AdamWArgs& a, const OptHyper& h, cudaStream_t stream)
+{
+    return a.bits == 32 ? adamw_all<PK, GK, MASTER, 0>(a, h, stream)
+           : a.stochastic ? adamw_all<PK, GK, MASTER, 2>(a, h, stream)
+                          : adamw_all<PK, GK, MASTER, 1>(a, h, stream);
+}
+
+template <int PK>
+cudaError_t adamw_types(const AdamWArgs& a, const OptHyper& h, cudaStream_t stream)
+{
+    if constexpr (PK == kF32) {
+        return adamw_mode<kF32, kF32, false>(a, h, stream);
+    } else {
+        if (a.gk == kF32) return a.master ? adamw_mode<PK, kF32, true>(a, h, stream) : adamw_mode<PK, kF32, false>(a, h, stream);
+        return a.master ? adamw_mode<PK, PK, true>(a, h, stream) : adamw_mode<PK, PK, false>(a, h, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_adamw(const AdamWArgs& a, cudaStream_t stream)
+{
+    OptHyper h{};
+    h.lr = static_cast<float>(a.lr);
+    h.b1 = static_cast<float>(a.beta1);
+    h.c1 = static_cast<float>(1.0 - a.beta1);
+    h.b2 = static_cast<float>(a.beta2);
+    h.c2 = static_cast<float>(1.0 - a.beta2);
+    h.eps = static_cast<float>(a.eps);
+    h.wd = static_cast<float>(a.weight_decay);
+    h.decay = static_cast<float>(1.0 - a.lr * a.weight_decay);
+    h.ibc1 = static_cast<float>(a.bias1);
+    h.ibc2 = static_cast<float>(a.bias2);
+    h.ln_b1 = static_cast<float>(a.ln_beta1);
+    h.ln_b2 = static_cast<float>(a.ln_beta2);
+    h.lr_dev = a.lr_dev;
+    h.step_dev = reinterpret_cast<const long long*>(a.step_dev);
+    h.scale = a.scale;
+    h.seed_lo = static_cast<uint32_t>(a.seed);
+    h.seed_hi = static_cast<uint32_t>(a.seed >> 32);
+    h.off_lo = static_cast<uint32_t>(a.offset);
+    h.off_hi = static_cast<uint32_t>(a.offset >> 32);
+    h.status = a.status;
+    return a.pk == kF32 ? adamw_types<kF32>(a, h, stream) : a.pk == kBF16 ? adamw_types<kBF16>(a, h, stream) : adamw_types<kF16>(a, h, stream);
+}
+
+cudaError_t launch_adamw_moments(const dgrad_adamw_tensor_t* t, float* const* m_out, float* const* v_out, int64_t count,
+                                 int* status, cudaStream_t stream)
+{
+    return in_runs(count, kManyTensors, [&](int64_t begin, int64_t end) {
+        MomentTable<kManyTensors> tab;
+        tab.count = 0;
+        tab.status = status;
+        unsigned chunks = 0;
+        for (int64_t i = begin; i < end; ++i) {
+            if (t[i].n == 0) continue;
+            const bool vec = ((reinterpret_cast<uintptr_t>(t[i].m) | reinterpret_cast<uintptr_t>(t[i].v)) & 3) == 0 &&
+                             ((reinterpret_cast<uintptr_t>(m_out[i]) | reinterpret_cast<uintptr_t>(v_out[i])) & 15) == 0;
+            tab.first[tab.count] = chunks;
+            tab.t[tab.count++] = {t[i].m, t[i].v, t[i].m_max, t[i].v_max, m_out[i], v_out[i], t[i].n, vec};
+            chunks += static_cast<unsigned>((t[i].n + kOptChunk - 1) / kOptChunk);
+        }
+        tab.first[tab.count] = chunks;
+        tab.chunks = chunks;
+        if (chunks == 0) return cudaSuccess;
+        return launch_kernel(moments_kernel<kManyTensors>, dim3(opt_grid(chunks, 8)), dim3(kOptBlock), 0, stream, 1, tab);
+    });
+}
+
+namespace {
+
+constexpr int kNormBlocks = 148 * 8;   // sums a launch leaves at most
+
+template <int EK, int CAP>
+cudaError_t norm_runs(const NormArgs& a, int& parts, cudaStream_t stream)
+{
+    return in_runs(a.count, CAP, [&](int64_t begin, int64_t end) {
+        NormTable<CAP> tab;
+        tab.count = 0;
+        tab.status = a.status;
+        unsigned chunks = 0;
+        for (int64_t i = begin; i < end; ++i) {
+            if (a.n[i] == 0) continue;
+            tab.first[tab.count] = chunks;
+            tab.t[tab.count].g = a.g[i];
+            tab.t[tab.count].n = a.n[i];
+            tab.t[tab.count++].vec = (reinterpret_cast<uintptr_t>(a.g[i]) & 15) == 0;
+            chunks += static_cast<unsigned>((a.n[i] + kNormChunk - 1) / kNormChunk);
+        }
+        tab.first[tab.count] = chunks;
+        tab.chunks = chunks;
+        if (chunks == 0) return cudaSuccess;
+        tab.part = a.ws + parts;
+        const unsigned grid = chunks < kNormBlocks ? chunks : kNormBlocks;
+        parts += static_cast<int>(grid);
+        return launch_kernel(norm_kernel<EK, CAP>, dim3(grid), dim3(kOptBlock), 0, stream, 1, tab);
+    });
+}
+
+template <int EK>
+cudaError_t norm_types(const NormArgs& a, int& parts, cudaStream_t stream)
+{
+    return a.count <= kFewNorms ? norm_runs<EK, kFewNorms>(a, parts, stream) : norm_runs<EK, kManyNorms>(a, parts, stream);
+}
+
+}  // namespace
+
+size_t grad_norm_workspace_bytes(int64_t count)
+{
+    return static_cast<size_t>((count + kManyNorms - 1) / kManyNorms) * kNormBlocks * 8;
+}
+
+cudaError_t launch_grad_norm(const NormArgs& a, cudaStream_t stream)
+{
+    int parts = 0;
+    const cudaError_t e = a.ek == kF32 ? norm_types<kF32>(a, parts, stream)
+                          : a.ek == kBF16 ? norm_types<kBF16>(a, parts, stream) : norm_types<kF16>(a, parts, stream);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(norm_join_kernel, dim3(1), dim3(kOptBlock), 0, stream, 1, static_cast<const double*>(a.ws), parts,
+                         a.max_norm, a.out, a.status);
+}
+
+}  // namespace dgrad

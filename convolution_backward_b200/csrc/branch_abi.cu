@@ -1,5 +1,6 @@
 // branch_abi.cu -- the C entry points of the residual branch's operators (declared
-// in include/dgrad.h): layer norm, the gated pointwise block and dropout, forward and backward.
+// in include/dgrad.h): layer norm, group norm, the gated pointwise block and dropout, forward and
+// backward.
 //
 // Host side only: every argument is checked before anything is launched, then
 // the launchers enqueue their kernels on the caller's stream.
@@ -65,8 +66,37 @@ dgrad_status_t gated_shape(int64_t M, int64_t C, int64_t F)
 
 static_assert(int(DGRAD_ACT_SILU) == dgrad::kSilu && int(DGRAD_ACT_GELU) == dgrad::kGelu &&
                   int(DGRAD_ACT_GELU_TANH) == dgrad::kGeluTanh && int(DGRAD_ACT_RELU) == dgrad::kRelu &&
-                  int(DGRAD_ACT_SIGMOID) == dgrad::kSigmoid,
+                  int(DGRAD_ACT_SIGMOID) == dgrad::kSigmoid && int(DGRAD_ACT_NONE) == dgrad::kNoAct,
               "the kernels' activation codes are the ABI's");
+
+dgrad_status_t gn_shape(int64_t N, int64_t S, int64_t C, int64_t G, dgrad_dtype_t dtype)
+{
+    if (!valid_dtype(dtype) || N < 0 || S < 0 || C < 1 || G < 1 || C % G) return DGRAD_ERR_INVALID;
+    if (C > kMaxChannels || N > kMaxRows || S > kMaxRows || N * S > kMaxRows || N * G > kMaxRows)
+        return DGRAD_ERR_UNSUPPORTED;
+    return DGRAD_OK;
+}
+
+struct Range {
+    const void* p;
+    int64_t n;
+};
+
+// True when one of the written ranges shares a byte with another of them or with one that is
+// read; the first written one may be exactly one of the first `inplace` read ones.
+template <size_t NO, size_t NI>
+bool overlaps(const Range (&out)[NO], const Range (&in)[NI], size_t inplace)
+{
+    for (size_t i = 0; i < NO; ++i) {
+        for (size_t j = 0; j < NI; ++j)
+            if (i == 0 && j < inplace ? clash(out[i].p, out[i].n, in[j].p, in[j].n)
+                                      : shared(out[i].p, out[i].n, in[j].p, in[j].n))
+                return true;
+        for (size_t j = 0; j < i; ++j)
+            if (shared(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+    }
+    return false;
+}
 
 dgrad_status_t gated_types(dgrad_dtype_t dtype, dgrad_act_t act)
 {
@@ -175,6 +205,101 @@ dgrad_status_t dgrad_layernorm_backward(int64_t M, int64_t C, dgrad_dtype_t dtyp
     return done(dgrad::launch_layernorm_backward(a, cs));
 }
 
+dgrad_status_t dgrad_groupnorm_forward_workspace(int64_t N, int64_t S, int64_t C, int64_t G, dgrad_dtype_t dtype,
+                                                 size_t* bytes)
+{
+    if (!bytes) return DGRAD_ERR_INVALID;
+    const dgrad_status_t s = gn_shape(N, S, C, G, dtype);
+    if (s != DGRAD_OK) return s;
+    *bytes = N == 0 || S == 0 ? 0 : dgrad::groupnorm_forward_workspace_bytes(N, S, C, G, elem_kind(dtype));
+    return DGRAD_OK;
+}
+
+dgrad_status_t dgrad_groupnorm_forward(int64_t N, int64_t S, int64_t C, int64_t G, dgrad_dtype_t dtype, double eps,
+                                       dgrad_act_t act, const void* X, const void* gamma, const void* beta, void* Y,
+                                       float* mean, float* rstd, void* workspace, size_t workspace_bytes,
+                                       void* stream)
+{
+    dgrad_status_t s = gn_shape(N, S, C, G, dtype);
+    if (s != DGRAD_OK) return s;
+    if (!(eps >= 0.0) || !std::isfinite(static_cast<float>(eps))) return DGRAD_ERR_INVALID;
+    if (act < DGRAD_ACT_SILU || act > DGRAD_ACT_NONE) return DGRAD_ERR_INVALID;
+    if (!aligned16(X) || !aligned16(Y) || !aligned16(gamma) || !aligned16(beta) || !aligned4(mean) || !aligned4(rstd) ||
+        !aligned16(workspace))
+        return DGRAD_ERR_ALIGNMENT;
+    const int64_t stats = N * G * 4;
+    if (shared(mean, stats, rstd, stats)) return DGRAD_ERR_INVALID;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (N == 0 || S == 0) {   // statistics of no values
+        for (float* stat : {mean, rstd})
+            if (stat && stats) {
+                s = done(cudaMemsetAsync(stat, 0xFF, static_cast<size_t>(stats), cs));
+                if (s != DGRAD_OK) return s;
+            }
+        return DGRAD_OK;
+    }
+    if (!X || !Y || !workspace) return DGRAD_ERR_INVALID;
+    const size_t need = dgrad::groupnorm_forward_workspace_bytes(N, S, C, G, elem_kind(dtype));
+    if (workspace_bytes < need) return DGRAD_ERR_INVALID;
+    const int64_t es = elem_size(dtype), n = N * S * C * es;
+    const Range out[4] = {{Y, n}, {mean, stats}, {rstd, stats}, {workspace, static_cast<int64_t>(need)}};
+    const Range in[3] = {{X, n}, {gamma, C * es}, {beta, C * es}};
+    if (overlaps(out, in, 1)) return DGRAD_ERR_INVALID;
+    int* status = nullptr;
+    s = static_cast<dgrad_status_t>(dgrad::device_status_word(&status));
+    if (s != DGRAD_OK) return s;
+    const dgrad::GnFwdArgs a{N, S, C, G, elem_kind(dtype), static_cast<float>(eps), static_cast<int>(act), X, gamma, beta,
+                             Y, mean, rstd, static_cast<float*>(workspace), status};
+    return done(dgrad::launch_groupnorm_forward(a, cs));
+}
+
+dgrad_status_t dgrad_groupnorm_backward_workspace(int64_t N, int64_t S, int64_t C, int64_t G, dgrad_dtype_t dtype,
+                                                  size_t* bytes)
+{
+    if (!bytes) return DGRAD_ERR_INVALID;
+    const dgrad_status_t s = gn_shape(N, S, C, G, dtype);
+    if (s != DGRAD_OK) return s;
+    *bytes = N == 0 || S == 0 ? 0 : dgrad::groupnorm_backward_workspace_bytes(N, S, C, G, elem_kind(dtype));
+    return DGRAD_OK;
+}
+
+dgrad_status_t dgrad_groupnorm_backward(int64_t N, int64_t S, int64_t C, int64_t G, dgrad_dtype_t dtype,
+                                        dgrad_act_t act, const void* dY, const void* X, const void* gamma,
+                                        const void* beta, const float* mean, const float* rstd, void* dX,
+                                        void* dgamma, void* dbeta, void* workspace, size_t workspace_bytes,
+                                        void* stream)
+{
+    dgrad_status_t s = gn_shape(N, S, C, G, dtype);
+    if (s != DGRAD_OK) return s;
+    if (act < DGRAD_ACT_SILU || act > DGRAD_ACT_NONE) return DGRAD_ERR_INVALID;
+    if (!aligned16(dY) || !aligned16(X) || !aligned16(gamma) || !aligned16(beta) || !aligned4(mean) || !aligned4(rstd) ||
+        !aligned16(dX) || !aligned16(dgamma) || !aligned16(dbeta) || !aligned16(workspace))
+        return DGRAD_ERR_ALIGNMENT;
+    const int64_t es = elem_size(dtype), n = N * S * C * es, stats = N * G * 4;
+    if (shared(dgamma, C * es, dbeta, C * es)) return DGRAD_ERR_INVALID;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (N == 0 || S == 0) {   // sums over no positions
+        for (void* g : {dgamma, dbeta})
+            if (g) {
+                s = done(cudaMemsetAsync(g, 0, static_cast<size_t>(C * es), cs));
+                if (s != DGRAD_OK) return s;
+            }
+        return DGRAD_OK;
+    }
+    if (!dY || !X || !mean || !rstd || !dX || !workspace) return DGRAD_ERR_INVALID;
+    const size_t need = dgrad::groupnorm_backward_workspace_bytes(N, S, C, G, elem_kind(dtype));
+    if (workspace_bytes < need) return DGRAD_ERR_INVALID;
+    const Range out[4] = {{dX, n}, {dgamma, C * es}, {dbeta, C * es}, {workspace, static_cast<int64_t>(need)}};
+    const Range in[6] = {{dY, n}, {X, n}, {gamma, C * es}, {beta, C * es}, {mean, stats}, {rstd, stats}};
+    if (overlaps(out, in, 2)) return DGRAD_ERR_INVALID;
+    int* status = nullptr;
+    s = static_cast<dgrad_status_t>(dgrad::device_status_word(&status));
+    if (s != DGRAD_OK) return s;
+    const dgrad::GnBwdArgs a{N, S, C, G, elem_kind(dtype), static_cast<int>(act), dY, X, gamma, beta, mean, rstd, dX,
+                             dgamma, dbeta, static_cast<float*>(workspace), status};
+    return done(dgrad::launch_groupnorm_backward(a, cs));
+}
+
 dgrad_status_t dgrad_gated_forward(int64_t M, int64_t C, int64_t F, dgrad_dtype_t dtype, dgrad_act_t act,
                                    const void* X, const void* W, void* H, void* Z, void* stream)
 {
@@ -223,10 +348,6 @@ dgrad_status_t dgrad_gated_backward(int64_t M, int64_t C, int64_t F, dgrad_dtype
     const size_t need = dgrad::gated_backward_workspace_bytes(M, C, F);
     if (workspace_bytes < need) return DGRAD_ERR_INVALID;
     const int64_t ws = static_cast<int64_t>(need);
-    struct Range {
-        const void* p;
-        int64_t n;
-    };
     const Range out[3] = {{dX, nx}, {dW, nw}, {workspace, ws}};
     const Range in[4] = {{dH, nh}, {X, dW ? nx : 0}, {Z, 2 * nh}, {W, dX ? nw : 0}};
     for (int i = 0; i < 3; ++i) {

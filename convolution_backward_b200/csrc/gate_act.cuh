@@ -8,6 +8,7 @@
 //                                           s + 2 g s (1 - s) dv/dg
 //   relu       max(g, 0)                    g > 0
 //   sigmoid    s(g)                         s(g) s(-g)
+//   none       g                            1                 (group norm only)
 // The forms keep their relative precision for large negative g, where 1 + tanh and
 // 1 + erf cancel, and sigmoid's derivative for large positive g, where 1 - s does (at
 // g = 12 s (1 - s) is off by 1%, from 17 on it is 0).  P's tail is
@@ -26,7 +27,7 @@
 
 namespace dgrad {
 
-enum GateAct : int { kSilu = 0, kGelu = 1, kGeluTanh = 2, kRelu = 3, kSigmoid = 4 };
+enum GateAct : int { kSilu = 0, kGelu = 1, kGeluTanh = 2, kRelu = 3, kSigmoid = 4, kNoAct = 5 };
 
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 
@@ -86,6 +87,8 @@ __device__ __forceinline__ float2 gate_act(float2 g)
         return __fmul2_rn(g, logistic2(__fmul2_rn(g, c)));
     } else if constexpr (ACT == kRelu) {
         return make_float2(g.x <= 0.f ? 0.f : g.x, g.y <= 0.f ? 0.f : g.y);   // NaN stays
+    } else if constexpr (ACT == kNoAct) {
+        return g;
     } else {
         return logistic2(__fmul2_rn(g, splat(-kLog2e)));
     }
@@ -116,6 +119,9 @@ __device__ __forceinline__ void gate_act_grad(float2 g, float2& a, float2& d)
     } else if constexpr (ACT == kRelu) {
         a = gate_act<kRelu>(g);
         d = make_float2(g.x > 0.f ? 1.0f : 0.f, g.y > 0.f ? 1.0f : 0.f);
+    } else if constexpr (ACT == kNoAct) {
+        a = g;
+        d = splat(1.0f);
     } else {
         const float2 x = ex2_pair(__fmul2_rn(make_float2(fabsf(g.x), fabsf(g.y)), splat(-kLog2e)));
         const float2 r = rcp_pair(__fadd2_rn(x, splat(1.0f))), o = __fmul2_rn(x, r);   // s(|g|), s(-|g|)

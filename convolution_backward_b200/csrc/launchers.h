@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "dgrad.h"
+
 namespace dgrad {
 
 // Pointwise dgrad as a GEMM: dX[M][C] = dY[M][K] * W[K][C], all row-major.
@@ -204,6 +206,45 @@ struct LnBwdArgs {
 size_t layernorm_backward_workspace_bytes(int64_t M, int64_t C, int ek);
 cudaError_t launch_layernorm_backward(const LnBwdArgs& a, cudaStream_t stream);
 
+// Group norm over N samples of S positions of C channels in G groups, with an activation
+// (a dgrad_act_t).  ws: groupnorm_forward_workspace_bytes; null mean or rstd: not kept.
+struct GnFwdArgs {
+    int64_t N, S, C, G;
+    int ek;
+    float eps;
+    int act;
+    const void* X;
+    const void* gamma;
+    const void* beta;
+    void* Y;
+    float* mean;
+    float* rstd;
+    float* ws;
+    int* status;
+};
+size_t groupnorm_forward_workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, int ek);
+cudaError_t launch_groupnorm_forward(const GnFwdArgs& a, cudaStream_t stream);
+
+// Its gradients; null dgamma or dbeta: not computed.
+struct GnBwdArgs {
+    int64_t N, S, C, G;
+    int ek;
+    int act;
+    const void* dY;
+    const void* X;
+    const void* gamma;
+    const void* beta;
+    const float* mean;
+    const float* rstd;
+    void* dX;
+    void* dgamma;
+    void* dbeta;
+    float* ws;
+    int* status;
+};
+size_t groupnorm_backward_workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, int ek);
+cudaError_t launch_groupnorm_backward(const GnBwdArgs& a, cudaStream_t stream);
+
 // Dropout of n elements, kept where their 16-bit draw is >= threshold (0 .. 65536),
 // plus the residual when there is one.
 struct DropArgs {
@@ -249,6 +290,41 @@ struct GatedBwdArgs {
 };
 size_t gated_backward_workspace_bytes(int64_t M, int64_t C, int64_t F);
 cudaError_t launch_gated_backward(const GatedBwdArgs& a, cudaStream_t stream);
+
+// The AdamW step (all checked; the tensors are the caller's, read while the call is made).
+struct AdamWArgs {
+    int64_t count;
+    const dgrad_adamw_tensor_t* t;
+    int pk, gk;            // ElemKind of parameters and gradients
+    bool master;
+    int bits;              // 32 or 8
+    bool stochastic;
+    double lr, beta1, beta2, eps, weight_decay;
+    double bias1, bias2;   // 1/(1 - beta^t)
+    double ln_beta1, ln_beta2;
+    const float* lr_dev;
+    const int64_t* step_dev;
+    const float* scale;
+    uint64_t seed, offset;
+    int* status;
+};
+cudaError_t launch_adamw(const AdamWArgs& a, cudaStream_t stream);
+cudaError_t launch_adamw_moments(const dgrad_adamw_tensor_t* t, float* const* m_out, float* const* v_out, int64_t count,
+                                 int* status, cudaStream_t stream);
+
+// The norm over all elements of many tensors, and the factor that brings it to max_norm.
+struct NormArgs {
+    int64_t count;
+    const void* const* g;
+    const int64_t* n;
+    int ek;
+    float max_norm;
+    float* out;    // norm, factor
+    double* ws;
+    int* status;
+};
+size_t grad_norm_workspace_bytes(int64_t count);
+cudaError_t launch_grad_norm(const NormArgs& a, cudaStream_t stream);
 
 // Encode a tensor map over a dense tensor (dims inner first, strides in bytes of the
 // outer dimensions, zero fill); swizzled: 128-byte swizzle.  Nothing is kept.

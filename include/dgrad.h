@@ -255,11 +255,12 @@ dgrad_status_t dgrad_layernorm_backward(int64_t M, int64_t C, dgrad_dtype_t dtyp
 /* Workspace bytes dgrad_layernorm_backward needs (host only, no CUDA call). */
 dgrad_status_t dgrad_layernorm_backward_workspace(int64_t M, int64_t C, dgrad_dtype_t dtype, size_t* bytes);
 
-/* The gate's activation: silu g/(1 + exp(-g)); gelu g*P(g) with the normal
+/* The activations: silu g/(1 + exp(-g)); gelu g*P(g) with the normal
  * distribution P (exact) or its tanh form g*(1 + tanh(sqrt(2/pi)*(g + 0.044715 g^3)))/2;
- * relu max(g, 0); sigmoid 1/(1 + exp(-g)). */
+ * relu max(g, 0); sigmoid 1/(1 + exp(-g)); none g (group norm only). */
 typedef enum {
-    DGRAD_ACT_SILU = 0, DGRAD_ACT_GELU = 1, DGRAD_ACT_GELU_TANH = 2, DGRAD_ACT_RELU = 3, DGRAD_ACT_SIGMOID = 4
+    DGRAD_ACT_SILU = 0, DGRAD_ACT_GELU = 1, DGRAD_ACT_GELU_TANH = 2, DGRAD_ACT_RELU = 3, DGRAD_ACT_SIGMOID = 4,
+    DGRAD_ACT_NONE = 5
 } dgrad_act_t;
 
 /* Gated pointwise block in one kernel: two 1x1 projections of C to F channels, the
@@ -296,6 +297,42 @@ dgrad_status_t dgrad_gated_backward(int64_t M, int64_t C, int64_t F, dgrad_dtype
 /* Workspace bytes dgrad_gated_backward needs (host only, no CUDA call). */
 dgrad_status_t dgrad_gated_backward_workspace(int64_t M, int64_t C, int64_t F, size_t* bytes);
 
+/* Group norm over NHWC samples with an activation.  X is [N][S][C], S positions (H*W) of C
+ * channels; a group is C/G adjacent channels of a sample at all positions, m = S*C/G values:
+ *     mean = sum(x)/m,  rstd = 1/sqrt(sum((x - mean)^2)/m + eps),
+ *     z = (x - mean)*rstd*gamma + beta,  Y = act(z).
+ * All element types (gamma, beta [C] and Y have X's).  gamma or beta null: ones, zeros.
+ * mean, rstd (fp32, [N][G] each, either may be null) are what the backward pass needs.
+ * Y may be X.  eps finite and >= 0.  G divides C (else DGRAD_ERR_INVALID).  A group that
+ * holds an infinity or NaN becomes NaN, and so do its mean and rstd.  C <= 65536, N*S and
+ * N*G < 2^31 (else DGRAD_ERR_UNSUPPORTED).  N or S of 0: nothing but mean and rstd is
+ * written, and those are NaN (sums over no values).  workspace: at least
+ * dgrad_groupnorm_forward_workspace bytes, 16-byte aligned, as for layer norm's gradients. */
+dgrad_status_t dgrad_groupnorm_forward(int64_t N, int64_t S, int64_t C, int64_t G, dgrad_dtype_t dtype, double eps,
+                                       dgrad_act_t act, const void* X, const void* gamma, const void* beta, void* Y,
+                                       float* mean, float* rstd, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/* Its gradients, with n = (x - mean)*rstd, dz = dY*act'(z) and q = dz*gamma (z is formed again
+ * from x, the statistics, gamma and beta):
+ *     dX = rstd*(q - sum(q)/m - n*sum(q*n)/m) with the sums over the group,
+ *     dgamma = sum over samples and positions of dz*n,  dbeta = the same of dz.
+ * relu's derivative is 0 where z, every operation rounded to fp32 in the order
+ * ((x - mean)*rstd)*gamma + beta, is 0.  dgamma or dbeta null: not computed.  dX may be dY or X.
+ * N or S of 0: dgamma and dbeta are set to zero.  workspace: always needed, at least
+ * dgrad_groupnorm_backward_workspace bytes.  Two calls that may overlap need a workspace each. */
+dgrad_status_t dgrad_groupnorm_backward(int64_t N, int64_t S, int64_t C, int64_t G, dgrad_dtype_t dtype,
+                                        dgrad_act_t act, const void* dY, const void* X, const void* gamma,
+                                        const void* beta, const float* mean, const float* rstd, void* dX,
+                                        void* dgamma, void* dbeta, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
+/* Workspace bytes the two need (host only, no CUDA call; 0 for N or S of 0). */
+dgrad_status_t dgrad_groupnorm_forward_workspace(int64_t N, int64_t S, int64_t C, int64_t G, dgrad_dtype_t dtype,
+                                                 size_t* bytes);
+dgrad_status_t dgrad_groupnorm_backward_workspace(int64_t N, int64_t S, int64_t C, int64_t G, dgrad_dtype_t dtype,
+                                                  size_t* bytes);
+
 /* Dropout of n elements with no stored mask: Y = keep ? X*scale : 0, plus residual
  * when it is not null.  Element i of block b = i/8 draws 16 bits of Philox-4x32-10
  * (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3", 2011) at counter
@@ -314,6 +351,90 @@ dgrad_status_t dgrad_dropout_forward(int64_t n, dgrad_dtype_t dtype, double p, u
  * dX may be dY. */
 dgrad_status_t dgrad_dropout_backward(int64_t n, dgrad_dtype_t dtype, double p, uint64_t seed, uint64_t offset,
                                       const void* dY, void* dX, void* stream);
+
+/* ---- The optimizer's step over all parameters at once, and the norm of their gradients.
+ * No counterpart on the pages.  Lists of tensors are host arrays, read while the call is
+ * made: a call captured into a graph keeps its tensors' addresses.  Tensors of 0 elements are
+ * allowed (their pointers are not looked at). Pointers are aligned to their elements; those on
+ * 16 bytes (8-bit codes: 4) are read four elements at a time.  One launch takes up to 380
+ * tensors (norms: 1600). ---- */
+
+/* One tensor: param [n] of the parameters' type, grad [n] (null: the tensor is left as it is),
+ * the states m and v, and an fp32 master copy (null: none; for all tensors or none).
+ * 32-bit states: m, v fp32 [n]; m_max and v_max are not used.
+ * 8-bit states: blocks of 256 elements share m_max and v_max (fp32, ceil(n/256) each); m holds
+ * int8 codes -127 .. 127 for m = c|c|/127^2 m_max, v uint8 codes for v = (c/255)^4 v_max.  All
+ * zero: a fresh state. */
+typedef struct {
+    void* param;
+    const void* grad;
+    void* m;
+    void* v;
+    float* master;
+    float* m_max;
+    float* v_max;
+    int64_t n;
+} dgrad_adamw_tensor_t;
+
+/* A step's scalars.  step: t, counted from 1.  lr_device, step_device (one fp32, one int64; null:
+ * lr and step): read by the kernels, so that a captured step follows them.  grad_scale (one
+ * fp32 in device memory, null: 1): every gradient is multiplied by it; if it is no finite
+ * number the step changes nothing (parameters, states and maxima).  state_bits: 32 or 8.
+ * stochastic (8 bits only): codes are rounded by the random bits of (seed, offset), as below. */
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;
+    const float* lr_device;
+    const int64_t* step_device;
+    const float* grad_scale;
+    int32_t state_bits, stochastic;
+    uint64_t seed, offset;
+} dgrad_adamw_t;
+
+/* The AdamW step, with g = grad_scale*grad:
+ *     m' = beta1 m + (1 - beta1) g,   v' = beta2 v + (1 - beta2) g g,
+ *     p' = p (1 - lr weight_decay) - lr (m'/(1 - beta1^t)) / (sqrt(v'/(1 - beta2^t)) + eps),
+ * all in fp32; p is the master copy where there is one (both are written), and is rounded once
+ * to the parameter's type.  param_type: any; grad_type: the same or DGRAD_F32.
+ * 8-bit states enter p' unrounded.  Their codes are defined by fp32 operations, each rounded
+ * (in the order written: m' = beta1*m + (1-beta1)*g, v' = beta2*v + ((1-beta2)*g)*g), so that
+ * they can be reproduced bit for bit: with M the block's largest |m'|, k = 2^64 where M < 2^-60,
+ * 2^-64 where M > 2^60, else 1, and w = (|m'| k) ((1/(M k)) 127^2), low is the largest c with
+ * c*c <= w, and c = low + 1 if (w - low^2) 65536 > ((low+1)^2 - low^2) draw, else low, at most
+ * 127; draw is 32768 (the nearer value), or with `stochastic` 16 random bits.  v likewise with 255, c^4 = (c*c)*(c*c)
+ * and V the largest v', where a v' above 0 has a code of at least 1.  The random bits are those
+ * of Philox-4x32-10 at counter (b, offset), key seed (as for dropout): with every tensor rounded up to 256 elements,
+ * element i of the whole list takes word i % 4 of b = i/4, the low half for m, the high half for v.
+ * An infinity or NaN in a gradient makes the states of its 256 elements NaN (8 bits), or its own (32).
+ * count 0: no-op.  beta1, beta2 in [0, 1); eps >= 0; finite scalars; step >= 1 (unless
+ * step_device), else DGRAD_ERR_INVALID.  A master copy of fp32 parameters: DGRAD_ERR_UNSUPPORTED.
+ * The written ranges must lie apart from each other and from the gradients; dgrad_adamw_check
+ * looks at that, once for a list. */
+dgrad_status_t dgrad_adamw_step(int64_t count, const dgrad_adamw_tensor_t* tensors, dgrad_dtype_t param_type,
+                                dgrad_dtype_t grad_type, const dgrad_adamw_t* opt, void* stream);
+
+/* Host only: the checks of dgrad_adamw_step on the tensors, and DGRAD_ERR_INVALID where a written
+ * range shares a byte with another range of the list. */
+dgrad_status_t dgrad_adamw_check(int64_t count, const dgrad_adamw_tensor_t* tensors, dgrad_dtype_t param_type,
+                                 dgrad_dtype_t grad_type, int32_t state_bits);
+
+/* What 8-bit states stand for: m_out[i], v_out[i] (host arrays of fp32 device pointers, n elements each,
+ * apart from everything else), each operation rounded: m = ((c|c|) (1/127^2)) m_max,
+ * v = (c^4 (1/255^4)) v_max. */
+dgrad_status_t dgrad_adamw_moments(int64_t count, const dgrad_adamw_tensor_t* tensors, float* const* m_out,
+                                   float* const* v_out, void* stream);
+
+/* The norm over all elements of the tensors grads[i] (n[i] elements, one type):
+ *     out[0] = sqrt(sum of squares),  out[1] = min(1, max_norm/(out[0] + 1e-6)),
+ * fp32 in device memory; squares and sums are formed in 64 bits.  out[1] is the step's grad_scale;
+ * it is NaN where the norm is no finite number, so that the step is left out.  max_norm >= 0 (it may be
+ * infinite: out[1] = 1).  count 0: a norm of 0.  workspace: 16-byte aligned, at least
+ * dgrad_grad_norm_workspace bytes; two calls that may overlap need one each. */
+dgrad_status_t dgrad_grad_norm(int64_t count, const void* const* grads, const int64_t* n, dgrad_dtype_t dtype,
+                               double max_norm, float* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes dgrad_grad_norm needs for a list of count tensors (host only). */
+dgrad_status_t dgrad_grad_norm_workspace(int64_t count, size_t* bytes);
 
 /* Output extents of the forward convolution the problem describes (host only,
  * no CUDA call).  Returns DGRAD_ERR_INVALID for an invalid problem. */

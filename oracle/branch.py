@@ -1,5 +1,5 @@
-"""fp64 CPU oracle for the residual branch's operators: layer norm, the gated pointwise
-block and dropout, each with its gradients.
+"""fp64 CPU oracle for the residual branch's operators: layer norm, group norm, the gated
+pointwise block and dropout, each with its gradients.
 
 TEST INFRASTRUCTURE ONLY, like the rest of this package.  Plain numpy in float64 from
 the definitions; nothing here is shared with the CUDA path.  tests/test_branch_ops.py
@@ -46,6 +46,36 @@ def act(name, g):
     k = math.sqrt(2 / math.pi)
     t = np.tanh(k * (g + 0.044715 * g ** 3))
     return 0.5 * g * (1 + t), 0.5 * (1 + t) + 0.5 * g * (1 - t * t) * k * (1 + 3 * 0.044715 * g * g)
+
+
+def _spread(stat, C):
+    """(N, G) statistics to (N, 1, C)."""
+    return np.repeat(stat, C // stat.shape[1], axis=1)[:, None, :]
+
+
+def groupnorm(x, G, gamma, beta, eps, name=None):
+    """(y, mean, rstd) of x (N, S, C) in G groups of channels; name: an activation or None."""
+    N, S, C = x.shape
+    g = x.reshape(N, S, G, C // G)
+    mean = g.mean(axis=(1, 3))
+    rstd = 1.0 / np.sqrt(((g - mean[:, None, :, None]) ** 2).mean(axis=(1, 3)) + eps)
+    z = (x - _spread(mean, C)) * _spread(rstd, C) * gamma + beta
+    return (z if name is None else act(name, z)[0]), mean, rstd
+
+
+def groupnorm_backward(dy, x, gamma, beta, mean, rstd, name=None, slope=None):
+    """(dx, dgamma, dbeta) with the given statistics; slope: act'(z) where it is known already."""
+    N, S, C = x.shape
+    G = mean.shape[1]
+    n = (x - _spread(mean, C)) * _spread(rstd, C)
+    if slope is None:
+        slope = np.ones_like(n) if name is None else act(name, n * gamma + beta)[1]
+    dz = dy * slope
+    q = (dz * gamma).reshape(N, S, G, C // G)
+    ng = n.reshape(N, S, G, C // G)
+    a, b = q.mean(axis=(1, 3)), (q * ng).mean(axis=(1, 3))
+    dx = _spread(rstd, C) * (dz * gamma - _spread(a, C) - n * _spread(b, C))
+    return dx, (dz * n).sum(axis=(0, 1)), dz.sum(axis=(0, 1))
 
 
 def gated(x, w, name):
