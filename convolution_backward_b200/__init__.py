@@ -660,10 +660,11 @@ def groupnorm_backward_workspace_bytes(N, S, C, groups, dtype) -> int:
 
 
 def _workspace(al, workspace, like, nbytes):
-    """(tensor, bytes): the given workspace, or one from torch."""
+    """(pointer's tensor, bytes): the given workspace, or one from torch where any is needed."""
     if workspace is not None:
         return workspace, workspace.numel() * workspace.element_size()
-    nbytes = max(nbytes, 16)
+    if nbytes == 0:
+        return None, 0
     return _empty(al, like, (nbytes,), _torch().uint8), nbytes
 
 
@@ -697,7 +698,7 @@ def groupnorm_forward(X, groups, gamma=None, beta=None, eps=1e-5, act=None, stat
     if al is not None:
         al.uses(X, *given)
     _call(dev, "dgrad_groupnorm_forward", lib().dgrad_groupnorm_forward, N, S, C, G, code, float(eps), acode,
-          X.data_ptr(), _ptr(gamma), _ptr(beta), out.data_ptr(), _ptr(mean), _ptr(rstd), workspace.data_ptr(), ws_bytes,
+          X.data_ptr(), _ptr(gamma), _ptr(beta), out.data_ptr(), _ptr(mean), _ptr(rstd), _ptr(workspace), ws_bytes,
           stream=stream)
     return (out, mean, rstd) if stats else out
 
@@ -737,7 +738,7 @@ def groupnorm_backward(dY, X, mean, rstd, gamma=None, beta=None, act=None, param
         al.uses(dY, X, mean, rstd, *given)
     _call(dev, "dgrad_groupnorm_backward", lib().dgrad_groupnorm_backward, N, S, C, G, code, acode, dY.data_ptr(),
           X.data_ptr(), _ptr(gamma), _ptr(beta), mean.data_ptr(), rstd.data_ptr(), out.data_ptr(), _ptr(dgamma),
-          _ptr(dbeta), workspace.data_ptr(), ws_bytes, stream=stream)
+          _ptr(dbeta), _ptr(workspace), ws_bytes, stream=stream)
     return out, dgamma, dbeta
 
 
@@ -1163,7 +1164,7 @@ def grad_norm(grads, max_norm=None, workspace=None, stream=None):
     at = np.array([g.data_ptr() for g in grads], dtype=np.uint64)
     n = np.array([g.numel() for g in grads], dtype=np.int64)
     _call(dev, "dgrad_grad_norm", lib().dgrad_grad_norm, len(grads), at.ctypes.data, n.ctypes.data, code, limit,
-          out.data_ptr(), workspace.data_ptr(), ws_bytes, stream=stream)
+          out.data_ptr(), _ptr(workspace), ws_bytes, stream=stream)
     return out[0] if max_norm is None else (out[0], out[1])
 
 

@@ -238,9 +238,9 @@ dgrad_status_t dgrad_groupnorm_forward(int64_t N, int64_t S, int64_t C, int64_t 
             }
         return DGRAD_OK;
     }
-    if (!X || !Y || !workspace) return DGRAD_ERR_INVALID;
+    if (!X || !Y) return DGRAD_ERR_INVALID;
     const size_t need = dgrad::groupnorm_forward_workspace_bytes(N, S, C, G, elem_kind(dtype));
-    if (workspace_bytes < need) return DGRAD_ERR_INVALID;
+    if (need && (!workspace || workspace_bytes < need)) return DGRAD_ERR_INVALID;
     const int64_t es = elem_size(dtype), n = N * S * C * es;
     const Range out[4] = {{Y, n}, {mean, stats}, {rstd, stats}, {workspace, static_cast<int64_t>(need)}};
     const Range in[3] = {{X, n}, {gamma, C * es}, {beta, C * es}};
@@ -286,9 +286,9 @@ dgrad_status_t dgrad_groupnorm_backward(int64_t N, int64_t S, int64_t C, int64_t
             }
         return DGRAD_OK;
     }
-    if (!dY || !X || !mean || !rstd || !dX || !workspace) return DGRAD_ERR_INVALID;
+    if (!dY || !X || !mean || !rstd || !dX) return DGRAD_ERR_INVALID;
     const size_t need = dgrad::groupnorm_backward_workspace_bytes(N, S, C, G, elem_kind(dtype));
-    if (workspace_bytes < need) return DGRAD_ERR_INVALID;
+    if (need && (!workspace || workspace_bytes < need)) return DGRAD_ERR_INVALID;
     const Range out[4] = {{dX, n}, {dgamma, C * es}, {dbeta, C * es}, {workspace, static_cast<int64_t>(need)}};
     const Range in[6] = {{dY, n}, {X, n}, {gamma, C * es}, {beta, C * es}, {mean, stats}, {rstd, stats}};
     if (overlaps(out, in, 2)) return DGRAD_ERR_INVALID;

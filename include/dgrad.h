@@ -307,7 +307,8 @@ dgrad_status_t dgrad_gated_backward_workspace(int64_t M, int64_t C, int64_t F, s
  * holds an infinity or NaN becomes NaN, and so do its mean and rstd.  C <= 65536, N*S and
  * N*G < 2^31 (else DGRAD_ERR_UNSUPPORTED).  N or S of 0: nothing but mean and rstd is
  * written, and those are NaN (sums over no values).  workspace: at least
- * dgrad_groupnorm_forward_workspace bytes, 16-byte aligned, as for layer norm's gradients. */
+ * dgrad_groupnorm_forward_workspace bytes (0 for sizes that need none; it may be null then), 16-byte
+ * aligned, as for layer norm's gradients. */
 dgrad_status_t dgrad_groupnorm_forward(int64_t N, int64_t S, int64_t C, int64_t G, dgrad_dtype_t dtype, double eps,
                                        dgrad_act_t act, const void* X, const void* gamma, const void* beta, void* Y,
                                        float* mean, float* rstd, void* workspace, size_t workspace_bytes,
@@ -319,7 +320,7 @@ dgrad_status_t dgrad_groupnorm_forward(int64_t N, int64_t S, int64_t C, int64_t 
  *     dgamma = sum over samples and positions of dz*n,  dbeta = the same of dz.
  * relu's derivative is 0 where z, every operation rounded to fp32 in the order
  * ((x - mean)*rstd)*gamma + beta, is 0.  dgamma or dbeta null: not computed.  dX may be dY or X.
- * N or S of 0: dgamma and dbeta are set to zero.  workspace: always needed, at least
+ * N or S of 0: dgamma and dbeta are set to zero.  workspace: at least
  * dgrad_groupnorm_backward_workspace bytes.  Two calls that may overlap need a workspace each. */
 dgrad_status_t dgrad_groupnorm_backward(int64_t N, int64_t S, int64_t C, int64_t G, dgrad_dtype_t dtype,
                                         dgrad_act_t act, const void* dY, const void* X, const void* gamma,

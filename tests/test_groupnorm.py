@@ -79,10 +79,12 @@ def test_forward_refusals():
     assert size(2, 4, 16, 4, 1, None) == INVALID
     assert size(0, 4, 16, 4, 1, ctypes.byref(nb)) == OK and nb.value == 0
     assert size(2, 4, 16, 5, 1, ctypes.byref(nb)) == INVALID
-    assert size(2, 4, 16, 4, 1, ctypes.byref(nb)) == OK and nb.value > 0
+    assert size(2, 4, 16, 4, 1, ctypes.byref(nb)) == OK
+    large = dict(N=1, S=1 << 20, C=8, G=1)      # one group of 2^23 values: sums over the whole GPU
+    assert size(1, 1 << 20, 8, 1, 1, ctypes.byref(nb)) == OK and nb.value > 0
     for bad in ({"N": -1}, {"S": -1}, {"C": 0}, {"G": 0}, {"G": 3}, {"G": 32}, {"dtype": 3}, {"eps": -1e-9},
-                {"eps": float("nan")}, {"eps": 1e300}, {"act": 6}, {"act": -1}, {"X": 0}, {"Y": 0}, {"ws": 0},
-                {"nb": nb.value - 1}):
+                {"eps": float("nan")}, {"eps": 1e300}, {"act": 6}, {"act": -1}, {"X": 0}, {"Y": 0}, {"ws": 0, **large},
+                {"nb": nb.value - 1, **large}):
         assert _fwd(**bad) == INVALID, bad
     assert _fwd(C=65544, G=8) == UNSUPPORTED
     assert _fwd(N=1 << 20, S=1 << 12) == UNSUPPORTED
@@ -95,9 +97,10 @@ def test_forward_refusals():
     assert _fwd(g=2 * FAKE + 32) == INVALID      # gamma inside Y
     assert _fwd(mean=3 * FAKE, rstd=3 * FAKE) == INVALID
     assert _fwd(mean=FAKE) == INVALID
-    assert _fwd(ws=FAKE + 16) == INVALID
-    assert _fwd(ws=2 * FAKE + 16) == INVALID
-    assert _fwd(mean=8 * FAKE) == INVALID
+    large.update(X=0x40 * FAKE, Y=0x50 * FAKE)
+    assert _fwd(ws=0x40 * FAKE + 16, **large) == INVALID
+    assert _fwd(ws=0x50 * FAKE + 16, **large) == INVALID
+    assert _fwd(mean=8 * FAKE, **large) == INVALID
     assert _fwd(N=0, X=0, Y=0, ws=0, nb=0) == OK
     assert _fwd(S=0, X=0, Y=0, ws=0, nb=0) == OK
 
@@ -161,6 +164,15 @@ def test_binding_refusals():
         cb.groupnorm_backward_workspace_bytes(2, 3, 16, 4, torch.int8)
 
 
+@pytest.fixture(params=["", "s", "c"], ids=["auto", "streaming", "cluster"])
+def way(request, monkeypatch):
+    """The library's own choice between its two ways, and each of them at every size it serves."""
+    monkeypatch.setenv("DGRAD_GN_WAY", request.param)
+    cb._gn_workspace.cache_clear()
+    yield request.param
+    cb._gn_workspace.cache_clear()
+
+
 # ------------------------------------------------------------------ forward
 
 def _inputs(N, S, C, dtype, seed, offset=0.5):
@@ -219,7 +231,7 @@ IDS = lambda s: "x".join(map(str, s))
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("shape", SHAPES, ids=IDS)
-def test_forward(shape, dtype):
+def test_forward(shape, dtype, way):
     S, C, G = shape
     for N, act in ((1, "silu"), (3, None), (17, "gelu")):
         x, g, b, _ = _inputs(N, S, C, dtype, seed=S + C + N)
@@ -232,7 +244,7 @@ def test_forward(shape, dtype):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("act", ACTS)
-def test_forward_activations_and_optional_parts(act, dtype):
+def test_forward_activations_and_optional_parts(act, dtype, way):
     for S, C, G in ((50, 96, 8), (11, 33, 3)):
         x, g, b, _ = _inputs(4, S, C, dtype, seed=5)
         for gg, bb in ((None, None), (g, None), (None, b), (g, b)):
@@ -247,7 +259,7 @@ def test_forward_activations_and_optional_parts(act, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("shape", [(400, 64, 8), (4000, 24, 1), (333, 21, 7)], ids=IDS)
-def test_forward_far_mean_and_odd_rows(shape):
+def test_forward_far_mean_and_odd_rows(shape, way):
     """A mean far above the spread, a first position or block far from the others, constant groups, and
     an infinity or NaN, which spoil their own group alone."""
     S, C, G = shape
@@ -338,7 +350,7 @@ def _check_bwd(dy, x, g, b, mean, rstd, act, dtype, got, what):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("shape", SHAPES, ids=IDS)
-def test_backward(shape, dtype):
+def test_backward(shape, dtype, way):
     S, C, G = shape
     for N, act in ((1, "silu"), (3, None), (17, "gelu")):
         x, g, b, dy = _inputs(N, S, C, dtype, seed=S + C + N)
@@ -355,7 +367,7 @@ def test_backward(shape, dtype):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("act", ACTS)
-def test_backward_activations_and_optional_parts(act, dtype):
+def test_backward_activations_and_optional_parts(act, dtype, way):
     for S, C, G in ((50, 96, 8), (11, 33, 3)):
         x, g, b, dy = _inputs(4, S, C, dtype, seed=6)
         for gg, bb in ((None, None), (g, None), (None, b), (g, b)):
@@ -371,7 +383,7 @@ def test_backward_activations_and_optional_parts(act, dtype):
 
 
 @pytest.mark.gpu
-def test_backward_of_groups_of_one_value_is_zero():
+def test_backward_of_groups_of_one_value_is_zero(way):
     x, g, b, dy = _inputs(5, 1, 24, "f32", seed=4)
     for act in ACTS:
         _, mean, rstd = cb.groupnorm_forward(x, 24, g, b, act=act, stats=True)
@@ -405,7 +417,7 @@ def test_gradients_by_differences_of_the_kernel():
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("shape", [(9, 50, 96, 8), (3, 33, 1001, 7), (2, 17, 4104, 2), (40, 1, 24, 24)], ids=IDS)
-def test_every_store_in_bounds(shape, dtype, monkeypatch):
+def test_every_store_in_bounds(shape, dtype, monkeypatch, way):
     """Under the debug build, whose stores check their place."""
     import os
     path = os.path.join(os.path.dirname(cb.library_path()), "libdgrad_debug.so")
@@ -423,7 +435,28 @@ def test_every_store_in_bounds(shape, dtype, monkeypatch):
 
 
 @pytest.mark.gpu
-def test_captured_streams_and_workspaces():
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("cluster", [1, 2, 4, 8])
+@pytest.mark.parametrize("shape", [(3, 700, 96, 8, 2), (2, 1000, 40, 1, 1), (1, 4001, 66, 6, 3), (5, 9, 256, 32, 5), (2, 6000, 24, 8, 1)], ids=IDS)
+def test_cluster_sizes(shape, cluster, dtype, monkeypatch):
+    """Every cluster size; slices of unequal width; blocks without positions; more positions than stay in
+    shared memory."""
+    N, S, C, G, slices = shape
+    monkeypatch.setenv("DGRAD_GN_WAY", "c")
+    monkeypatch.setenv("DGRAD_GN_CLUSTER", str(cluster))
+    monkeypatch.setenv("DGRAD_GN_SLICES", str(slices))
+    cb._gn_workspace.cache_clear()
+    x, g, b, dy = _inputs(N, S, C, dtype, seed=S + cluster)
+    y, mean, rstd = cb.groupnorm_forward(x, G, g, b, act="silu", stats=True)
+    _check_fwd(x, G, g, b, 1e-5, "silu", dtype, y, mean, rstd, "forward")
+    got = cb.groupnorm_backward(dy, x, mean, rstd, g, b, act="silu")
+    _check_bwd(dy, x, g, b, mean, rstd, "silu", dtype, got, "backward")
+    cb.check_status()
+    cb._gn_workspace.cache_clear()
+
+
+@pytest.mark.gpu
+def test_captured_streams_and_workspaces(way):
     """One workspace in two captured graphs, another stream, and a replay on new inputs."""
     N, S, C, G = 4, 200, 96, 8
     x, g, b, dy = _inputs(N, S, C, "bf16", seed=12)
@@ -456,4 +489,4 @@ def test_captured_streams_and_workspaces():
     side.synchronize()
     assert torch.equal(y, w2)
     with pytest.raises(cb.DgradError):
-        cb.groupnorm_forward(x, G, g, b, workspace=ws[:16])
+        cb.groupnorm_backward(dy, x, want[1], want[2], g, b, workspace=ws[:16])
