@@ -883,6 +883,31 @@ _TABLE = [("param", "u8"), ("grad", "u8"), ("m", "u8"), ("v", "u8"), ("master", 
           ("n", "i8")]   # dgrad_adamw_tensor_t
 
 
+def _lists():
+    """The native reader of tensor lists (csrc/tensor_lists.cpp)."""
+    global _reader
+    if _reader is None:
+        import importlib
+
+        import torch  # noqa: F401  (its libraries come first)
+        try:
+            _reader = importlib.import_module("._tensor_lists", __name__)
+        except ImportError as e:
+            raise DgradUnavailable(f"cannot load _tensor_lists: {e}; build it with "
+                                   "`python -m convolution_backward_b200._build`") from e
+    return _reader
+
+
+_reader = None
+
+
+class _Array:
+    """A numpy array and its address."""
+
+    def __init__(self, a):
+        self.a, self.at = a, a.ctypes.data
+
+
 def _same(ts, what):
     """The one dtype and CUDA device of a list of contiguous tensors."""
     if not ts:
@@ -946,16 +971,22 @@ class AdamWState:
                 self._table[name] = [t.data_ptr() for t in ts]
         self._table["n"] = [p.numel() for p in self.params]
         self._address = self._table.ctypes.data
-        self._where = self._table["param"].tolist()
         status = lib().dgrad_adamw_check(n, self._address, self._code, self._code, self.bits)
         if status == 1:
             raise ValueError("parameters and states must not share memory")
         _check(status, "dgrad_adamw_check")
-        # the written ranges in order, for the gradients to be held against
+        self._where = _Array(np.ascontiguousarray(self._table["param"]))
+        self._n = _Array(np.ascontiguousarray(self._table["n"]))
+        # the written ranges in order, for gradients and results to be held against
         lo = np.array([t.data_ptr() for t in everything if t.numel()], dtype=np.uint64)
         size = np.array([t.numel() * t.element_size() for t in everything if t.numel()], dtype=np.uint64)
         order = np.argsort(lo)
-        self._lo, self._hi = lo[order], (lo + size)[order]
+        self._lo, self._hi = _Array(lo[order]), _Array((lo + size)[order])
+        # one step's gradients; a call of adamw_step fills them and has read them when it returns
+        self._grads = _Array(np.zeros(n, dtype=np.uint64))
+
+    def _apart(self, at, nbytes):
+        return _lists().apart(at, self._n.at, len(self.params), nbytes, self._lo.at, self._hi.at, len(self._lo.a))
 
     def __len__(self):
         return len(self.params)
@@ -1012,41 +1043,23 @@ def adamw_step(state, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_deca
     rounded stochastically by the bits of (seed, offset): give every step its own pair, and dropout others;
     None: to the nearer value.  Moments and weights are fp32 within the step, and the weights
     (master copies) are rounded once to the parameters' dtype."""
-    import numpy as np
     import torch
     n = len(state.params)
     grads = list(grads)
-    if len(grads) != n:
-        raise ValueError(f"expected {n} gradients, got {len(grads)}")
     dev = state.device
-    some = grads
-    shapes = state.shapes
-    if any(g is None for g in grads):
-        some = [g for g in grads if g is not None]
-        shapes = [s for g, s in zip(grads, shapes) if g is not None]
-    dtypes = {g.dtype for g in some}
-    if len(dtypes) > 1:
-        raise TypeError("gradients must have one dtype, got " + ", ".join(sorted(map(str, dtypes))))
-    gcode = _code_of(dtypes.pop()) if dtypes else state._code
+    to = state._grads
+    gcode, gdev = _lists().read(grads, state.params, "gradients", to.at, 0)
+    if gcode < 0:
+        gcode, gdev = state._code, dev.index     # nothing to step
     if gcode != state._code and gcode != 0:
         raise TypeError(f"gradients must be {state.dtype} or float32")
-    if [g.shape for g in some] != shapes:
-        raise ValueError("gradients must have their parameters' shapes")
-    if not all([g.is_cuda for g in some]):
-        raise ValueError("tensors must be CUDA tensors (no CPU path)")
-    if not all([g.is_contiguous() for g in some]):
-        raise ValueError("tensors must be contiguous")
-    if {g.get_device() for g in some} - {dev.index}:
+    if gdev != dev.index:
         raise ValueError("all tensors of one call must be on the same CUDA device")
-    if [p.data_ptr() for p in state.params] != state._where:
+    if not _lists().same(state.params, state._where.at):
         raise ValueError("a parameter's storage has changed since its AdamWState was made")
-    at = np.array([0 if g is None else g.data_ptr() for g in grads], dtype=np.uint64)
-    if len(state._lo):
-        size = state._table["n"].astype(np.uint64) * np.uint64(4 if gcode == 0 else 2)
-        k = np.searchsorted(state._hi, at, side="right")
-        if np.any((size > 0) & (at > 0) & (state._lo[np.minimum(k, len(state._lo) - 1)] < at + size) & (k < len(state._lo))):
-            raise ValueError("gradients must not share memory with parameters or states")
-    state._table["grad"] = at
+    if not state._apart(to.at, 4 if gcode == 0 else 2):
+        raise ValueError("gradients must not share memory with parameters or states")
+    state._table["grad"] = to.a
     h = _AdamW()
     given = []
     if isinstance(lr, torch.Tensor):
@@ -1070,7 +1083,7 @@ def adamw_step(state, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_deca
         h.stochastic, h.seed, h.offset = 1, _counter(seed, "seed"), _counter(offset, "offset")
     al = _allocator(dev, stream)
     if al is not None:
-        al.uses(*some, *given, *state._all)
+        al.uses(*grads, *given, *state._all)
     _call(dev, "dgrad_adamw_step", lib().dgrad_adamw_step, n, state._address, state._code, gcode, ctypes.byref(h),
           stream=stream)
 
@@ -1094,28 +1107,22 @@ def adamw_moments(state, out=None, stream=None):
         out = tuple(list(ts) for ts in out)
         if len(out) != 2:
             raise ValueError("out: expected two lists of tensors")
-        for ts, what in zip(out, ("m", "v")):
-            if [t.shape for t in ts] != state.shapes:
-                raise ValueError(f"out: {what} must have the parameters' shapes")
-            if {t.dtype for t in ts} != {torch.float32}:
-                raise TypeError(f"out: {what} must be float32")
-            if not all([t.is_cuda and t.is_contiguous() for t in ts]):
-                raise ValueError("tensors must be contiguous CUDA tensors")
-            if {t.get_device() for t in ts} != {dev.index}:
-                raise ValueError("all tensors of one call must be on the same CUDA device")
         given = out[0] + out[1]
-    to = np.array([[t.data_ptr() for t in ts] for ts in out], dtype=np.uint64)
-    size = state._table["n"].astype(np.uint64) * np.uint64(4)
-    if given:
-        lo = np.concatenate([state._lo, *[to[i][size > 0] for i in range(2)]])
-        hi = np.concatenate([state._hi, *[(to[i] + size)[size > 0] for i in range(2)]])
-        order = np.argsort(lo, kind="stable")
-        if np.any(lo[order][1:] < np.maximum.accumulate(hi[order])[:-1]):
-            raise ValueError("out must not share memory with itself or the state")
+        if any(t is None for t in given):
+            raise TypeError("out must be tensors")
+    to = [_Array(np.empty(len(state), dtype=np.uint64)) for _ in range(2)]
+    for ts, at, what in zip(out, to, ("out: m", "out: v")):
+        code, index = _lists().read(ts, state.params, what, at.at, 0)
+        if code != 0:
+            raise TypeError(f"{what} must be float32")
+        if index != dev.index:
+            raise ValueError("all tensors of one call must be on the same CUDA device")
+    if given and not (state._apart(to[0].at, 4) and state._apart(to[1].at, 4) and
+                      _lists().disjoint(to[0].at, to[1].at, state._n.at, len(state), 4)):
+        raise ValueError("out must not share memory with itself or the state")
     if al is not None:
         al.uses(*given, *state._all)
-    _call(dev, "dgrad_adamw_moments", lib().dgrad_adamw_moments, len(state), state._address, to[0].ctypes.data,
-          to[1].ctypes.data, stream=stream)
+    _call(dev, "dgrad_adamw_moments", lib().dgrad_adamw_moments, len(state), state._address, to[0].at, to[1].at, stream=stream)
     return out
 
 
@@ -1141,17 +1148,11 @@ def grad_norm(grads, max_norm=None, workspace=None, stream=None):
     grads = list(grads)
     if not grads:
         raise ValueError("grads: expected at least one tensor")
+    lists = _Array(np.empty((2, len(grads)), dtype=np.int64))     # addresses, elements
+    elements = lists.at + 8 * len(grads)
+    code, _ = _lists().read(grads, None, "gradients", lists.at, elements)
     first = grads[0]
-    if not all([g.is_cuda for g in grads]):
-        raise ValueError("tensors must be CUDA tensors (no CPU path)")
-    if not all([g.is_contiguous() for g in grads]):
-        raise ValueError("tensors must be contiguous")
-    if len({g.dtype for g in grads}) != 1:
-        raise TypeError("gradients must have one dtype")
-    code = _code_of(first.dtype)
     dev = first.device
-    if {g.get_device() for g in grads} != {dev.index}:
-        raise ValueError("all tensors of one call must be on the same CUDA device")
     limit = float("inf") if max_norm is None else float(max_norm)
     given = [] if workspace is None else [workspace]
     _need_cuda(*given)
@@ -1161,9 +1162,7 @@ def grad_norm(grads, max_norm=None, workspace=None, stream=None):
     workspace, ws_bytes = _workspace(al, workspace, first, _norm_workspace(len(grads)))
     if al is not None:
         al.uses(*grads, *given)
-    at = np.array([g.data_ptr() for g in grads], dtype=np.uint64)
-    n = np.array([g.numel() for g in grads], dtype=np.int64)
-    _call(dev, "dgrad_grad_norm", lib().dgrad_grad_norm, len(grads), at.ctypes.data, n.ctypes.data, code, limit,
+    _call(dev, "dgrad_grad_norm", lib().dgrad_grad_norm, len(grads), lists.at, elements, code, limit,
           out.data_ptr(), _ptr(workspace), ws_bytes, stream=stream)
     return out[0] if max_norm is None else (out[0], out[1])
 

@@ -5,16 +5,19 @@ then linked into convolution_backward_b200/libdgrad.so with the CUDA runtime
 linked statically.  ptxas register/spill reports go to _build/ptxas.log.  The
 same sources built with -DDGRAD_DEBUG (objects in _build/debug/) give
 libdgrad_debug.so, whose kernels check every hand-indexed store against its
-output buffer.  Rebuilds only when a source, header or this file is newer than
-a library.
+output buffer.  csrc/tensor_lists.cpp, the binding's reader of tensor lists, becomes the Python
+extension module convolution_backward_b200/_tensor_lists.so (g++, torch's headers).  Rebuilds only
+when a source, header or this file is newer than a library.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,6 +26,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdgrad.so")
 LIB_DEBUG = os.path.join(PKG, "libdgrad_debug.so")
+
+LISTS = os.path.join(PKG, "_tensor_lists.so")
+LISTS_SRC = os.path.join(CSRC, "tensor_lists.cpp")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -51,9 +57,38 @@ def needs_build() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _build_lists() -> None:
+    torch = importlib.util.find_spec("torch")
+    if torch is None or not torch.submodule_search_locations:
+        raise RuntimeError("torch not found: the binding is built against its headers")
+    root = list(torch.submodule_search_locations)[0]
+    tmp = LISTS + f".tmp{os.getpid()}"
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "/usr/local/cuda/include", sysconfig.get_paths()["include"]]
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", *[f"-I{i}" for i in inc], LISTS_SRC, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {LISTS_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, LISTS)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not needs_build():
-        return LIB
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        lists = None
+        if force or not os.path.exists(LISTS) or any(os.path.getmtime(f) > os.path.getmtime(LISTS)
+                                                     for f in (LISTS_SRC, os.path.abspath(__file__))):
+            lists = ex.submit(_build_lists)
+        if force or needs_build():
+            _build_kernels()
+        if lists is not None:
+            lists.result()
+    if verbose:
+        print(f"built {LIB}")
+    return LIB
+
+
+def _build_kernels() -> None:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     srcs, _ = _inputs()
@@ -85,9 +120,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, lib)
-    if verbose:
-        print(f"built {LIB}")
-    return LIB
 
 
 if __name__ == "__main__":

@@ -25,6 +25,8 @@
 // numbers: as easy as 1, 2, 3", 2011) at counter (b, offset) and key seed; elements are counted
 // with every tensor rounded up to whole blocks of 256, element i takes word i % 4 of b = i / 4, its low
 // half for m, its high half for v.
+#include <type_traits>
+
 #include "common.cuh"
 #include "host_util.h"
 #include "launchers.h"
@@ -41,7 +43,7 @@ constexpr int kSteps = kQuant / (32 * 4);       // vectors of four a thread take
 constexpr int kFewTensors = 24, kManyTensors = 380;   // tables; a launch's parameters hold 32764 bytes
 
 struct OptHyper {
-    float lr, b1, c1, b2, c2, eps, decay, wd, ibc1, ibc2, ln_b1, ln_b2;
+    float lr, b1, c1, b2, c2, eps, decay, wd, ibc1, ibc2, ln_b1, ln_b2, zero;   // zero: -0
     const float* lr_dev;         // null: lr and decay above
     const long long* step_dev;   // null: ibc1 and ibc2 above
     const float* scale;          // null: 1
@@ -71,21 +73,19 @@ struct OptTable {
     AdamTensor t[CAP];
 };
 
-// Four elements of kind EK at element i of p (16-byte vectors of fp32, 8-byte of 16 bits), or the
-// `have` that there are.
-template <int EK>
-__device__ __forceinline__ float4 load4(const void* p, long long i, int have, bool vec)
+// Four elements of kind EK at element i of p: FULL, at once (16 bytes of fp32, 8 of 16 bits); else the
+// `have` that there are, one by one.
+template <int EK, bool FULL>
+__device__ __forceinline__ float4 load4(const void* p, long long i, int have)
 {
-    float f[4] = {0.f, 0.f, 0.f, 0.f};
-    if (have == 4 && vec) {
-        if constexpr (EK == kF32) {
-            return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-        } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-            const float2 a = h16x2_to_float2<EK>(u.x), b = h16x2_to_float2<EK>(u.y);
-            return make_float4(a.x, a.y, b.x, b.y);
-        }
+    if constexpr (FULL && EK == kF32) {
+        return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    } else if constexpr (FULL) {
+        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+        const float2 a = h16x2_to_float2<EK>(u.x), b = h16x2_to_float2<EK>(u.y);
+        return make_float4(a.x, a.y, b.x, b.y);
     }
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         if (k < have) {
@@ -98,12 +98,12 @@ __device__ __forceinline__ float4 load4(const void* p, long long i, int have, bo
     return make_float4(f[0], f[1], f[2], f[3]);
 }
 
-template <int EK>
-__device__ __forceinline__ void store4(void* p, long long i, int have, bool vec, float4 x, long long n, int* status)
+template <int EK, bool FULL>
+__device__ __forceinline__ void store4(void* p, long long i, int have, float4 x, long long n, int* status)
 {
     constexpr int es = elem_bytes<EK>();
     char* at = static_cast<char*>(p) + i * es;
-    if (have == 4 && vec) {
+    if constexpr (FULL) {
         if (!store_ok(p, n * es, at, 4 * es, status)) return;
         if constexpr (EK == kF32)
             *reinterpret_cast<float4*>(at) = x;
@@ -122,27 +122,27 @@ __device__ __forceinline__ void store4(void* p, long long i, int have, bool vec,
         }
 }
 
-__device__ __forceinline__ uint32_t load_codes(const void* p, long long i, int have, bool vec)
+template <bool FULL>
+__device__ __forceinline__ uint32_t load_codes(const void* p, long long i, int have)
 {
     const uint8_t* c = static_cast<const uint8_t*>(p) + i;
-    if (have == 4 && vec) return *reinterpret_cast<const uint32_t*>(c);
+    if constexpr (FULL) return *reinterpret_cast<const uint32_t*>(c);
     uint32_t w = 0;
     for (int k = 0; k < have; ++k) w |= static_cast<uint32_t>(c[k]) << (8 * k);
     return w;
 }
 
-__device__ __forceinline__ void store_codes(void* p, long long i, int have, bool vec, uint32_t w, long long n, int* status)
+template <bool FULL>
+__device__ __forceinline__ void store_codes(void* p, long long i, int have, uint32_t w, long long n, int* status)
 {
     uint8_t* c = static_cast<uint8_t*>(p) + i;
-    if (have == 4 && vec) {
+    if constexpr (FULL) {
         if (store_ok(p, n, c, 4, status)) *reinterpret_cast<uint32_t*>(c) = w;
         return;
     }
     for (int k = 0; k < have; ++k)
         if (store_ok(p, n, c + k, 1, status)) c[k] = static_cast<uint8_t>(w >> (8 * k));
 }
-
-__device__ __forceinline__ float elem(const float4& v, int k) { return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w; }
 
 __device__ __forceinline__ uint4 opt_philox(const OptHyper& h, unsigned long long b)
 {
@@ -162,6 +162,21 @@ __device__ __forceinline__ uint4 opt_philox(const OptHyper& h, unsigned long lon
     return make_uint4(c0, c1, c2, c3);
 }
 
+// Pairs of fp32 operations, each rounded on its own.  A packed product and the sum that follows it
+// become one multiply-add in the assembler, rounded once, whatever rounding they name, and so does a
+// multiply-add with a -0 that it can see.  One with a -0 that comes with the call does not.
+struct Packed {
+    float2 zero;     // -0, -0
+    __device__ __forceinline__ float2 mul(float2 a, float2 b) const { return __ffma2_rn(a, b, zero); }
+};
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 pair(float v) { return make_float2(v, v); }
+
+// 2^23 plus byte k of w, or its half h: numbers without the slow conversions.
+__device__ __forceinline__ float byte_float(uint32_t w, int k) { return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | k)); }
+__device__ __forceinline__ float half_float(uint32_t w, int h) { return __uint_as_float(__byte_perm(w, 0x4B000000u, h ? 0x7432u : 0x7410u)); }
+constexpr float kTwo23 = 8388608.0f;
+
 // Values that codes stand for, as multiples of 1/127^2 and 1/255^4 of the block's largest.
 template <bool FOURTH>
 __device__ __forceinline__ float code_value(float c)
@@ -172,14 +187,18 @@ __device__ __forceinline__ float code_value(float c)
 constexpr float kMostM = 16129.0f, kMostV = 4228250625.0f;                 // value(127), value(255)
 constexpr float kUnitM = static_cast<float>(1.0 / 16129.0), kUnitV = static_cast<float>(1.0 / 4228250625.0);
 
-__device__ __forceinline__ float decode_m(int c, float top)
+// The values of codes k and k + 1 of a word of four.
+__device__ __forceinline__ float2 decode_m2(const Packed& P, uint32_t word, int k, float2 top)
 {
-    const float f = static_cast<float>(c);
-    return __fmul_rn(__fmul_rn(__fmul_rn(f, fabsf(f)), kUnitM), top);
+    const uint32_t w = word ^ 0x80808080u;    // c + 128
+    const float2 f = add2(make_float2(byte_float(w, k), byte_float(w, k + 1)), pair(-(kTwo23 + 128.0f)));
+    return P.mul(P.mul(make_float2(__fmul_rn(f.x, fabsf(f.x)), __fmul_rn(f.y, fabsf(f.y))), pair(kUnitM)), top);
 }
-__device__ __forceinline__ float decode_v(uint32_t c, float top)
+__device__ __forceinline__ float2 decode_v2(const Packed& P, uint32_t word, int k, float2 top)
 {
-    return __fmul_rn(__fmul_rn(code_value<true>(static_cast<float>(c)), kUnitV), top);
+    const float2 f = add2(make_float2(byte_float(word, k), byte_float(word, k + 1)), pair(-kTwo23));
+    const float2 q = P.mul(f, f);
+    return P.mul(P.mul(P.mul(q, q), pair(kUnitV)), top);
 }
 
 // What a block's largest value scales the others by: w = (x k) inv, with k a power of two that
@@ -199,25 +218,53 @@ __device__ __forceinline__ CodeScale code_scale(float top)
 
 // The code of x >= 0: low is the largest c with value(c) <= w; the upper neighbour is taken where
 // (w - value(low)) 65536 > (value(low + 1) - value(low)) draw; nearest: draw = 32768.  The
-// approximate roots (2^-22) find low or, so lowered by 2^-10, the code below it.
-template <bool FOURTH>
-__device__ __forceinline__ int code_of(float x, const CodeScale& s, float draw)
+// approximate root r (2^-21) finds low or, lowered by 2^-11, the code below it; that is seen from
+// w - value(low) >= value(low + 1) - value(low).  Then w lies above value(low + 1) by less than 2^-10 of the
+// next step, and low + 1 is taken all the same, but for draws below 64, which set `below`: the codes
+// are formed again by code_of.
+__device__ __forceinline__ float2 low_of(float2 r)
 {
-    constexpr float kTop = FOURTH ? 255.0f : 127.0f;
-    const float w = __fmul_rn(__fmul_rn(x, s.k), s.inv);
-    float r;
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(w));
-    if constexpr (FOURTH) asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(r));
-    float low = fmaxf(rintf(r - (0.5f + 0x1p-10f)), 0.f);
-    float at = code_value<FOURTH>(low), up = code_value<FOURTH>(low + 1.f);
-    if (up <= w) {
-        low += 1.f;
-        at = up;
-        up = code_value<FOURTH>(low + 1.f);
+    const float2 t = add2(add2(add2(r, pair(-(0.5f + 0x1p-11f))), pair(1.5f * kTwo23)), pair(-1.5f * kTwo23));
+    return make_float2(fmaxf(t.x, 0.f), fmaxf(t.y, 0.f));
+}
+template <bool FOURTH>
+__device__ __noinline__ float code_of(float w, float low, float draw)
+{
+    while (code_value<FOURTH>(low + 1.f) <= w && low < 256.f) low += 1.f;
+    const float at = code_value<FOURTH>(low);
+    const float d = __fsub_rn(w, at), step = __fsub_rn(code_value<FOURTH>(low + 1.f), at);
+    return fminf(__fmul_rn(d, 65536.f) > __fmul_rn(step, draw) ? low + 1.f : low, FOURTH ? 255.0f : 127.0f);
+}
+template <bool FOURTH, bool NEAREST>
+__device__ __forceinline__ float2 code2(const Packed& P, float2 w, float2 r, float2 draw, bool& below)
+{
+    float2 low = low_of(r), d, step;    // the largest of a block has low = 126 (254) and goes up: no code passes 127 (255)
+    if constexpr (FOURTH) {
+        const float2 q = P.mul(low, low), next = add2(low, pair(1.f)), q1 = P.mul(next, next);
+        const float2 minus = P.mul(P.mul(q, pair(-1.f)), q);
+        step = add2(P.mul(q1, q1), minus);
+        d = add2(w, minus);
+    } else {     // whole numbers below 2^24: exact
+        step = ffma2(low, pair(2.f), pair(1.f));
+        d = ffma2(P.mul(low, pair(-1.f)), low, w);
     }
-    if (__fmul_rn(__fsub_rn(w, at), 65536.f) > __fmul_rn(__fsub_rn(up, at), draw)) low += 1.f;
-    if (FOURTH && x > 0.f) low = fmaxf(low, 1.f);
-    return static_cast<int>(fminf(low, kTop));
+    if constexpr (NEAREST) {
+        d = add2(d, d);
+    } else {
+        below = below || (d.x >= step.x && draw.x < 64.f) || (d.y >= step.y && draw.y < 64.f);
+        d = P.mul(d, pair(65536.f));
+        step = P.mul(step, draw);
+    }
+    low.x = d.x > step.x ? low.x + 1.f : low.x;
+    low.y = d.y > step.y ? low.y + 1.f : low.y;
+    return low;
+}
+
+__device__ __forceinline__ float root_of(float v)
+{
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 // The largest of a warp's values >= 0 (the order of the bits is that of the values); NaN where
@@ -253,29 +300,164 @@ __device__ __forceinline__ OptStep opt_step(const OptHyper& h)
     return s;
 }
 
-__device__ __forceinline__ float new_weight(float w, float m, float v, const OptHyper& h, const OptStep& s)
+// m', v' and the new weights of a pair; root: that of v'/(1 - b2^t).
+__device__ __forceinline__ void step2(const Packed& P, float2 g, float2& m, float2& v, float2& w, float2& root, const OptHyper& h, const OptStep& s)
 {
-    float root, inv;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v * s.ibc2));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(root + h.eps));
-    return fmaf(s.nlr, m * s.ibc1 * inv, w * s.decay);
+    g = P.mul(g, pair(s.scale));
+    m = add2(P.mul(m, pair(h.b1)), P.mul(g, pair(h.c1)));
+    v = add2(P.mul(v, pair(h.b2)), P.mul(P.mul(g, pair(h.c2)), g));
+    const float2 u = P.mul(v, pair(s.ibc2));
+    float2 inv;
+    // below 2^-126 the root may be 0 beside an eps from 1e-12 on; den is 0 or an ordinary number
+    root = make_float2(root_of(u.x), root_of(u.y));
+    if (h.eps < 1e-12f) {
+        asm("sqrt.approx.f32 %0, %1;" : "=f"(root.x) : "f"(u.x));
+        asm("sqrt.approx.f32 %0, %1;" : "=f"(root.y) : "f"(u.y));
+    }
+    const float2 den = add2(root, pair(h.eps));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv.x) : "f"(den.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv.y) : "f"(den.y));
+    w = ffma2(pair(s.nlr), P.mul(P.mul(m, pair(s.ibc1)), inv), P.mul(w, pair(s.decay)));
 }
 
-__device__ __forceinline__ float new_m(float m, float g, const OptHyper& h)
+// The larger magnitude; NaN where one is NaN.
+__device__ __forceinline__ float larger(float a, float b)
 {
-    return __fadd_rn(__fmul_rn(m, h.b1), __fmul_rn(g, h.c1));
-}
-__device__ __forceinline__ float new_v(float v, float g, const OptHyper& h)
-{
-    return __fadd_rn(__fmul_rn(v, h.b2), __fmul_rn(__fmul_rn(g, h.c2), g));
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+    return r;
 }
 
-// PK, GK: the parameters' and gradients' types; MASTER: an fp32 copy of the parameters is what is
-// stepped.  MODE 0: fp32 states; 1: 8 bits, nearest; 2: 8 bits, stochastic.
+// Block q of 256 elements of tensor t, by a warp.  PK, GK: the parameters' and gradients' types; MASTER: an
+// fp32 copy of the parameters is what is stepped.  MODE 0: fp32 states; 1: 8 bits, nearest; 2: 8 bits,
+// stochastic.  FULL: all of them are there, and every pointer is aligned for four.
+template <int PK, int GK, bool MASTER, int MODE, bool FULL>
+__device__ __forceinline__ void adamw_block(const AdamTensor& t, long long q, const OptHyper& h, const OptStep& st, const Packed& P)
+{
+    const int lane = threadIdx.x & 31;
+    const long long i0 = q * kQuant + lane * 4;
+            float4 g[kSteps], w[kSteps], m[kSteps], v[kSteps];
+            uint32_t cm[kSteps], cv[kSteps];
+            float mtop = 0.f, vtop = 0.f;
+            if constexpr (MODE != 0) {
+                mtop = t.m_max[q];
+                vtop = t.v_max[q];
+            }
+    #pragma unroll
+            for (int j = 0; j < kSteps; ++j) {
+                const long long i = i0 + j * 128;
+                const int have = FULL ? 4 : static_cast<int>(max(0LL, min(4LL, t.n - i)));
+                g[j] = load4<GK, FULL>(t.g, i, have);
+                w[j] = MASTER ? load4<kF32, FULL>(t.w, i, have) : load4<PK, FULL>(t.p, i, have);
+                if constexpr (MODE == 0) {
+                    m[j] = load4<kF32, FULL>(t.m, i, have);
+                    v[j] = load4<kF32, FULL>(t.v, i, have);
+                } else {
+                    cm[j] = load_codes<FULL>(t.m, i, have);
+                    cv[j] = load_codes<FULL>(t.v, i, have);
+                }
+            }
+            float big_m = 0.f, big_v = 0.f;
+            float2 root[kSteps][2];
+    #pragma unroll
+            for (int j = 0; j < kSteps; ++j) {
+                float2 gg[2] = {make_float2(g[j].x, g[j].y), make_float2(g[j].z, g[j].w)};
+                float2 ww[2] = {make_float2(w[j].x, w[j].y), make_float2(w[j].z, w[j].w)};
+                float2 mm[2], vv[2];
+                if constexpr (MODE == 0) {
+                    mm[0] = make_float2(m[j].x, m[j].y);
+                    mm[1] = make_float2(m[j].z, m[j].w);
+                    vv[0] = make_float2(v[j].x, v[j].y);
+                    vv[1] = make_float2(v[j].z, v[j].w);
+                }
+    #pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if constexpr (MODE != 0) {
+                        mm[k] = decode_m2(P, cm[j], 2 * k, pair(mtop));
+                        vv[k] = decode_v2(P, cv[j], 2 * k, pair(vtop));
+                    }
+                    step2(P, gg[k], mm[k], vv[k], ww[k], root[j][k], h, st);
+                    if constexpr (MODE != 0) {
+                        big_m = larger(larger(big_m, mm[k].x), mm[k].y);
+                        big_v = larger(larger(big_v, vv[k].x), vv[k].y);
+                    }
+                }
+                m[j] = make_float4(mm[0].x, mm[0].y, mm[1].x, mm[1].y);
+                v[j] = make_float4(vv[0].x, vv[0].y, vv[1].x, vv[1].y);
+                w[j] = make_float4(ww[0].x, ww[0].y, ww[1].x, ww[1].y);
+            }
+            CodeScale sm, sv;
+            float roots = 0.f;      // root_of(v' inv) = root_of(root roots), where ordinary numbers allow it
+            if constexpr (MODE != 0) {
+                big_m = warp_largest(big_m);
+                big_v = warp_largest(big_v);
+                sm = code_scale<false>(big_m);
+                sv = code_scale<true>(big_v);
+                if (sv.k == 1.0f && st.ibc2 < 0x1p30f) roots = root_of(sv.inv / st.ibc2);
+                const long long nq = (t.n + kQuant - 1) / kQuant;
+                if (lane == 0 && store_ok(t.m_max, nq * 4, t.m_max + q, 4, h.status)) t.m_max[q] = big_m;
+                if (lane == 0 && store_ok(t.v_max, nq * 4, t.v_max + q, 4, h.status)) t.v_max[q] = big_v;
+            }
+    #pragma unroll
+            for (int j = 0; j < kSteps; ++j) {
+                const long long i = i0 + j * 128;
+                const int have = FULL ? 4 : static_cast<int>(max(0LL, min(4LL, t.n - i)));
+                if (MASTER) store4<kF32, FULL>(t.w, i, have, w[j], t.n, h.status);
+                store4<PK, FULL>(t.p, i, have, w[j], t.n, h.status);
+                if constexpr (MODE == 0) {
+                    store4<kF32, FULL>(t.m, i, have, m[j], t.n, h.status);
+                    store4<kF32, FULL>(t.v, i, have, v[j], t.n, h.status);
+                } else {
+                    uint4 bits = make_uint4(0, 0, 0, 0);
+                    if constexpr (MODE == 2)
+                        bits = opt_philox(h, static_cast<unsigned long long>(t.block0 + q) * (kQuant / 4) + lane + j * 32);
+                    const uint32_t word[4] = {bits.x, bits.y, bits.z, bits.w};
+                    uint32_t om[2], ov[2];
+    #pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float2 x = k ? make_float2(m[j].z, m[j].w) : make_float2(m[j].x, m[j].y);
+                        const float2 y = k ? make_float2(v[j].z, v[j].w) : make_float2(v[j].x, v[j].y);
+                        float2 dm = pair(0.f), dv = pair(0.f);
+                        if constexpr (MODE == 2) {
+                            dm = add2(make_float2(half_float(word[2 * k], 0), half_float(word[2 * k + 1], 0)), pair(-kTwo23));
+                            dv = add2(make_float2(half_float(word[2 * k], 1), half_float(word[2 * k + 1], 1)), pair(-kTwo23));
+                        }
+                        float2 wm = make_float2(fabsf(x.x), fabsf(x.y)), wv = y;
+            if (sm.k != 1.0f) wm = P.mul(wm, pair(sm.k));
+            if (sv.k != 1.0f) wv = P.mul(wv, pair(sv.k));
+            wm = P.mul(wm, pair(sm.inv));
+            wv = P.mul(wv, pair(sv.inv));
+                                    const float2 rm = make_float2(root_of(wm.x), root_of(wm.y));
+                        float2 rv = P.mul(root[j][k], pair(roots));
+                        if (roots == 0.f) rv = make_float2(root_of(wv.x), root_of(wv.y));
+                        rv = make_float2(root_of(rv.x), root_of(rv.y));
+                        bool below = false;
+                        float2 a = code2<false, MODE == 1>(P, wm, rm, dm, below), b = code2<true, MODE == 1>(P, wv, rv, dv, below);
+                        if (MODE == 2 && below) {
+                            const float2 la = low_of(rm), lb = low_of(rv);
+                            a = make_float2(code_of<false>(wm.x, la.x, dm.x), code_of<false>(wm.y, la.y, dm.y));
+                            b = make_float2(code_of<true>(wv.x, lb.x, dv.x), code_of<true>(wv.y, lb.y, dv.y));
+                        }
+                        // the low byte of 2^23 + code; m's codes are 128 higher there
+                        const float2 as = add2(make_float2(copysignf(a.x, x.x), copysignf(a.y, x.y)), pair(kTwo23 + 128.0f));
+                        // v' inf is inf, or NaN for 0: 1 or 0
+                    const float inf = __int_as_float(0x7F800000);
+                    const float2 bs = add2(make_float2(fmaxf(b.x, __saturatef(y.x * inf)), fmaxf(b.y, __saturatef(y.y * inf))), pair(kTwo23));
+                        om[k] = __byte_perm(__float_as_uint(as.x), __float_as_uint(as.y), 0x0040);
+                        ov[k] = __byte_perm(__float_as_uint(bs.x), __float_as_uint(bs.y), 0x0040);
+                    }
+                    store_codes<FULL>(t.m, i, have, __byte_perm(om[0], om[1], 0x5410) ^ 0x80808080u, t.n, h.status);
+                    store_codes<FULL>(t.v, i, have, __byte_perm(ov[0], ov[1], 0x5410), t.n, h.status);
+                }
+            }
+}
+
+// A register more than 64 (80) a thread would leave an SM fewer blocks: 60 M parameters, fp32 states, 274 us with
+// four blocks and 301 with three.
 template <int PK, int GK, bool MASTER, int MODE, int CAP>
-__global__ void __launch_bounds__(kOptBlock) adamw_kernel(const __grid_constant__ OptTable<CAP> tab)
+__global__ void __launch_bounds__(kOptBlock, MODE == 0 ? 4 : 3) adamw_kernel(const __grid_constant__ OptTable<CAP> tab)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5;
     // equal runs of chunks
     const unsigned each = tab.chunks / gridDim.x, more = tab.chunks % gridDim.x;
     unsigned c = blockIdx.x * each + min(blockIdx.x, more);
@@ -292,100 +474,17 @@ __global__ void __launch_bounds__(kOptBlock) adamw_kernel(const __grid_constant_
     pdl_trigger();
     const OptHyper& h = tab.h;
     const OptStep st = opt_step(h);
+    const Packed P{make_float2(h.zero, h.zero)};
     if (st.skip) return;
     for (; c < end; ++c) {
         while (tab.first[lo + 1] <= c) ++lo;
         const AdamTensor& t = tab.t[lo];
         const long long q = static_cast<long long>(c - tab.first[lo]) * (kOptBlock / 32) + warp;   // block of 256
-        const long long i0 = q * kQuant + lane * 4;
         if (q * kQuant >= t.n) continue;
-        const bool vec = t.vec != 0;
-        float4 g[kSteps], w[kSteps], m[kSteps], v[kSteps];
-        uint32_t cm[kSteps], cv[kSteps];
-        float mtop = 0.f, vtop = 0.f;
-        if constexpr (MODE != 0) {
-            mtop = t.m_max[q];
-            vtop = t.v_max[q];
-        }
-#pragma unroll
-        for (int j = 0; j < kSteps; ++j) {
-            const long long i = i0 + j * 128;
-            const int have = static_cast<int>(max(0LL, min(4LL, t.n - i)));
-            g[j] = load4<GK>(t.g, i, have, vec);
-            w[j] = MASTER ? load4<kF32>(t.w, i, have, vec) : load4<PK>(t.p, i, have, vec);
-            if constexpr (MODE == 0) {
-                m[j] = load4<kF32>(t.m, i, have, vec);
-                v[j] = load4<kF32>(t.v, i, have, vec);
-            } else {
-                cm[j] = load_codes(t.m, i, have, vec);
-                cv[j] = load_codes(t.v, i, have, vec);
-            }
-        }
-        float big_m = 0.f, big_v = 0.f;
-#pragma unroll
-        for (int j = 0; j < kSteps; ++j) {
-            float mm[4], vv[4], ww[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float gs = __fmul_rn(elem(g[j], k), st.scale);
-                float om, ov;
-                if constexpr (MODE == 0) {
-                    om = elem(m[j], k);
-                    ov = elem(v[j], k);
-                } else {
-                    om = decode_m(static_cast<int8_t>(cm[j] >> (8 * k)), mtop);
-                    ov = decode_v((cv[j] >> (8 * k)) & 0xFFu, vtop);
-                }
-                mm[k] = new_m(om, gs, h);
-                vv[k] = new_v(ov, gs, h);
-                ww[k] = new_weight(elem(w[j], k), mm[k], vv[k], h, st);
-                if constexpr (MODE != 0) {
-                    // the order of the bits is that of the values, and a NaN's lie above
-                    big_m = __uint_as_float(max(__float_as_uint(big_m), __float_as_uint(mm[k]) & 0x7FFFFFFFu));
-                    big_v = __uint_as_float(max(__float_as_uint(big_v), __float_as_uint(vv[k]) & 0x7FFFFFFFu));
-                }
-            }
-            m[j] = make_float4(mm[0], mm[1], mm[2], mm[3]);
-            v[j] = make_float4(vv[0], vv[1], vv[2], vv[3]);
-            w[j] = make_float4(ww[0], ww[1], ww[2], ww[3]);
-        }
-        CodeScale sm, sv;
-        if constexpr (MODE != 0) {
-            big_m = warp_largest(big_m);
-            big_v = warp_largest(big_v);
-            sm = code_scale<false>(big_m);
-            sv = code_scale<true>(big_v);
-            const long long nq = (t.n + kQuant - 1) / kQuant;
-            if (lane == 0 && store_ok(t.m_max, nq * 4, t.m_max + q, 4, h.status)) t.m_max[q] = big_m;
-            if (lane == 0 && store_ok(t.v_max, nq * 4, t.v_max + q, 4, h.status)) t.v_max[q] = big_v;
-        }
-#pragma unroll
-        for (int j = 0; j < kSteps; ++j) {
-            const long long i = i0 + j * 128;
-            const int have = static_cast<int>(max(0LL, min(4LL, t.n - i)));
-            if (MASTER) store4<kF32>(t.w, i, have, vec, w[j], t.n, h.status);
-            store4<PK>(t.p, i, have, vec, w[j], t.n, h.status);
-            if constexpr (MODE == 0) {
-                store4<kF32>(t.m, i, have, vec, m[j], t.n, h.status);
-                store4<kF32>(t.v, i, have, vec, v[j], t.n, h.status);
-            } else {
-                uint4 bits = make_uint4(0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u);
-                if constexpr (MODE == 2)
-                    bits = opt_philox(h, static_cast<unsigned long long>(t.block0 + q) * (kQuant / 4) + lane + j * 32);
-                const uint32_t word[4] = {bits.x, bits.y, bits.z, bits.w};
-                uint32_t om = 0, ov = 0;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float x = elem(m[j], k);
-                    const int a = code_of<false>(fabsf(x), sm, static_cast<float>(word[k] & 0xFFFFu));
-                    const int b = code_of<true>(elem(v[j], k), sv, static_cast<float>(word[k] >> 16));
-                    om |= (static_cast<uint32_t>(x < 0.f ? -a : a) & 0xFFu) << (8 * k);
-                    ov |= static_cast<uint32_t>(b) << (8 * k);
-                }
-                store_codes(t.m, i, have, vec, om, t.n, h.status);
-                store_codes(t.v, i, have, vec, ov, t.n, h.status);
-            }
-        }
+        if (t.vec != 0 && (q + 1) * kQuant <= t.n)
+            adamw_block<PK, GK, MASTER, MODE, true>(t, q, h, st, P);
+        else
+            adamw_block<PK, GK, MASTER, MODE, false>(t, q, h, st, P);
     }
 }
 
@@ -404,6 +503,7 @@ struct MomentTensor {
 
 template <int CAP>
 struct MomentTable {
+    float zero;                   // -0
     int count;
     unsigned chunks;
     int* status;
@@ -433,22 +533,25 @@ __global__ void __launch_bounds__(kOptBlock) moments_kernel(const __grid_constan
         const MomentTensor& t = tab.t[lo];
         const long long q = static_cast<long long>(c - tab.first[lo]) * (kOptBlock / 32) + warp;
         if (q * kQuant >= t.n) continue;
-        const bool vec = t.vec != 0;
         const float mtop = t.m_max[q], vtop = t.v_max[q];
+        const Packed P{make_float2(tab.zero, tab.zero)};
+        const auto block = [&](auto full) {
+            constexpr bool FULL = full.value;
 #pragma unroll
-        for (int j = 0; j < kSteps; ++j) {
-            const long long i = q * kQuant + lane * 4 + j * 128;
-            const int have = static_cast<int>(max(0LL, min(4LL, t.n - i)));
-            const uint32_t cm = load_codes(t.m, i, have, vec), cv = load_codes(t.v, i, have, vec);
-            float m[4], v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                m[k] = decode_m(static_cast<int8_t>(cm >> (8 * k)), mtop);
-                v[k] = decode_v((cv >> (8 * k)) & 0xFFu, vtop);
+            for (int j = 0; j < kSteps; ++j) {
+                const long long i = q * kQuant + lane * 4 + j * 128;
+                const int have = FULL ? 4 : static_cast<int>(max(0LL, min(4LL, t.n - i)));
+                const uint32_t cm = load_codes<FULL>(t.m, i, have), cv = load_codes<FULL>(t.v, i, have);
+                const float2 m0 = decode_m2(P, cm, 0, pair(mtop)), m1 = decode_m2(P, cm, 2, pair(mtop));
+                const float2 v0 = decode_v2(P, cv, 0, pair(vtop)), v1 = decode_v2(P, cv, 2, pair(vtop));
+                store4<kF32, FULL>(t.m_out, i, have, make_float4(m0.x, m0.y, m1.x, m1.y), t.n, tab.status);
+                store4<kF32, FULL>(t.v_out, i, have, make_float4(v0.x, v0.y, v1.x, v1.y), t.n, tab.status);
             }
-            store4<kF32>(t.m_out, i, have, vec, make_float4(m[0], m[1], m[2], m[3]), t.n, tab.status);
-            store4<kF32>(t.v_out, i, have, vec, make_float4(v[0], v[1], v[2], v[3]), t.n, tab.status);
-        }
+        };
+        if (t.vec != 0 && (q + 1) * kQuant <= t.n)
+            block(std::true_type{});
+        else
+            block(std::false_type{});
     }
 }
 
@@ -655,6 +758,7 @@ cudaError_t launch_adamw(const AdamWArgs& a, cudaStream_t stream)
     h.off_lo = static_cast<uint32_t>(a.offset);
     h.off_hi = static_cast<uint32_t>(a.offset >> 32);
     h.status = a.status;
+    h.zero = -0.0f;
     return a.pk == kF32 ? adamw_types<kF32>(a, h, stream) : a.pk == kBF16 ? adamw_types<kBF16>(a, h, stream) : adamw_types<kF16>(a, h, stream);
 }
 
@@ -663,6 +767,7 @@ cudaError_t launch_adamw_moments(const dgrad_adamw_tensor_t* t, float* const* m_
 {
     return in_runs(count, kManyTensors, [&](int64_t begin, int64_t end) {
         MomentTable<kManyTensors> tab;
+        tab.zero = -0.0f;
         tab.count = 0;
         tab.status = status;
         unsigned chunks = 0;
