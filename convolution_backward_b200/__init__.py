@@ -25,6 +25,7 @@ float32, bfloat16 or float16 (16-bit in, 16-bit out, fp32 accumulate).
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import os
@@ -1143,14 +1144,14 @@ def grad_norm(grads, max_norm=None, workspace=None, stream=None):
     (dgrad_grad_norm).  With max_norm: (norm, scale) with scale = min(1, max_norm/(norm + 1e-6)), the
     grad_scale that clips an adamw_step; NaN where the norm is no finite number, which leaves that step
     out.  Nothing waits for the GPU."""
-    import numpy as np
     import torch
     grads = list(grads)
     if not grads:
         raise ValueError("grads: expected at least one tensor")
-    lists = _Array(np.empty((2, len(grads)), dtype=np.int64))     # addresses, elements
-    elements = lists.at + 8 * len(grads)
-    code, _ = _lists().read(grads, None, "gradients", lists.at, elements)
+    lists = array.array("q", bytes(16 * len(grads)))     # addresses, elements
+    at = lists.buffer_info()[0]
+    elements = at + 8 * len(grads)
+    code, _ = _lists().read(grads, None, "gradients", at, elements)
     first = grads[0]
     dev = first.device
     limit = float("inf") if max_norm is None else float(max_norm)
@@ -1158,12 +1159,17 @@ def grad_norm(grads, max_norm=None, workspace=None, stream=None):
     _need_cuda(*given)
     _device_of(first, *given)
     al = _allocator(dev, stream)
-    out = _empty(al, first, (2,), torch.float32)
-    workspace, ws_bytes = _workspace(al, workspace, first, _norm_workspace(len(grads)))
+    ws_bytes = _norm_workspace(len(grads))
+    if workspace is None:       # behind the two results
+        out = _empty(al, first, (4 + ws_bytes // 4,), torch.float32)
+        ws_at = out.data_ptr() + 16
+    else:
+        out = _empty(al, first, (2,), torch.float32)
+        ws_at, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if al is not None:
         al.uses(*grads, *given)
-    _call(dev, "dgrad_grad_norm", lib().dgrad_grad_norm, len(grads), lists.at, elements, code, limit,
-          out.data_ptr(), _ptr(workspace), ws_bytes, stream=stream)
+    _call(dev, "dgrad_grad_norm", lib().dgrad_grad_norm, len(grads), at, elements, code, limit,
+          out.data_ptr(), ws_at, ws_bytes, stream=stream)
     return out[0] if max_norm is None else (out[0], out[1])
 
 

@@ -475,12 +475,71 @@ __global__ void __launch_bounds__(kGnBlock) gn_join_sums_kernel(const GnBwd a)
     if (lane == 0) reinterpret_cast<float2*>(a.ab)[ng] = make_float2(sa / m, sb / m);
 }
 
-template <int EK, int VEC, int ACT>
-__global__ void __launch_bounds__(kGnBlock, 2) gn_dx_kernel(const GnBwd a)
+// dgamma and dbeta of eight adjacent channels: columns of [rows][2][C] fp32 sums.
+struct GnParams {
+    const float* cols;
+    long long rows;
+    int C;
+    void* dgamma;
+    void* dbeta;
+    int* status;
+};
+constexpr int kAcross = 8;
+template <int EK>
+__device__ __forceinline__ void gn_params(const GnParams& a, int block, float2* buf)
 {
-    constexpr int es = elem_bytes<EK>(), NP = gn_pairs<VEC>();
-    __shared__ __align__(16) char ring[gn_ring(VEC) + 16];
+    constexpr int kDown = kGnBlock / kAcross, es = elem_bytes<EK>();
+    const int c = block * kAcross + threadIdx.x % kAcross;
+    float2 s = make_float2(0.f, 0.f);
+    if (c < a.C) {
+        const float* at = a.cols + c;
+#pragma unroll 4
+        for (long long b = threadIdx.x / kAcross; b < a.rows; b += kDown) {
+            s.x += at[b * 2 * a.C];
+            s.y += at[b * 2 * a.C + a.C];
+        }
+    }
+    buf[threadIdx.x] = s;
+    for (int o = kGnBlock / 2; o >= kAcross; o >>= 1) {
+        __syncthreads();
+        if (static_cast<int>(threadIdx.x) < o) {
+            buf[threadIdx.x].x += buf[threadIdx.x + o].x;
+            buf[threadIdx.x].y += buf[threadIdx.x + o].y;
+        }
+    }
+    if (threadIdx.x < kAcross && c < a.C) {
+        RowVec<EK, 1> v;
+        float f[1] = {buf[threadIdx.x].y};
+        v.pack(f);
+        if (a.dgamma && store_ok(a.dgamma, a.C * es, static_cast<char*>(a.dgamma) + c * es, es, a.status)) v.store(a.dgamma, c);
+        f[0] = buf[threadIdx.x].x;
+        v.pack(f);
+        if (a.dbeta && store_ok(a.dbeta, a.C * es, static_cast<char*>(a.dbeta) + c * es, es, a.status)) v.store(a.dbeta, c);
+    }
+}
+
+// Behind the cluster way.
+template <int EK>
+__global__ void __launch_bounds__(kGnBlock) gn_params_kernel(const GnParams a)
+{
+    __shared__ float2 buf[kGnBlock];
+    pdl_wait();
+    pdl_trigger();
+    gn_params<EK>(a, static_cast<int>(blockIdx.x), buf);
+}
+
+template <int EK, int VEC, int ACT>
+__global__ void __launch_bounds__(kGnBlock, 2) gn_dx_kernel(const GnBwd a, const GnParams params, int blocks)
+{
+    constexpr int es = elem_bytes<EK>(), NP = gn_pairs<VEC>(), kBuf = kGnBlock * 8;
+    __shared__ __align__(16) char ring[gn_ring(VEC) > kBuf ? gn_ring(VEC) : kBuf];
     const GnPlan& p = a.p;
+    if (static_cast<int>(blockIdx.x) >= blocks) {    // the blocks behind those of dX
+        pdl_wait();
+        pdl_trigger();
+        if (blockIdx.y == 0) gn_params<EK>(params, static_cast<int>(blockIdx.x) - blocks, reinterpret_cast<float2*>(ring));
+        return;
+    }
     const GnThread<EK, VEC> t(p, blockIdx.y);
     const void* const src[2] = {a.x, a.dy};
     GnDown<EK, VEC, 2> down(src, t, ring);     // as above: read by the kernels before this one
@@ -501,44 +560,6 @@ __global__ void __launch_bounds__(kGnBlock, 2) gn_dx_kernel(const GnBwd a)
         gn_pack<EK, VEC>(v[0], dz);
         if (store_ok(a.dx, bytes, static_cast<char*>(a.dx) + at * es, VEC * es, a.status)) v[0].store(a.dx, at);
     });
-}
-
-// dgamma and dbeta: columns of [rows][2][C] fp32 sums, eight adjacent channels a block.
-template <int EK>
-__global__ void __launch_bounds__(kGnBlock) gn_params_kernel(const float* cols, long long rows, int C, void* dgamma, void* dbeta,
-                                                             int* status)
-{
-    __shared__ float2 buf[kGnBlock];
-    constexpr int kAcross = 8, kDown = kGnBlock / kAcross, es = elem_bytes<EK>();
-    const int c = static_cast<int>(blockIdx.x) * kAcross + threadIdx.x % kAcross;
-    pdl_wait();
-    pdl_trigger();
-    float2 s = make_float2(0.f, 0.f);
-    if (c < C) {
-        const float* at = cols + c;
-#pragma unroll 4
-        for (long long b = threadIdx.x / kAcross; b < rows; b += kDown) {
-            s.x += at[b * 2 * C];
-            s.y += at[b * 2 * C + C];
-        }
-    }
-    buf[threadIdx.x] = s;
-    for (int o = kGnBlock / 2; o >= kAcross; o >>= 1) {
-        __syncthreads();
-        if (static_cast<int>(threadIdx.x) < o) {
-            buf[threadIdx.x].x += buf[threadIdx.x + o].x;
-            buf[threadIdx.x].y += buf[threadIdx.x + o].y;
-        }
-    }
-    if (threadIdx.x < kAcross && c < C) {
-        RowVec<EK, 1> v;
-        float f[1] = {buf[threadIdx.x].y};
-        v.pack(f);
-        if (dgamma && store_ok(dgamma, C * es, static_cast<char*>(dgamma) + c * es, es, status)) v.store(dgamma, c);
-        f[0] = buf[threadIdx.x].x;
-        v.pack(f);
-        if (dbeta && store_ok(dbeta, C * es, static_cast<char*>(dbeta) + c * es, es, status)) v.store(dbeta, c);
-    }
 }
 
 }  // namespace
@@ -588,15 +609,15 @@ size_t groupnorm_backward_workspace_bytes(int64_t N, int64_t S, int64_t C, int64
 cudaError_t launch_groupnorm_backward(const GnBwdArgs& a, cudaStream_t stream)
 {
     const bool params = a.dgamma || a.dbeta;
-    const auto join = [&](long long rows) {
-        auto kernel = a.ek == kF32 ? gn_params_kernel<kF32> : a.ek == kBF16 ? gn_params_kernel<kBF16> : gn_params_kernel<kF16>;
-        return launch_kernel(kernel, dim3(static_cast<unsigned>((a.C + 7) / 8)), dim3(kGnBlock), 0, stream, 1,
-                             static_cast<const float*>(a.ws), rows, static_cast<int>(a.C), a.dgamma, a.dbeta, a.status);
-    };
+    const unsigned across = static_cast<unsigned>((a.C + kAcross - 1) / kAcross);
+    GnParams g{a.ws, 0, static_cast<int>(a.C), a.dgamma, a.dbeta, a.status};
     GnSlices s;
     if (gn_slices(a.N, a.S, a.C, a.G, a.ek, true, &s)) {
         const cudaError_t e = launch_gn_cluster_backward(s, a, params ? a.ws : nullptr, stream);
-        return e != cudaSuccess || !params ? e : join(static_cast<long long>(s.N) * s.K);
+        if (e != cudaSuccess || !params) return e;
+        g.rows = static_cast<long long>(s.N) * s.K;
+        auto kernel = a.ek == kF32 ? gn_params_kernel<kF32> : a.ek == kBF16 ? gn_params_kernel<kBF16> : gn_params_kernel<kF16>;
+        return launch_kernel(kernel, dim3(across), dim3(kGnBlock), 0, stream, 1, g);
     }
     GnBwd f{gn_plan(a.N, a.S, a.C, a.G, a.ek, true), a.dY, a.X, a.gamma, a.beta, a.mean, a.rstd, a.dX, nullptr, nullptr, nullptr,
             a.status};
@@ -614,12 +635,15 @@ cudaError_t launch_groupnorm_backward(const GnBwdArgs& a, cudaStream_t stream)
     const unsigned groups = static_cast<unsigned>((p.N * p.G + kGnBlock / 32 - 1) / (kGnBlock / 32));
     e = launch_kernel(gn_join_sums_kernel, dim3(groups), dim3(kGnBlock), 0, stream, 1, f);
     if (e != cudaSuccess) return e;
-    e = gn_with_kind(a.ek, p.vec, [&](auto ek, auto vec) {
+    // dgamma and dbeta ride behind dX: a launch of their own took 3 us more
+    const int blocks = p.N * p.P;
+    g.rows = blocks;
+    const dim3 both(static_cast<unsigned>(blocks) + (params ? across : 0), grid.y);
+    return gn_with_kind(a.ek, p.vec, [&](auto ek, auto vec) {
         return gn_with_act(a.act, [&](auto act) {
-            return launch_kernel(gn_dx_kernel<ek.value, vec.value, act.value>, grid, dim3(kGnBlock), 0, stream, 1, f);
+            return launch_kernel(gn_dx_kernel<ek.value, vec.value, act.value>, both, dim3(kGnBlock), 0, stream, 1, f, g, blocks);
         });
     });
-    return e != cudaSuccess || !params ? e : join(static_cast<long long>(p.N) * p.P);
 }
 
 }  // namespace dgrad
