@@ -927,14 +927,15 @@ class AdamWState:
     params: one dtype.  32-bit states: m, v fp32 of the parameters' shapes.  8-bit states: m int8 and v
     uint8 codes of the parameters' shapes, and m_max, v_max fp32 with an element for every 256 of a tensor.
     master: fp32 copies of 16-bit parameters, which are then what is stepped.  No two tensors may
-    share memory.  The tensors stay the caller's (save and load them as they are); a parameter
-    whose storage is replaced later is refused by adamw_step."""
+    share memory.  The tensors stay the caller's: save them as they are, load them with copy_; where the
+    storage of one has been replaced, adamw_step refuses the state.  A step writes them without autograd's
+    knowledge: no graph that still needs the old parameters may be alive."""
 
     def __init__(self, params, m, v, master=None, m_max=None, v_max=None):
         import numpy as np
         import torch
-        self.params, self.m, self.v = list(params), list(m), list(v)
-        self.master = None if master is None else list(master)
+        self.params, self.m, self.v = tuple(params), tuple(m), tuple(v)
+        self.master = None if master is None else tuple(master)
         dtype, self.device = _same(self.params, "params")
         self._code = _code_of(dtype)
         self.dtype = dtype
@@ -942,8 +943,8 @@ class AdamWState:
         self.bits = 8 if (self.m and self.m[0].dtype == torch.int8) else 32
         if (self.bits == 8) != (m_max is not None) or (self.bits == 8) != (v_max is not None):
             raise ValueError("m_max and v_max go with int8 m and uint8 v")
-        self.m_max = None if m_max is None else list(m_max)
-        self.v_max = None if v_max is None else list(v_max)
+        self.m_max = None if m_max is None else tuple(m_max)
+        self.v_max = None if v_max is None else tuple(v_max)
         lists = [("m", self.m, torch.int8 if self.bits == 8 else torch.float32),
                  ("v", self.v, torch.uint8 if self.bits == 8 else torch.float32), ("master", self.master, torch.float32)]
         self.shapes = [tuple(p.shape) for p in self.params]
@@ -964,7 +965,7 @@ class AdamWState:
         everything = [t for ts in (self.params, self.m, self.v, self.master, self.m_max, self.v_max) if ts for t in ts]
         _need_cuda(*everything)
         _device_of(*everything)
-        self._all = everything
+        self._list, self._all = list(self.params), everything
         self._table = np.zeros(n, dtype=_TABLE)
         for name, ts in (("param", self.params), ("m", self.m), ("v", self.v), ("master", self.master),
                          ("m_max", self.m_max), ("v_max", self.v_max)):
@@ -976,7 +977,7 @@ class AdamWState:
         if status == 1:
             raise ValueError("parameters and states must not share memory")
         _check(status, "dgrad_adamw_check")
-        self._where = _Array(np.ascontiguousarray(self._table["param"]))
+        self._where = _Array(np.array([t.data_ptr() for t in everything], dtype=np.uint64))
         self._n = _Array(np.ascontiguousarray(self._table["n"]))
         # the written ranges in order, for gradients and results to be held against
         lo = np.array([t.data_ptr() for t in everything if t.numel()], dtype=np.uint64)
@@ -1038,7 +1039,8 @@ def adamw_step(state, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_deca
 
     grads: one tensor per parameter, of its shape and of the parameters' dtype or float32 (one dtype
     for the list), or None for a parameter that is left as it is.  step counts from 1.  step and lr
-    may be one-element CUDA tensors (int64, float32), which a captured step reads in every replay.
+    may be one-element CUDA tensors (int64, float32), which a captured step reads in every replay (a step
+    below 1 or a rate that is no finite number changes nothing).
     grad_scale: a one-element fp32 CUDA tensor that multiplies the gradients (grad_norm's factor); where
     it is no finite number the step changes nothing.  seed (8-bit states): codes are
     rounded stochastically by the bits of (seed, offset): give every step its own pair, and dropout others;
@@ -1049,15 +1051,15 @@ def adamw_step(state, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_deca
     grads = list(grads)
     dev = state.device
     to = state._grads
-    gcode, gdev = _lists().read(grads, state.params, "gradients", to.at, 0)
+    gcode, gdev = _lists().read(grads, state._list, "gradients", to.at, 0)
     if gcode < 0:
         gcode, gdev = state._code, dev.index     # nothing to step
     if gcode != state._code and gcode != 0:
         raise TypeError(f"gradients must be {state.dtype} or float32")
     if gdev != dev.index:
         raise ValueError("all tensors of one call must be on the same CUDA device")
-    if not _lists().same(state.params, state._where.at):
-        raise ValueError("a parameter's storage has changed since its AdamWState was made")
+    if not _lists().same(state._all, state._where.at):
+        raise ValueError("a parameter's or state's storage has changed since its AdamWState was made")
     if not state._apart(to.at, 4 if gcode == 0 else 2):
         raise ValueError("gradients must not share memory with parameters or states")
     state._table["grad"] = to.a
@@ -1076,6 +1078,11 @@ def adamw_step(state, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_deca
     if grad_scale is not None:
         h.grad_scale = _scalar(grad_scale, torch.float32, dev, "grad_scale")
         given.append(grad_scale)
+    if given:
+        scalars = array.array("q", [t.data_ptr() for t in given] + [1] * len(given))
+        where = scalars.buffer_info()[0]
+        if not _lists().apart(where, where + 8 * len(given), len(given), 8, state._lo.at, state._hi.at, len(state._lo.a)):
+            raise ValueError("lr, step and grad_scale must not share memory with parameters or states")
     h.beta1, h.beta2 = betas
     h.eps, h.weight_decay, h.state_bits = eps, weight_decay, state.bits
     if seed is not None:
@@ -1090,7 +1097,7 @@ def adamw_step(state, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_deca
 
 
 def adamw_moments(state, out=None, stream=None):
-    """(m, v): what a state's moments stand for, as lists of fp32 tensors (dgrad_adamw_moments): for
+    """(m, v): what a state's moments stand for, as fp32 tensors (dgrad_adamw_moments): for
     checkpoints, or to go on with 32-bit states.  32-bit states are returned as they are.  out: two lists of
     fp32 tensors of the parameters' shapes to write to."""
     import numpy as np
@@ -1111,9 +1118,11 @@ def adamw_moments(state, out=None, stream=None):
         given = out[0] + out[1]
         if any(t is None for t in given):
             raise TypeError("out must be tensors")
+    if not _lists().same(state._all, state._where.at):
+        raise ValueError("a parameter's or state's storage has changed since its AdamWState was made")
     to = [_Array(np.empty(len(state), dtype=np.uint64)) for _ in range(2)]
     for ts, at, what in zip(out, to, ("out: m", "out: v")):
-        code, index = _lists().read(ts, state.params, what, at.at, 0)
+        code, index = _lists().read(ts, state._list, what, at.at, 0)
         if code != 0:
             raise TypeError(f"{what} must be float32")
         if index != dev.index:

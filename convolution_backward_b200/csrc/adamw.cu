@@ -289,11 +289,13 @@ __device__ __forceinline__ OptStep opt_step(const OptHyper& h)
     }
     if (h.lr_dev) {
         const float lr = *h.lr_dev;
+        s.skip = s.skip || !isfinite(lr);
         s.nlr = -lr;
         s.decay = fmaf(-lr, h.wd, 1.f);
     }
     if (h.step_dev) {
         const float t = static_cast<float>(*h.step_dev);
+        s.skip = s.skip || t < 1.f;
         s.ibc1 = -1.f / expm1f(t * h.ln_b1);
         s.ibc2 = -1.f / expm1f(t * h.ln_b2);
     }

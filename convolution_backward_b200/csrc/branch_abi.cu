@@ -46,7 +46,7 @@ dgrad_status_t done(cudaError_t e)
 }
 
 constexpr int64_t kMaxRows = 0x7FFFFFFFLL;
-constexpr int64_t kMaxGatedRows = INT64_C(1) << 30;   // rows rounded up to a tile stay within 32 bits
+constexpr int64_t kMaxGatedRows = INT64_C(1) << 30;   // rows rounded up to a tile, blocks for them, stay within 32 bits
 constexpr int64_t kMaxChannels = 65536;
 
 dgrad_status_t ln_shape(int64_t M, int64_t C, dgrad_dtype_t dtype)
@@ -72,7 +72,7 @@ static_assert(int(DGRAD_ACT_SILU) == dgrad::kSilu && int(DGRAD_ACT_GELU) == dgra
 dgrad_status_t gn_shape(int64_t N, int64_t S, int64_t C, int64_t G, dgrad_dtype_t dtype)
 {
     if (!valid_dtype(dtype) || N < 0 || S < 0 || C < 1 || G < 1 || C % G) return DGRAD_ERR_INVALID;
-    if (C > kMaxChannels || N > kMaxRows || S > kMaxRows || N * S > kMaxRows || N * G > kMaxRows)
+    if (C > kMaxChannels || N > kMaxGatedRows || S > kMaxGatedRows || N * S > kMaxGatedRows || N * G > kMaxGatedRows)
         return DGRAD_ERR_UNSUPPORTED;
     return DGRAD_OK;
 }

@@ -223,6 +223,13 @@ struct GnFwd {
     int* status;
 };
 
+// The squares about the mean, of squares about another value: not below zero, infinite where those are
+// (and the mean's part is too), NaN where they are.
+__device__ __forceinline__ float left_of(float squares, float about)
+{
+    return squares == __int_as_float(0x7F800000) ? squares : about < 0.f ? 0.f : about;
+}
+
 template <int EK, int VEC>
 __global__ void __launch_bounds__(kGnBlock) gn_stats_kernel(const GnFwd a)
 {
@@ -264,8 +271,8 @@ __global__ void __launch_bounds__(kGnBlock) gn_stats_kernel(const GnFwd a)
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const float2 d = __fmul2_rn(s1[i], splat(rk));
-        s2[i] = ffma2(gn_minus(s1[i]), d, s2[i]);
-        s2[i] = make_float2(s2[i].x < 0.f ? 0.f : s2[i].x, s2[i].y < 0.f ? 0.f : s2[i].y);   // NaN stays
+        const float2 about = ffma2(gn_minus(s1[i]), d, s2[i]);
+        s2[i] = make_float2(left_of(s2[i].x, about.x), left_of(s2[i].y, about.y));
         K[i] = __fadd2_rn(d, gn_minus(K[i]));
         s1[i] = __fmul2_rn(K[i], splat(k));
     }

@@ -303,9 +303,10 @@ dgrad_status_t dgrad_gated_backward_workspace(int64_t M, int64_t C, int64_t F, s
  *     z = (x - mean)*rstd*gamma + beta,  Y = act(z).
  * All element types (gamma, beta [C] and Y have X's).  gamma or beta null: ones, zeros.
  * mean, rstd (fp32, [N][G] each, either may be null) are what the backward pass needs.
- * Y may be X.  eps finite and >= 0.  G divides C (else DGRAD_ERR_INVALID).  A group that
- * holds an infinity or NaN becomes NaN, and so do its mean and rstd.  C <= 65536, N*S and
- * N*G < 2^31 (else DGRAD_ERR_UNSUPPORTED).  N or S of 0: nothing but mean and rstd is
+ * Y may be X.  eps finite and >= 0 (at eps 0 a constant group gives NaN).  G divides C (else
+ * DGRAD_ERR_INVALID).  A group that holds an infinity or NaN becomes NaN, and so do its mean and rstd;
+ * one whose squares pass fp32's range has rstd 0.  C <= 65536, N*S and N*G <= 2^30 (else
+ * DGRAD_ERR_UNSUPPORTED).  N or S of 0: nothing but mean and rstd is
  * written, and those are NaN (sums over no values).  workspace: at least
  * dgrad_groupnorm_forward_workspace bytes (0 for sizes that need none; it may be null then), 16-byte
  * aligned, as for layer norm's gradients. */
@@ -395,7 +396,8 @@ typedef struct {
 /* The AdamW step, with g = grad_scale*grad:
  *     m' = beta1 m + (1 - beta1) g,   v' = beta2 v + (1 - beta2) g g,
  *     p' = p (1 - lr weight_decay) - lr (m'/(1 - beta1^t)) / (sqrt(v'/(1 - beta2^t)) + eps),
- * all in fp32; p is the master copy where there is one (both are written), and is rounded once
+ * (a t below 1 or an lr that is no finite number, read from device memory, leaves the step out as a
+ * grad_scale does), all in fp32; p is the master copy where there is one (both are written), and is rounded once
  * to the parameter's type.  param_type: any; grad_type: the same or DGRAD_F32.
  * 8-bit states enter p' unrounded.  Their codes are defined by fp32 operations, each rounded
  * (in the order written: m' = beta1*m + (1-beta1)*g, v' = beta2*v + ((1-beta2)*g)*g), so that

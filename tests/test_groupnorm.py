@@ -287,6 +287,61 @@ def test_forward_far_mean_and_odd_rows(shape, way):
 
 
 @pytest.mark.gpu
+def test_squares_past_the_range(way):
+    """Values whose squares pass fp32's range: rstd 0, and beta is left; the other groups are untouched."""
+    x, g, b, _ = _inputs(3, 300, 32, "f32", seed=4)
+    clean = cb.groupnorm_forward(x, 4, g, b)
+    x[1, :, :8] *= 1e25
+    y, mean, rstd = cb.groupnorm_forward(x, 4, g, b, stats=True)
+    assert torch.equal(y[1, :, :8], b[:8].expand(300, 8)) and rstd[1, 0] == 0 and torch.isfinite(mean).all()
+    assert torch.equal(y[1, :, 8:], clean[1, :, 8:]) and torch.equal(y[0], clean[0])
+    cb.check_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [64, 61])
+def test_two_streams_at_once(C, way):
+    """Two calls that overlap, each with its own workspace, on streams of their own."""
+    G = 8 if C == 64 else 61
+    sets = [_inputs(6, 900, C, "bf16", seed=k) for k in (1, 2)]
+    want = []
+    for x, g, b, dy in sets:
+        o = cb.groupnorm_forward(x, G, g, b, act="gelu", stats=True)
+        want.append((*o, *cb.groupnorm_backward(dy, x, o[1], o[2], g, b, act="gelu")))
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for (x, g, b, dy), s in zip(sets, streams):
+            with torch.cuda.stream(s):
+                o = cb.groupnorm_forward(x, G, g, b, act="gelu", stats=True)
+                got.append((*o, *cb.groupnorm_backward(dy, x, o[1], o[2], g, b, act="gelu")))
+        torch.cuda.synchronize()
+        for w, q in zip(want, got):
+            assert all(torch.equal(p, r) for p, r in zip(w, q))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [96, 99])
+def test_past_32_bits(C):
+    """More than 2^31 elements: the last samples against the same samples alone."""
+    N, S = 34, -(-(1 << 31) // (33 * C))
+    r = torch.Generator(device="cuda").manual_seed(1)
+    few = torch.randn(2, S, C, device="cuda", generator=r).bfloat16()
+    x = few.repeat(N // 2, 1, 1)
+    assert x.numel() > 1 << 31
+    g, b = torch.rand(C, device="cuda").bfloat16() + 0.5, torch.rand(C, device="cuda").bfloat16()
+    y, mean, rstd = cb.groupnorm_forward(x, 3, g, b, act="silu", stats=True)
+    assert all(torch.equal(y[k], y[k % 2]) for k in range(2, N))
+    ref = branch.groupnorm(to64(few[1:, :, :]), 3, to64(g), to64(b), 1e-5, "silu")
+    assert np.abs(to64(mean[N - 1]) - ref[1][0]).max() < 1e-4 and np.abs(to64(rstd[N - 1]) / ref[2][0] - 1).max() < 1e-4
+    assert np.abs(to64(y[N - 1]) - ref[0][0]).max() <= 2.0 ** -8 * np.abs(ref[0]).max() + 1e-3
+    dx, dg, db = cb.groupnorm_backward(y, x, mean, rstd, g, b, act="silu", out=y)
+    assert all(torch.equal(dx[k], dx[k % 2]) for k in range(2, N))
+    cb.check_status()
+
+
+@pytest.mark.gpu
 def test_no_samples_and_no_positions():
     g = torch.ones(8, device="cuda")
     for shape in ((0, 4, 8), (2, 0, 8), (2, 3, 0, 8)):

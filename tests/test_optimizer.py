@@ -500,6 +500,65 @@ def test_device_step_and_rate_in_a_graph(bits):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_device_scalars_that_say_nothing_leave_the_step_out(bits):
+    _, grads, state = _make([700, 3], "f32", "f32", False, bits, seed=9)
+    before = _snapshot(state)
+    zero = torch.zeros(1, dtype=torch.int64, device="cuda")
+    _step(state, grads, zero)
+    _step(state, grads, zero - 5)
+    for bad in (float("nan"), float("inf")):
+        _step(state, grads, 1, lr=torch.tensor(bad, device="cuda"))
+    _check_step(before, state, [None, None], "f32", "left out")
+    _step(state, grads, zero + 1)
+    _check_step(before, state, grads, "f32", "step 1")
+
+
+@pytest.mark.gpu
+def test_replaced_states_and_shared_scalars_are_refused():
+    _, grads, state = _make([300, 3], "f32", "f32", False, 8, seed=9)
+    with pytest.raises(ValueError, match="must not share"):
+        _step(state, grads, 1, grad_scale=state.params[0][:1])
+    with pytest.raises(ValueError, match="must not share"):
+        _step(state, grads, 1, lr=state.m_max[0][1:2])
+    assert isinstance(state.params, tuple) and isinstance(state.m_max, tuple)
+    state.m[1].data = state.m[1].clone()
+    with pytest.raises(ValueError, match="storage"):
+        _step(state, grads, 1)
+    with pytest.raises(ValueError, match="storage"):
+        cb.adamw_moments(state)
+
+
+@pytest.mark.gpu
+def test_one_tensor_past_32_bits():
+    """More than 2^31 elements in one tensor, and one behind it in the list: its end against the same
+    values alone."""
+    n, tail = (1 << 31) + 1000, 5000
+    p = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    r = torch.Generator(device="cuda").manual_seed(3)
+    p[-tail:] = torch.randn(tail, device="cuda", generator=r).bfloat16()
+    g[-tail:] = torch.randn(tail, device="cuda", generator=r).bfloat16()
+    at = (n - tail) // 256 * 256
+    small_p, small_g = p[at:].clone(), g[at:].clone()
+    state, small = cb.adamw_state([p, small_p], bits=8), cb.adamw_state([small_p.clone()], bits=8)
+    _step(state, [g, small_g], 1)
+    _step(small, [small_g], 1)
+    assert torch.equal(state.params[0][at:], small.params[0]) and torch.equal(state.params[1], small.params[0])
+    assert torch.equal(state.m[0][at:], small.m[0]) and torch.equal(state.v[0][at:], small.v[0])
+    assert torch.equal(state.v_max[0][at // 256:], small.v_max[0]) and not state.m[0][:at].any()
+    _step(state, [g, small_g], 2, seed=7, offset=1)
+    first = -(-n // 256) * 256       # the second tensor's elements are counted from there
+    before = optim.decode_m(_np(small.m[0]), _np(small.m_max[0]))
+    m, _ = optim.moments(before, before, _np(small_g.float()), 1.0, HYPER["beta1"], HYPER["beta2"])
+    d, _ = optim.draws(first, -(-m.size // 256) * 256, 7, 1)
+    assert np.array_equal(_np(state.m[1]), optim.encode(m, 2, d)[0])
+    ref = optim.norm([to64(g[-tail:])])
+    assert abs(cb.grad_norm([g]).item() - ref) <= 2 * E32 * ref
+    cb.check_status()
+
+
+@pytest.mark.gpu
 def test_on_another_stream():
     _, grads, state = _make([70_000, 33], "f32", "f32", False, 8, seed=10)
     before = _snapshot(state)
