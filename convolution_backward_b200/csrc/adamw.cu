@@ -764,11 +764,14 @@ cudaError_t launch_adamw(const AdamWArgs& a, cudaStream_t stream)
     return a.pk == kF32 ? adamw_types<kF32>(a, h, stream) : a.pk == kBF16 ? adamw_types<kBF16>(a, h, stream) : adamw_types<kF16>(a, h, stream);
 }
 
-cudaError_t launch_adamw_moments(const dgrad_adamw_tensor_t* t, float* const* m_out, float* const* v_out, int64_t count,
-                                 int* status, cudaStream_t stream)
+namespace {
+
+template <int CAP>
+cudaError_t moments_runs(const dgrad_adamw_tensor_t* t, float* const* m_out, float* const* v_out, int64_t count, int* status,
+                         cudaStream_t stream)
 {
-    return in_runs(count, kManyTensors, [&](int64_t begin, int64_t end) {
-        MomentTable<kManyTensors> tab;
+    return in_runs(count, CAP, [&](int64_t begin, int64_t end) {
+        MomentTable<CAP> tab;
         tab.zero = -0.0f;
         tab.count = 0;
         tab.status = status;
@@ -776,7 +779,7 @@ cudaError_t launch_adamw_moments(const dgrad_adamw_tensor_t* t, float* const* m_
         for (int64_t i = begin; i < end; ++i) {
             if (t[i].n == 0) continue;
             const bool vec = ((reinterpret_cast<uintptr_t>(t[i].m) | reinterpret_cast<uintptr_t>(t[i].v)) & 3) == 0 &&
-                             ((reinterpret_cast<uintptr_t>(m_out[i]) | reinterpret_cast<uintptr_t>(v_out[i])) & 15) == 0;
+                             on4<kF32>(m_out[i]) && on4<kF32>(v_out[i]);
             tab.first[tab.count] = chunks;
             tab.t[tab.count++] = {t[i].m, t[i].v, t[i].m_max, t[i].v_max, m_out[i], v_out[i], t[i].n, vec};
             chunks += static_cast<unsigned>((t[i].n + kOptChunk - 1) / kOptChunk);
@@ -784,8 +787,17 @@ cudaError_t launch_adamw_moments(const dgrad_adamw_tensor_t* t, float* const* m_
         tab.first[tab.count] = chunks;
         tab.chunks = chunks;
         if (chunks == 0) return cudaSuccess;
-        return launch_kernel(moments_kernel<kManyTensors>, dim3(opt_grid(chunks, 8)), dim3(kOptBlock), 0, stream, 1, tab);
+        return launch_kernel(moments_kernel<CAP>, dim3(opt_grid(chunks, 8)), dim3(kOptBlock), 0, stream, 1, tab);
     });
+}
+
+}  // namespace
+
+cudaError_t launch_adamw_moments(const dgrad_adamw_tensor_t* t, float* const* m_out, float* const* v_out, int64_t count,
+                                 int* status, cudaStream_t stream)
+{
+    return count <= kFewTensors ? moments_runs<kFewTensors>(t, m_out, v_out, count, status, stream)
+                                : moments_runs<kManyTensors>(t, m_out, v_out, count, status, stream);
 }
 
 namespace {

@@ -519,7 +519,8 @@ bool choose(int64_t N, int64_t S, int64_t C, int64_t G, int ek, bool backward, G
             if (rest + step_bytes > limit) continue;
             const int64_t fit = (limit - rest) / step_bytes, cap = steps < fit ? steps : fit;
             if (!forced && (cap < steps || waves > 1)) continue;
-            const double sectors = tw * es < 32 ? 3.5 : tw * es < 64 ? 1.2 : 1.0;    // half-used ones
+            // half-used sectors; fp32 rows of two vectors were as slow (1 x 16384 x 128 backward 21 us, streaming 16)
+            const double sectors = tw * es < 32 ? 3.5 : tw * es >= 64 ? 1.0 : es == 4 ? 2.2 : 1.2;
             const double cost = (backward ? 5.6 : 5.2) + (K == 1 ? 0.0 : 1.0 + 0.15 * K) +
                                 step_us * sectors * static_cast<double>(waves * on_sm) * static_cast<double>(2 * steps - cap);
             if (cost >= best) continue;

@@ -287,6 +287,35 @@ def test_forward_far_mean_and_odd_rows(shape, way):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("shape", [(60, 24, 8), (60, 32, 32), (50, 40, 8)], ids=IDS)
+def test_nan_and_far_values_stay_in_their_group(shape, act, way):
+    """Groups that end inside a 16-byte vector: a NaN, an infinity or a gamma that takes the activation to its ends in
+    one of them changes nothing in the others."""
+    S, C, G = shape
+    D = C // G
+    for dtype in TYPES:
+        x, g, b, dy = _inputs(2, S, C, dtype, seed=S)
+        y, mean, rstd = cb.groupnorm_forward(x, G, g, b, act=act, stats=True)
+        grads = cb.groupnorm_backward(dy, x, mean, rstd, g, b, act=act)
+        keep = torch.ones(C, dtype=torch.bool, device="cuda")
+        keep[D:2 * D] = keep[3 * D:4 * D] = False
+        for bad in (float("nan"), float("inf"), None):
+            z, h = x.clone(), g.clone()
+            if bad is None:
+                h[~keep] = 6e4
+            else:
+                z[1, 7, D], z[0, 3, 3 * D] = bad, -bad
+            y2, m2, r2 = cb.groupnorm_forward(z, G, h, b, act=act, stats=True)
+            d2 = cb.groupnorm_backward(dy, z, m2, r2, h, b, act=act)
+            assert torch.equal(y2[..., keep], y[..., keep]) and torch.equal(d2[0][..., keep], grads[0][..., keep])
+            assert torch.equal(d2[1][keep], grads[1][keep]) and torch.equal(d2[2][keep], grads[2][keep])
+            if bad is None and act in ("silu", "gelu", "gelu_tanh", "relu"):
+                assert not (y2[..., ~keep] < -1).any() and torch.isfinite(y2.float()).any()
+    cb.check_status()
+
+
+@pytest.mark.gpu
 def test_squares_past_the_range(way):
     """Values whose squares pass fp32's range: rstd 0, and beta is left; the other groups are untouched."""
     x, g, b, _ = _inputs(3, 300, 32, "f32", seed=4)
