@@ -479,7 +479,7 @@ int64_t gcd(int64_t a, int64_t b) { return b == 0 ? a : gcd(b, a % b); }
 // device time).  The cluster way is 5.2 us (backward 5.6) and 0.38 us (0.75) for each step of its
 // busiest SM, and 1.3 to 2.2 us more for clusters of 2 to 8, as long as everything stays in shared memory
 // and rows fill their 32-byte sectors; the streaming way 8.5 us and 0.25 us per MB of tensors (10 and
-// 0.33), and 0.008 for each block that shares a sample.  So the cluster way takes what one
+// 0.33, fp32 0.22), and 0.008 for each block that shares a sample.  So the cluster way takes what one
 // wave of blocks holds: 16 x 256 x 1024 channels, 32 groups: 8.8 us forward against 13.4, 1 x 64 x 512: 5.2
 // against 6.6, backward 6.1 against 8.0; 16 x 4096 x 384 would be 41 us against 34.
 bool choose(int64_t N, int64_t S, int64_t C, int64_t G, int ek, bool backward, GnSlices* out)
@@ -493,7 +493,7 @@ bool choose(int64_t N, int64_t S, int64_t C, int64_t G, int ek, bool backward, G
     if (unit > C || unit / vec > kT) return false;
     const double mb = static_cast<double>(N) * S * C * es * (backward ? 3e-6 : 2e-6);
     const double blocks = (backward ? 296.0 : 592.0) / static_cast<double>(N);
-    const double streaming = (backward ? 10.0 + 0.33 * mb : 8.5 + 0.25 * mb) + 0.008 * (blocks < S / 16.0 ? blocks : S / 16.0) +
+    const double streaming = (backward ? 10.0 + (es == 4 ? 0.22 : 0.33) * mb : 8.5 + 0.25 * mb) + 0.008 * (blocks < S / 16.0 ? blocks : S / 16.0) +
                              (vec == 1 ? 3.0 : 0.0);
     if (!forced && mb > 64.0) return false;
     const int64_t units = C / unit;
