@@ -4,9 +4,10 @@
 // For each element, all in fp32, with g = scale * grad:
 //     m' = b1 m + (1 - b1) g,   v' = b2 v + (1 - b2) g g
 //     p' = p (1 - lr wd) - lr (m' / (1 - b1^t)) / (sqrt(v' / (1 - b2^t)) + eps)
-// A handful of operations for 22 to 28 bytes: HBM bounds it.  A launch takes a table of
+// A handful of operations for 22 to 28 bytes (8-bit states 10 to 18): HBM bounds it, the 8-bit step its
+// instructions.  A launch takes a table of
 // tensors among its parameters (no copy to the device, nothing kept between calls, so a
-// captured step carries its own), and its blocks take equal runs of 1024-element chunks.
+// captured step carries its own), and its blocks take equal runs of 2048-element chunks.
 //
 // 8-bit states.  Blocks of 256 elements of a tensor share the largest |m| and the largest v
 // (fp32, M and V).  Codes are linear in the square root of a gradient's magnitude:
@@ -18,7 +19,7 @@
 // A code stands for the nearer of two values (the lower at a tie), or with a seed for the upper with
 // probability (w - low)/(high - low): what nearest rounding keeps losing, a v that moves by less
 // than half a step at a time, adds up on average.  The stored bits are defined by fp32
-// operations each rounded on its own (no fused multiply-add), given beside code_of, so that
+// operations each rounded on its own (no fused multiply-add), given in include/dgrad.h, so that
 // a step's states can be reproduced exactly.  A warp holds a block: one reduction for M, one for V.
 //
 // Random bits: Philox-4x32-10 (J. Salmon, M. Moraes, R. Dror and D. Shaw, "Parallel random

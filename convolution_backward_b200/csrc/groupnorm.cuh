@@ -256,7 +256,7 @@ struct GnSlices {
     int R, parts;                // positions at a time, column_totals' parts
     int K;                       // blocks of a cluster
     int rpc;                     // positions of a block
-    int cap;                     // steps of R positions that are kept
+    int cap;                     // steps of R positions, at most
     int ng;                      // groups of a slice, at most
     int smem;
 };

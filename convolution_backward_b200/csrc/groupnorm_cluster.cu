@@ -5,8 +5,7 @@
 // needs stays on the SM: forward X, backward X and dz in fp32, so that the activation's
 // derivative (two or three of the slow exponential and reciprocal instructions) is formed once.
 // A thread's steps lie at its own places in shared memory, 16 bytes next to those of its
-// neighbours, and nobody else reads them.  Positions beyond `cap` steps do not fit and are read
-// again (forward twice) from L2.
+// neighbours, and nobody else reads them.  The way is taken where all of them fit.
 // The forward pass takes the block's mean, then the squares about it, and the blocks of the
 // cluster join both over distributed shared memory:
 //     mean = sum count_k mean_k / m,  M2 = sum (M2_k + count_k (mean_k - mean)^2),
@@ -65,8 +64,8 @@ __device__ __forceinline__ float peer_float(const float* p, uint32_t rank)
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// The 2 ng values of every block of the cluster, in this block's `buf` or behind the others: all remote
-// loads under way at once.  Complete on return.
+// The 2 ng values of every block of the cluster, in this block's shared memory: all remote loads under
+// way at once.  Complete on return.
 __device__ __forceinline__ const float* gather(const GnShared& sh, const GnSlices& p)
 {
     for (int i = threadIdx.x; i < p.K * 2 * p.ng; i += kT) {
@@ -133,16 +132,16 @@ __global__ void __launch_bounds__(kT, 2) gn_cluster_fwd_kernel(const GnCluster a
     pdl_wait();
     pdl_trigger();
     const GnItem it(p, t, static_cast<int>(blockIdx.x / static_cast<unsigned>(p.K)));
+    const int kept = it.steps, ng = it.width / p.D;
     // step q: x to its place
     auto bring = [&](int q) {
         if (VEC > 1) {
-            if (q < min(it.steps, p.cap)) gn_copy16(mine + q * kT * 16, static_cast<const char*>(a.x) + (it.first + q * stride) * es);
+            if (q < kept) gn_copy16(mine + q * kT * 16, static_cast<const char*>(a.x) + (it.first + q * stride) * es);
             gn_copy_commit();
         }
     };
 #pragma unroll
     for (int q = 0; q < kAheadFwd; ++q) bring(q);
-    const int kept = min(it.steps, p.cap), ng = it.width / p.D;
     const long long stat_at = static_cast<long long>(it.n) * p.G + it.c0 / p.D;
 
     // the block's mean
@@ -182,11 +181,6 @@ __global__ void __launch_bounds__(kT, 2) gn_cluster_fwd_kernel(const GnCluster a
             bring(k + kAheadFwd);
         }
     }
-    for (; k < it.steps; ++k) {
-        V v;
-        v.load(a.x, it.first + k * stride);
-        add(v);
-    }
     column_totals<kT, VEC>(s, it.on, t.r, t.c, p.R, p.tw, p.parts, sh.buf, sh.part, sh.out);
     group_totals<kT, 1>(sh.out, p.tw, 1, p.tw, 0, it.width, p.D, sh.ex, p.ng);
     const float count = static_cast<float>(t.rows) * static_cast<float>(p.D);
@@ -210,11 +204,6 @@ __global__ void __launch_bounds__(kT, 2) gn_cluster_fwd_kernel(const GnCluster a
     for (k = 0; k < kept; ++k) {
         V v;
         v.load(mine, static_cast<long long>(k) * kT * VEC);
-        square(v);
-    }
-    for (; k < it.steps; ++k) {
-        V v;
-        v.load(a.x, it.first + k * stride);
         square(v);
     }
     if constexpr (VEC == 1) s[0].y = 0.f;
@@ -276,11 +265,6 @@ __global__ void __launch_bounds__(kT, 2) gn_cluster_fwd_kernel(const GnCluster a
             v.load(mine, static_cast<long long>(k) * kT * VEC);
             finish(v, k);
         }
-        for (int q = k; q < it.steps; ++q) {
-            V v;
-            v.load(a.x, it.first + q * stride);
-            finish(v, q);
-        }
     }
     if (p.K > 1) cluster_wait();
 }
@@ -301,10 +285,11 @@ __global__ void __launch_bounds__(kT, 2) gn_cluster_bwd_kernel(const GnCluster a
     pdl_wait();
     pdl_trigger();
     const GnItem it(p, t, static_cast<int>(blockIdx.x / static_cast<unsigned>(p.K)));
+    const int kept = it.steps, ng = it.width / p.D;
     // step q: x to its place, dy to where its dz will be
     auto bring = [&](int q) {
         if (VEC > 1) {
-            if (q < min(it.steps, p.cap)) {
+            if (q < kept) {
                 gn_copy16(mine + q * kT * 16, static_cast<const char*>(a.x) + (it.first + q * stride) * es);
                 gn_copy16(mine_dz + q * NQ * kT * 4, static_cast<const char*>(a.dy) + (it.first + q * stride) * es);
             }
@@ -313,7 +298,6 @@ __global__ void __launch_bounds__(kT, 2) gn_cluster_bwd_kernel(const GnCluster a
     };
 #pragma unroll
     for (int q = 0; q < kAheadBwd; ++q) bring(q);
-    const int kept = min(it.steps, p.cap), ng = it.width / p.D;
     const long long stat_at = static_cast<long long>(it.n) * p.G + it.c0 / p.D;
 
     float2 mean[NP], rstd[NP], gamma[NP], beta[NP];
@@ -336,17 +320,15 @@ __global__ void __launch_bounds__(kT, 2) gn_cluster_bwd_kernel(const GnCluster a
     auto take = [&](const V& xv, const V& dv, int step) {
         float2 n[NP], dz[NP];
         slope(xv, dv, n, dz);
-        if (step < kept) {
-            if constexpr (VEC == 1) {
-                xv.store(mine, static_cast<long long>(step) * kT * VEC);
-                mine_dz[step * kT] = dz[0].x;
-            } else {
-#pragma unroll
-                for (int q = 0; q < NQ; ++q)
-                    *reinterpret_cast<float4*>(mine_dz + (step * NQ + q) * kT * 4) =
-                        make_float4(dz[2 * q].x, dz[2 * q].y, dz[2 * q + 1].x, dz[2 * q + 1].y);
-            }
-        }
+                    if constexpr (VEC == 1) {
+                        xv.store(mine, static_cast<long long>(step) * kT * VEC);
+                        mine_dz[step * kT] = dz[0].x;
+                    } else {
+        #pragma unroll
+                        for (int q = 0; q < NQ; ++q)
+                            *reinterpret_cast<float4*>(mine_dz + (step * NQ + q) * kT * 4) =
+                                make_float4(dz[2 * q].x, dz[2 * q].y, dz[2 * q + 1].x, dz[2 * q + 1].y);
+                    }
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             A[i] = __fadd2_rn(A[i], dz[i]);
@@ -356,7 +338,7 @@ __global__ void __launch_bounds__(kT, 2) gn_cluster_bwd_kernel(const GnCluster a
     int k = 0;
     if constexpr (VEC == 1) {
         constexpr int U = 4;
-        for (; k + U <= it.steps; k += U) {
+        for (; k + U <= kept; k += U) {
             V xv[U], dv[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -376,11 +358,13 @@ __global__ void __launch_bounds__(kT, 2) gn_cluster_bwd_kernel(const GnCluster a
             bring(k + kAheadBwd);
         }
     }
-    for (; k < it.steps; ++k) {
-        V xv, dv;
-        xv.load(a.x, it.first + k * stride);
-        dv.load(a.dy, it.first + k * stride);
-        take(xv, dv, k);
+    if constexpr (VEC == 1) {
+        for (; k < kept; ++k) {
+            V xv, dv;
+            xv.load(a.x, it.first + k * stride);
+            dv.load(a.dy, it.first + k * stride);
+            take(xv, dv, k);
+        }
     }
     float* const outA = sh.out;
     float* const outB = sh.out + p.tw;
@@ -448,14 +432,6 @@ __global__ void __launch_bounds__(kT, 2) gn_cluster_bwd_kernel(const GnCluster a
             for (int i = 0; i < NP; ++i) n[i] = __fmul2_rn(__fadd2_rn(n[i], gn_minus(mean[i])), rstd[i]);
             finish(xv, n, dz, k);
         }
-        for (int q = k; q < it.steps; ++q) {
-            V xv, dv;
-            float2 n[NP], dz[NP];
-            xv.load(a.x, it.first + q * stride);
-            dv.load(a.dy, it.first + q * stride);
-            slope(xv, dv, n, dz);
-            finish(xv, n, dz, q);
-        }
     }
     if (p.K > 1) cluster_wait();
 }
@@ -466,10 +442,6 @@ cudaError_t launch(Kernel kernel, const GnCluster& c, cudaStream_t stream)
     const GnSlices& p = c.p;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), p.smem);
     if (e != cudaSuccess) return e;
-    if (p.K > 8) {
-        e = allow_large_clusters(reinterpret_cast<const void*>(kernel));
-        if (e != cudaSuccess) return e;
-    }
     return launch_kernel(kernel, dim3(static_cast<unsigned>(p.N * p.slices * p.K)), dim3(kT), p.smem, stream, p.K, c);
 }
 
@@ -484,7 +456,7 @@ int64_t gcd(int64_t a, int64_t b) { return b == 0 ? a : gcd(b, a % b); }
 // against 6.6, backward 6.1 against 8.0; 16 x 4096 x 384 would be 41 us against 34.
 bool choose(int64_t N, int64_t S, int64_t C, int64_t G, int ek, bool backward, GnSlices* out)
 {
-    const char* way = tuning_env("DGRAD_GN_WAY");      // 's', 'c': always the streaming, the cluster way
+    const char* way = tuning_env("DGRAD_GN_WAY");      // 's': always the streaming way; 'c': the cluster way wherever it fits
     if (way && way[0] == 's') return false;
     const bool forced = way && way[0] == 'c';
     const int es = ek == kF32 ? 4 : 2, full = 16 / es;
@@ -516,13 +488,11 @@ bool choose(int64_t N, int64_t S, int64_t C, int64_t G, int ek, bool backward, G
             const int64_t room = K == 1 ? 148 : 8 * (18 / K) * K;
             const int64_t on_sm = ctas <= room ? 1 : 2, waves = (ctas + 2 * room - 1) / (2 * room);
             const int64_t limit = on_sm == 1 ? 232448 : 115712;
-            if (rest + step_bytes > limit) continue;
-            const int64_t fit = (limit - rest) / step_bytes, cap = steps < fit ? steps : fit;
-            if (!forced && (cap < steps || waves > 1)) continue;
+            if (rest + steps * step_bytes > limit || (!forced && waves > 1)) continue;
             // half-used sectors; fp32 rows of two vectors were as slow (1 x 16384 x 128 backward 21 us, streaming 16)
             const double sectors = tw * es < 32 ? 3.5 : tw * es >= 64 ? 1.0 : es == 4 ? 2.2 : 1.2;
             const double cost = (backward ? 5.6 : 5.2) + (K == 1 ? 0.0 : 1.0 + 0.15 * K) +
-                                step_us * sectors * static_cast<double>(waves * on_sm) * static_cast<double>(2 * steps - cap);
+                                step_us * sectors * static_cast<double>(waves * on_sm * steps);
             if (cost >= best) continue;
             best = cost;
             GnSlices& p = *out;
@@ -538,10 +508,10 @@ bool choose(int64_t N, int64_t S, int64_t C, int64_t G, int ek, bool backward, G
             p.R = static_cast<int>(R);
             p.K = K;
             p.rpc = static_cast<int>(rpc);
-            p.cap = static_cast<int>(cap);
+            p.cap = static_cast<int>(steps);
             p.ng = ng;
-            p.smem = static_cast<int>(gn_up(static_cast<size_t>(cap) * kT * vec * es) +
-                                      (backward ? gn_up(static_cast<size_t>(cap) * kT * vec * 4) : 0)) + rest;
+            p.smem = static_cast<int>(gn_up(static_cast<size_t>(steps) * kT * vec * es) +
+                                      (backward ? gn_up(static_cast<size_t>(steps) * kT * vec * 4) : 0)) + rest;
         }
     }
     if (best >= 1e300) return false;

@@ -51,22 +51,6 @@ inline cudaError_t ensure_smem_limit(const void* kernel, int bytes)
     return cudaSuccess;
 }
 
-// Let a kernel run in clusters of more than eight blocks, once per (kernel, device).
-inline cudaError_t allow_large_clusters(const void* kernel)
-{
-    static std::mutex mu;
-    static std::vector<std::pair<const void*, int>> done;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lk(mu);
-    for (const auto& x : done)
-        if (x.first == kernel && x.second == dev) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess) done.push_back({kernel, dev});
-    return e;
-}
-
 // Clusters of the launch `cfg` that can be resident at once, asked once per (kernel, device);
 // `fallback` where the question fails (asked again by the next call).
 inline int resident_clusters(const void* kernel, const cudaLaunchConfig_t& cfg, int fallback)

@@ -166,7 +166,7 @@ def test_binding_refusals():
 
 @pytest.fixture(params=["", "s", "c"], ids=["auto", "streaming", "cluster"])
 def way(request, monkeypatch):
-    """The library's own choice between its two ways, and each of them at every size it serves."""
+    """The library's own choice between its two ways, the streaming one everywhere, the cluster one wherever it fits."""
     monkeypatch.setenv("DGRAD_GN_WAY", request.param)
     cb._gn_workspace.cache_clear()
     yield request.param
@@ -523,7 +523,7 @@ def test_every_store_in_bounds(shape, dtype, monkeypatch, way):
 @pytest.mark.parametrize("cluster", [1, 2, 4, 8])
 @pytest.mark.parametrize("shape", [(3, 700, 96, 8, 2), (2, 1000, 40, 1, 1), (1, 4001, 66, 6, 3), (5, 9, 256, 32, 5), (2, 6000, 24, 8, 1)], ids=IDS)
 def test_cluster_sizes(shape, cluster, dtype, monkeypatch):
-    """Every cluster size; slices of unequal width; blocks without positions; more positions than stay in
+    """Every cluster size; slices of unequal width; blocks without positions; more positions than fit the
     shared memory."""
     N, S, C, G, slices = shape
     monkeypatch.setenv("DGRAD_GN_WAY", "c")
