@@ -41,7 +41,9 @@ constexpr int kQuant = 256;                     // elements that share M and V: 
 constexpr int kOptChunk = kQuant * (kOptBlock / 32);   // elements a block takes at a time
 constexpr int kSteps = kQuant / (32 * 4);       // vectors of four a thread takes of it
 
-constexpr int kFewTensors = 24, kManyTensors = 380;   // tables; a launch's parameters hold 32764 bytes
+// Tensors of a launch's table (its parameters hold 32764 bytes).  The small one takes the host 2.2 us less
+// a call (10 tensors: a step 6.5 us, 8.7 with the large one); the device does not tell them apart.
+constexpr int kFewTensors = 24, kManyTensors = 380;
 
 struct OptHyper {
     float lr, b1, c1, b2, c2, eps, decay, wd, ibc1, ibc2, ln_b1, ln_b2, zero;   // zero: -0
@@ -560,7 +562,7 @@ __global__ void __launch_bounds__(kOptBlock) moments_kernel(const __grid_constan
 
 // ----------------------------------------------------------- the gradients' norm
 
-constexpr int kFewNorms = 64, kManyNorms = 1600;
+constexpr int kFewNorms = 64, kManyNorms = 1600;   // as above: 13.2 us of host time a call, 15.7
 constexpr int kNormChunk = 4096;     // elements a block takes at a time: 16 a thread
 
 struct NormTensor {
