@@ -20,6 +20,8 @@
 // bounds what cancellation costs wherever the mean lies.  From there means and squares about them
 // are joined, over the block's threads and over the blocks:
 //     mean = sum count_i mean_i / sum count_i,  M2 = sum (M2_i + count_i (mean_i - mean)^2).
+// Means are joined as differences to one of them, so that a mean far above the spread is rounded to its own
+// last place and no more, and that of equal values is the value.
 // All sums and statistics are fp32 in a fixed order (no atomics): results repeat bit for bit.
 #include "groupnorm.cuh"
 
@@ -230,8 +232,10 @@ __device__ __forceinline__ float left_of(float squares, float about)
     return squares == __int_as_float(0x7F800000) ? squares : about < 0.f ? 0.f : about;
 }
 
+// Four blocks an SM, and room for the loads of single elements (16 x 4096 x 384 fp32: 59.8 us, 60.9 with the registers that
+// the compiler takes by itself; 3 x 1961 x 1001 fp32 21.6, 26.9).
 template <int EK, int VEC>
-__global__ void __launch_bounds__(kGnBlock) gn_stats_kernel(const GnFwd a)
+__global__ void __launch_bounds__(kGnBlock, 4) gn_stats_kernel(const GnFwd a)
 {
     constexpr int Q = kGnBlock * VEC, NP = gn_pairs<VEC>();
     __shared__ __align__(16) char mem[gn_shared(VEC)];
@@ -239,6 +243,7 @@ __global__ void __launch_bounds__(kGnBlock) gn_stats_kernel(const GnFwd a)
     float* const out = buf + Q;
     float* const mean = out + Q;
     float* const part = mean + Q;
+    __shared__ float one[Q];
     const GnPlan& p = a.p;
     const GnThread<EK, VEC> t(p, blockIdx.y);
     pdl_wait();
@@ -268,13 +273,26 @@ __global__ void __launch_bounds__(kGnBlock) gn_stats_kernel(const GnFwd a)
     });
     // a column's mean and squares about it; the block's mean of every group; the squares about that
     const float k = static_cast<float>(t.steps), rk = t.steps > 0 ? 1.f / k : 0.f;
+    float2 w[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const float2 d = __fmul2_rn(s1[i], splat(rk));
         const float2 about = ffma2(gn_minus(s1[i]), d, s2[i]);
         s2[i] = make_float2(left_of(s2[i].x, about.x), left_of(s2[i].y, about.y));
-        K[i] = __fadd2_rn(d, gn_minus(K[i]));
-        s1[i] = __fmul2_rn(K[i], splat(k));
+        w[i] = __fadd2_rn(d, gn_minus(K[i]));
+    }
+    // the means less one of them, each group's own (of the middle row of threads: some steps' mean, not a single value
+    // that may lie far from all others)
+    if (t.on && t.r == (min(p.R, t.rows) >> 1)) gn_each_first<VEC>(t.group, p.D, t.c == 0, w, [&](int g, float v) { one[g] = v; });
+    __syncthreads();
+    if (t.on) {
+        gn_by_group<VEC>(t.group, p.D, w, [&](int g) { return one[g]; });
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const float2 above = gn_minus(__fadd2_rn(K[i], w[i]));
+            K[i] = ffma2(s1[i], splat(rk), above);
+            s1[i] = ffma2(above, splat(k), s1[i]);
+        }
     }
     column_totals<kGnBlock, VEC>(s1, t.on, t.r, t.c, p.R, p.tw, p.down, buf, part, out);
     group_totals<kGnBlock, 1>(out, Q, 1, p.tw, t.c0, t.c1, p.D, mean, Q);
@@ -292,7 +310,7 @@ __global__ void __launch_bounds__(kGnBlock) gn_stats_kernel(const GnFwd a)
     column_totals<kGnBlock, VEC>(s2, t.on, t.r, t.c, p.R, p.tw, p.down, buf, part, out);
     group_totals<kGnBlock, 1>(out, Q, 1, p.tw, t.c0, t.c1, p.D, buf, Q);
     float2* to = reinterpret_cast<float2*>(a.part) + static_cast<long long>(blockIdx.x) * p.parts;
-    for (int j = threadIdx.x; j < t.groups; j += kGnBlock) to[t.g0 + j + blockIdx.y] = make_float2(mean[j], buf[j]);
+    for (int j = threadIdx.x; j < t.groups; j += kGnBlock) to[t.g0 + j + blockIdx.y] = make_float2(one[j] + mean[j], buf[j]);
 }
 
 // Joins the parts of every group: a warp each.

@@ -85,6 +85,22 @@ __device__ __forceinline__ void gn_by_group(GnGroup k, int D, float2 (&f)[gn_pai
     for (int i = 0; i < gn_pairs<VEC>(); ++i) f[i] = make_float2(a[2 * i], a[2 * i + 1]);
 }
 
+// put(group, value) for each of a thread's columns that is its group's first in the tile; start: the thread's first column
+// is the tile's.
+template <int VEC, typename Put>
+__device__ __forceinline__ void gn_each_first(GnGroup k, int D, bool start, const float2 (&f)[gn_pairs<VEC>()], Put put)
+{
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        if (k.left == 0) {
+            ++k.g;
+            k.left = D;
+        }
+        if (k.left == D || (start && i == 0)) put(k.g, i % 2 ? f[i / 2].y : f[i / 2].x);
+        --k.left;
+    }
+}
+
 __device__ __forceinline__ float2 gn_minus(float2 v) { return make_float2(-v.x, -v.y); }
 
 // A pair's products, each rounded: never one half of a multiply-add with what follows.
@@ -206,6 +222,13 @@ __device__ __forceinline__ void group_totals(const float* in, int in_stride, int
         }
     }
     __syncthreads();
+}
+
+// Whether the mean of `count` values lies far above their spread, eight standard deviations or more (M2: the squares
+// about it): a few roundings of such a mean are no longer small beside the spread.
+__device__ __forceinline__ bool gn_far(float mean, float M2, float count)
+{
+    return mean * mean * count > 64.f * M2 || (M2 == 0.f && mean != 0.f);   // squares of small values are 0
 }
 
 // A thread's own copies of 16 bytes from global to shared memory: nobody else reads them, so

@@ -8,8 +8,9 @@
 // neighbours, and nobody else reads them.  The way is taken where all of them fit.
 // The forward pass takes the block's mean, then the squares about it, and the blocks of the
 // cluster join both over distributed shared memory:
-//     mean = sum count_k mean_k / m,  M2 = sum (M2_k + count_k (mean_k - mean)^2),
-// so nothing cancels however far the mean lies.  The backward pass adds its blocks' sums.
+//     mean = sum count_k mean_k / m,  M2 = sum (M2_k + count_k (mean_k - mean)^2).
+// A mean formed as a sum is a few roundings of itself off; one that lies far above the spread, or is that of equal
+// values, is formed again from the differences to it (finish_far_slice).  The backward pass adds its blocks' sums.
 // A block ends only when the others have read what it left for them.
 #include "groupnorm.cuh"
 
@@ -118,8 +119,123 @@ struct GnItem {
     }
 };
 
+// The statistics of a slice's groups, from what its blocks have in ex: stat on return, and a.mean and a.rstd.  Whole
+// block.  MARK: true where a mean is far above the spread, and that group's rstd in stat is negative.  The
+// cluster's blocks find the same.
+template <bool MARK>
+__device__ __forceinline__ bool slice_statistics(const GnCluster& a, const GnShared& sh, int rank, int ng, long long stat_at)
+{
+    const GnSlices& p = a.p;
+    if (p.K > 1) cluster_sync();
+    const float m = static_cast<float>(p.S) * static_cast<float>(p.D);
+    const float* all = sh.ex;
+    if (p.K > 1) all = gather(sh, p);
+    bool far = false;
+    for (int j = threadIdx.x; j < ng; j += kT) {
+        float mu = sh.ex[j], sq = sh.ex[p.ng + j];
+        if (p.K > 1) {
+            const float mu0 = all[j];
+            float d = 0.f;
+            for (int q = 1; q < p.K; ++q) d += (all[q * 2 * p.ng + j] - mu0) * count_of(p, q);
+            mu = mu0 + d / m;
+            sq = 0.f;
+            for (int q = 0; q < p.K; ++q) {
+                const float e = all[q * 2 * p.ng + j] - mu;
+                sq += fmaf(e * count_of(p, q), e, all[(q * 2 + 1) * p.ng + j]);
+            }
+        }
+        const float rs = 1.0f / sqrtf(sq / m + a.eps);
+        sh.stat[j] = mu;
+        const bool again = MARK && gn_far(mu, sq, m);
+        sh.stat[p.ng + j] = again ? -rs : rs;
+        far = far || again;
+        if (rank == 0) {
+            const long long at = stat_at + j, all_of = static_cast<long long>(p.N) * p.G * 4;
+            if (a.mean && store_ok(a.mean, all_of, a.mean + at, 4, a.status)) a.mean[at] = mu;
+            if (a.rstd && store_ok(a.rstd, all_of, a.rstd + at, 4, a.status)) a.rstd[at] = rs;
+        }
+    }
+    if (p.K > 1) cluster_arrive();   // this block has read the others' values
+    return __syncthreads_or(far);    // in the place of the barrier behind stat: one more took 0.1 us of 5.1
+}
+
+// Y of the values that a thread keeps.
 template <int EK, int VEC, int ACT>
-__global__ void __launch_bounds__(kT, 2) gn_cluster_fwd_kernel(const GnCluster a)
+__device__ __forceinline__ void slice_results(const GnCluster& a, const GnShared& sh, const char* mine, const GnLane& t, const GnItem& it)
+{
+    constexpr int es = elem_bytes<EK>(), NP = gn_pairs<VEC>();
+    const GnSlices& p = a.p;
+    if (!it.on) return;
+    float2 mean[NP], scale[NP], beta[NP];
+    gn_by_group<VEC>(t.group, p.D, mean, [&](int g) { return sh.stat[g]; });
+    gn_by_group<VEC>(t.group, p.D, scale, [&](int g) { return sh.stat[p.ng + g]; });
+    gn_param<EK, VEC>(a.gamma, it.c0 + t.col, 1.f, beta);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) scale[i] = __fmul2_rn(scale[i], beta[i]);
+    gn_param<EK, VEC>(a.beta, it.c0 + t.col, 0.f, beta);
+    const long long bytes = static_cast<long long>(p.N) * p.S * p.C * es, stride = static_cast<long long>(p.R) * p.C;
+    for (int k = 0; k < it.steps; ++k) {
+        RowVec<EK, VEC> v;
+        float2 f[NP];
+        v.load(mine, static_cast<long long>(k) * kT * VEC);
+        gn_unpack<EK, VEC>(v, f);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) f[i] = gate_act<ACT>(ffma2(__fadd2_rn(f[i], gn_minus(mean[i])), scale[i], beta[i]));
+        gn_pack<EK, VEC>(v, f);
+        const long long at = it.first + k * stride;
+        if (store_ok(a.y, bytes, static_cast<char*>(a.y) + at * es, VEC * es, a.status)) v.store(a.y, at);
+    }
+}
+
+// What is left of a slice where a mean is far above the spread: the statistics once more, with the blocks' means of
+// such groups formed from the differences to the first mean, and the results.  A function of its own that the kernel ends
+// with: what every other slice goes through keeps its registers (16 x 1024 x 512 bf16 13.0 us; a call that returned 13.4, the same
+// code in place 13.4).
+template <int EK, int VEC, int ACT>
+__device__ __noinline__ void finish_far_slice(const GnCluster& a)
+{
+    extern __shared__ __align__(16) char smem[];
+    constexpr int es = elem_bytes<EK>(), NP = gn_pairs<VEC>();
+    const GnSlices& p = a.p;
+    const GnShared sh(smem + gn_up(static_cast<size_t>(p.cap) * kT * VEC * es), p, std::integral_constant<int, VEC>{});
+    const char* const mine = smem + threadIdx.x * VEC * es;
+    const GnLane t(p, std::integral_constant<int, VEC>{});
+    const GnItem it(p, t, static_cast<int>(blockIdx.x / static_cast<unsigned>(p.K)));
+    const int ng = it.width / p.D;
+    const float count = count_of(p, t.rank);
+    if (p.K > 1) cluster_wait();
+    float2 s[NP], mean[NP];
+    gn_set<VEC>(mean, 0.f);
+#pragma unroll 1
+    for (int squares = 0; squares < 2; ++squares) {
+        if (it.on) gn_by_group<VEC>(t.group, p.D, mean, [&](int g) { return squares ? sh.ex[g] : sh.stat[g]; });
+        gn_set<VEC>(s, 0.f);
+        for (int k = 0; k < it.steps; ++k) {
+            RowVec<EK, VEC> v;
+            float2 d[NP];
+            v.load(mine, static_cast<long long>(k) * kT * VEC);
+            gn_unpack<EK, VEC>(v, d);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                d[i] = __fadd2_rn(d[i], gn_minus(mean[i]));
+                s[i] = squares ? ffma2(d[i], d[i], s[i]) : __fadd2_rn(s[i], d[i]);
+            }
+        }
+        column_totals<kT, VEC>(s, it.on, t.r, t.c, p.R, p.tw, p.parts, sh.buf, sh.part, sh.out);
+        group_totals<kT, 1>(sh.out, p.tw, 1, p.tw, 0, it.width, p.D, squares ? sh.ex + p.ng : sh.all, p.ng);
+        if (!squares) {
+            for (int j = threadIdx.x; j < ng; j += kT)
+                if (t.rows && sh.stat[p.ng + j] < 0.f) sh.ex[j] = sh.stat[j] + sh.all[j] / count;
+            __syncthreads();
+        }
+    }
+    slice_statistics<false>(a, sh, t.rank, ng, static_cast<long long>(it.n) * p.G + it.c0 / p.D);
+    slice_results<EK, VEC, ACT>(a, sh, mine, t, it);
+    if (p.K > 1) cluster_wait();
+}
+
+template <int EK, int VEC, int ACT>
+__global__ void __launch_bounds__(kT, 2) gn_cluster_fwd_kernel(const __grid_constant__ GnCluster a)
 {
     extern __shared__ __align__(16) char smem[];
     using V = RowVec<EK, VEC>;
@@ -210,62 +326,11 @@ __global__ void __launch_bounds__(kT, 2) gn_cluster_fwd_kernel(const GnCluster a
     column_totals<kT, VEC>(s, it.on, t.r, t.c, p.R, p.tw, p.parts, sh.buf, sh.part, sh.out);
     group_totals<kT, 1>(sh.out, p.tw, 1, p.tw, 0, it.width, p.D, sh.ex + p.ng, p.ng);
 
-    // the group's statistics
-    if (p.K > 1) cluster_sync();
-    const float m = static_cast<float>(p.S) * static_cast<float>(p.D);
-    const float* all = sh.ex;
-    if (p.K > 1) all = gather(sh, p);
-    for (int j = threadIdx.x; j < ng; j += kT) {
-        float mu = sh.ex[j], sq = sh.ex[p.ng + j];
-        if (p.K > 1) {
-            const float mu0 = all[j];
-            float d = 0.f;
-            for (int q = 1; q < p.K; ++q) d += (all[q * 2 * p.ng + j] - mu0) * count_of(p, q);
-            mu = mu0 + d / m;
-            sq = 0.f;
-            for (int q = 0; q < p.K; ++q) {
-                const float e = all[q * 2 * p.ng + j] - mu;
-                sq += fmaf(e * count_of(p, q), e, all[(q * 2 + 1) * p.ng + j]);
-            }
-        }
-        const float rs = 1.0f / sqrtf(sq / m + a.eps);
-        sh.stat[j] = mu;
-        sh.stat[p.ng + j] = rs;
-        if (t.rank == 0) {
-            const long long at = stat_at + j, all_of = static_cast<long long>(p.N) * p.G * 4;
-            if (a.mean && store_ok(a.mean, all_of, a.mean + at, 4, a.status)) a.mean[at] = mu;
-            if (a.rstd && store_ok(a.rstd, all_of, a.rstd + at, 4, a.status)) a.rstd[at] = rs;
-        }
+    if (slice_statistics<true>(a, sh, t.rank, ng, stat_at)) {
+        finish_far_slice<EK, VEC, ACT>(a);
+        return;
     }
-    if (p.K > 1) cluster_arrive();   // this block has read the others' values
-    __syncthreads();
-
-    k = 0;
-    if (it.on) {
-        float2 scale[NP], beta[NP];
-        gn_by_group<VEC>(t.group, p.D, mean, [&](int g) { return sh.stat[g]; });
-        gn_by_group<VEC>(t.group, p.D, scale, [&](int g) { return sh.stat[p.ng + g]; });
-        gn_param<EK, VEC>(a.gamma, it.c0 + t.col, 1.f, beta);
-#pragma unroll
-        for (int i = 0; i < NP; ++i) scale[i] = __fmul2_rn(scale[i], beta[i]);
-        gn_param<EK, VEC>(a.beta, it.c0 + t.col, 0.f, beta);
-        const long long bytes = static_cast<long long>(p.N) * p.S * p.C * es;
-        auto finish = [&](V& v, int step) {
-            float2 f[NP];
-            gn_unpack<EK, VEC>(v, f);
-#pragma unroll
-            for (int i = 0; i < NP; ++i)
-                f[i] = gate_act<ACT>(ffma2(__fadd2_rn(f[i], gn_minus(mean[i])), scale[i], beta[i]));
-            gn_pack<EK, VEC>(v, f);
-            const long long at = it.first + step * stride;
-            if (store_ok(a.y, bytes, static_cast<char*>(a.y) + at * es, VEC * es, a.status)) v.store(a.y, at);
-        };
-        for (; k < kept; ++k) {
-            V v;
-            v.load(mine, static_cast<long long>(k) * kT * VEC);
-            finish(v, k);
-        }
-    }
+    slice_results<EK, VEC, ACT>(a, sh, mine, t, it);
     if (p.K > 1) cluster_wait();
 }
 

@@ -1,0 +1,44 @@
+"""The AdamW step, its states and the gradients' norm at their edges: subnormal eps; tensors that have no
+memory, have shrunk or are not plain tensors; copies of states; autograd's knowledge of a step."""
+import numpy as np
+import pytest
+
+import convolution_backward_b200 as cb
+import test_optimizer as to
+from oracle import optim
+
+torch = pytest.importorskip("torch")
+
+HYPER = to.HYPER
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-40, 1.2e-38, 1e-30, 1e-13])
+def test_small_eps(eps, bits):
+    """Down to fp32's smallest numbers: where the moments are zero the update is 0/eps = 0 (at eps 0: NaN); where v' is
+    zero and m' is not, m'/eps; elsewhere eps does not count.  Bounds: test_optimizer's weights."""
+    n = 1000
+    r = np.random.default_rng(4)
+    h = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=float(np.float32(eps)), wd=0.1)
+    w = r.normal(size=n).astype(np.float32)
+    g = (1e-2 * r.normal(size=n)).astype(np.float32)
+    g[::3] = 0
+    g[1::3][:100] = 1e-30 * r.normal(size=100)          # whose square is zero
+    g[256:512] = 0                                      # a block of nothing
+    params = [torch.from_numpy(w).cuda()]
+    state = cb.adamw_state(params, bits=bits)
+    cb.adamw_step(state, [torch.from_numpy(g).cuda()], 1, h["lr"], (h["beta1"], h["beta2"]), eps, h["wd"])
+    zero = np.zeros(n, dtype=np.float32)
+    with np.errstate(all="ignore"):
+        m, v = optim.moments(zero, zero, g, 1.0, h["beta1"], h["beta2"])
+        ref, up = optim.weights(w.astype(np.float64), m, v, 1, **h)
+    got = to._np(state.params[0]).astype(np.float64)
+    nan = np.isnan(ref)
+    assert nan.any() == (eps == 0) and (np.isnan(got) == nan).all()
+    far = ~nan & (np.abs(ref) > 3.4e38)                 # m'/eps past fp32's range
+    assert (np.isinf(got[far]) & (np.sign(got[far]) == np.sign(ref[far]))).all()
+    near = ~nan & ~far
+    bound = to.E32 * np.abs(ref) + 3 * to.E32 * np.abs(w) + 2.0 ** -20 * np.abs(up)
+    assert (np.abs(got - ref)[near] <= bound[near]).all()
+    cb.check_status()
