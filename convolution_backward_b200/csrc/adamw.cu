@@ -312,17 +312,22 @@ __device__ __forceinline__ void step2(const Packed& P, float2 g, float2& m, floa
     m = add2(P.mul(m, pair(h.b1)), P.mul(g, pair(h.c1)));
     v = add2(P.mul(v, pair(h.b2)), P.mul(P.mul(g, pair(h.c2)), g));
     const float2 u = P.mul(v, pair(s.ibc2));
-    float2 inv;
-    // below 2^-126 the root may be 0 beside an eps from 1e-12 on; den is 0 or an ordinary number
+    float2 inv, top = P.mul(m, pair(s.ibc1));
+    // below 2^-126 the root may be 0 beside an eps from 1e-12 on
     root = make_float2(root_of(u.x), root_of(u.y));
+    float2 den = add2(root, pair(h.eps));
     if (h.eps < 1e-12f) {
         asm("sqrt.approx.f32 %0, %1;" : "=f"(root.x) : "f"(u.x));
         asm("sqrt.approx.f32 %0, %1;" : "=f"(root.y) : "f"(u.y));
+        den = add2(root, pair(h.eps));
+        // a subnormal den has no reciprocal: both ends of the fraction are raised by 2^64
+        const float2 up = make_float2(den.x < 0x1p-64f ? 0x1p64f : 1.f, den.y < 0x1p-64f ? 0x1p64f : 1.f);
+        den = P.mul(den, up);
+        top = P.mul(top, up);
     }
-    const float2 den = add2(root, pair(h.eps));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv.x) : "f"(den.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv.y) : "f"(den.y));
-    w = ffma2(pair(s.nlr), P.mul(P.mul(m, pair(s.ibc1)), inv), P.mul(w, pair(s.decay)));
+    w = ffma2(pair(s.nlr), P.mul(top, inv), P.mul(w, pair(s.decay)));
 }
 
 // The larger magnitude; NaN where one is NaN.
