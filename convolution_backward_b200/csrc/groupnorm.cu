@@ -348,8 +348,9 @@ __global__ void __launch_bounds__(kGnBlock) gn_join_kernel(const GnFwd a)
             mean = m0 + s / m;
     }
     if (lane == 0 && store_ok(a.mean, static_cast<long long>(p.N) * p.G * 4, a.mean + ng, 4, a.status)) {
-        a.mean[ng] = mean;
-        a.rstd[ng] = 1.0f / sqrtf(sq / m + a.eps);
+        const float2 stats = gn_statistics(mean, sq, m, a.eps);
+        a.mean[ng] = stats.x;
+        a.rstd[ng] = stats.y;
     }
 }
 

@@ -224,6 +224,14 @@ __device__ __forceinline__ void group_totals(const float* in, int in_stride, int
     __syncthreads();
 }
 
+// (mean, rstd) of a group of m values, NaN where one of them, or a sum of them, is no finite number: with one infinity
+// the mean alone would be infinite.
+__device__ __forceinline__ float2 gn_statistics(float mean, float M2, float m, float eps)
+{
+    if (!isfinite(mean)) return splat(__int_as_float(0x7FC00000));
+    return make_float2(mean, 1.0f / sqrtf(M2 / m + eps));
+}
+
 // Whether the mean of `count` values lies far above their spread, eight standard deviations or more (M2: the squares
 // about it): a few roundings of such a mean are no longer small beside the spread.
 __device__ __forceinline__ bool gn_far(float mean, float M2, float count)

@@ -144,15 +144,15 @@ __device__ __forceinline__ bool slice_statistics(const GnCluster& a, const GnSha
                 sq += fmaf(e * count_of(p, q), e, all[(q * 2 + 1) * p.ng + j]);
             }
         }
-        const float rs = 1.0f / sqrtf(sq / m + a.eps);
-        sh.stat[j] = mu;
-        const bool again = MARK && gn_far(mu, sq, m);
-        sh.stat[p.ng + j] = again ? -rs : rs;
+        const float2 stats = gn_statistics(mu, sq, m, a.eps);
+        sh.stat[j] = stats.x;
+        const bool again = MARK && gn_far(stats.x, sq, m);
+        sh.stat[p.ng + j] = again ? -stats.y : stats.y;
         far = far || again;
         if (rank == 0) {
             const long long at = stat_at + j, all_of = static_cast<long long>(p.N) * p.G * 4;
-            if (a.mean && store_ok(a.mean, all_of, a.mean + at, 4, a.status)) a.mean[at] = mu;
-            if (a.rstd && store_ok(a.rstd, all_of, a.rstd + at, 4, a.status)) a.rstd[at] = rs;
+            if (a.mean && store_ok(a.mean, all_of, a.mean + at, 4, a.status)) a.mean[at] = stats.x;
+            if (a.rstd && store_ok(a.rstd, all_of, a.rstd + at, 4, a.status)) a.rstd[at] = stats.y;
         }
     }
     if (p.K > 1) cluster_arrive();   // this block has read the others' values

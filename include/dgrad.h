@@ -305,7 +305,8 @@ dgrad_status_t dgrad_gated_backward_workspace(int64_t M, int64_t C, int64_t F, s
  * mean, rstd (fp32, [N][G] each, either may be null) are what the backward pass needs.
  * Y may be X.  eps finite and >= 0 (at eps 0 a constant group gives NaN).  G divides C (else
  * DGRAD_ERR_INVALID).  A group that holds an infinity or NaN becomes NaN, and so do its mean and rstd;
- * one whose squares pass fp32's range has rstd 0.  C <= 65536, N*S and N*G <= 2^30 (else
+ * one whose squares pass fp32's range has rstd 0, and one whose sums do (m times its largest magnitude
+ * 3.4e38 or more) has that or becomes NaN.  C <= 65536, N*S and N*G <= 2^30 (else
  * DGRAD_ERR_UNSUPPORTED).  N or S of 0: nothing but mean and rstd is
  * written, and those are NaN (sums over no values).  workspace: at least
  * dgrad_groupnorm_forward_workspace bytes (0 for sizes that need none; it may be null then), 16-byte

@@ -97,3 +97,50 @@ def test_a_far_mean_changes_its_own_group_alone(shape, way):
     got = cb.groupnorm_backward(dy, z, mean2, rstd2, g, b, act="silu")
     tg._check_bwd(dy, z, g, b, mean2, rstd2, "silu", "f32", got, "backward")
     cb.check_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(333, 21, 7), (400, 64, 8), (4000, 24, 1), (20000, 16, 4), (7, 40, 5)], ids=IDS)
+def test_an_infinity_makes_its_groups_statistics_nan(shape, way):
+    """At the first position, a middle one (in another block) and the last."""
+    S, C, G = shape
+    D = C // G
+    x, g, b, _ = tg._inputs(3, S, C, "f32", seed=21)
+    y0, mean0, rstd0 = cb.groupnorm_forward(x, G, g, b, stats=True)
+    for bad in (float("inf"), float("-inf"), float("nan")):
+        for n, s in ((0, 0), (1, S // 2), (2, S - 1)):
+            z = x.clone()
+            z[n, s, C - 1] = bad
+            y, mean, rstd = cb.groupnorm_forward(z, G, g, b, stats=True)
+            hit = torch.zeros(3, G, dtype=torch.bool, device="cuda")
+            hit[n, G - 1] = True
+            assert torch.isnan(mean[hit]).all() and torch.isnan(rstd[hit]).all(), (bad, s)
+            assert torch.equal(mean[~hit], mean0[~hit]) and torch.equal(rstd[~hit], rstd0[~hit]), (bad, s)
+            assert torch.isnan(y[n, :, C - D:]).all()
+            y[n, :, C - D:] = y0[n, :, C - D:]
+            assert torch.equal(y, y0)
+    cb.check_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(333, 21, 7), (400, 64, 8), (4000, 24, 1), (7, 40, 5)], ids=IDS)
+def test_sums_up_to_the_range(shape, way):
+    """m max|x| just inside fp32's range: the means are numbers, rstd is 0 and beta is left.  Past it a group's
+    results are its own formula's or NaN, never another number."""
+    S, C, G = shape
+    D, m = C // G, S * (C // G)
+    r = np.random.default_rng(5)
+    _, g, b, _ = tg._inputs(1, 1, C, "f32", seed=3)
+    X = (r.uniform(0.2, 1.0, size=(2, S, C)) * (3.3e38 / m)).astype(np.float32)
+    x = torch.from_numpy(X).cuda()
+    y, mean, rstd = cb.groupnorm_forward(x, G, g, b, stats=True)
+    _, rm, _ = branch.groupnorm(X.astype(np.float64), G, np.ones(C), np.zeros(C), 0.0)
+    within(mean, rm, (S + 132) * E32 * rm, "mean")
+    assert not rstd.any() and torch.equal(y, b.expand_as(y))
+    y, mean, rstd = cb.groupnorm_forward(x * m, G, g, b, stats=True)
+    rm *= m
+    ok = torch.isnan(mean) | ((mean.double() - torch.from_numpy(rm).cuda()).abs() <= 1e-3 * torch.from_numpy(rm).cuda())
+    assert ok.all() and (torch.isnan(rstd) == torch.isnan(mean)).all() and not torch.nan_to_num(rstd).any()
+    nan = torch.isnan(mean).repeat_interleave(D, dim=1)[:, None, :].expand_as(y)
+    assert torch.isnan(y[nan]).all() and torch.equal(y[~nan], b.expand_as(y)[~nan])
+    cb.check_status()
