@@ -928,7 +928,7 @@ class AdamWState:
     uint8 codes of the parameters' shapes, and m_max, v_max fp32 with an element for every 256 of a tensor.
     master: fp32 copies of 16-bit parameters, which are then what is stepped.  No two tensors may
     share memory.  The tensors stay the caller's: save them as they are, load them with copy_; where the
-    storage of one has been replaced, adamw_step refuses the state.  A step writes them without autograd's
+    storage of one has been replaced, or its size or type changed, adamw_step refuses the state.  A step writes them without autograd's
     knowledge: no graph that still needs the old parameters may be alive."""
 
     def __init__(self, params, m, v, master=None, m_max=None, v_max=None):
@@ -977,7 +977,8 @@ class AdamWState:
         if status == 1:
             raise ValueError("parameters and states must not share memory")
         _check(status, "dgrad_adamw_check")
-        self._where = _Array(np.array([t.data_ptr() for t in everything], dtype=np.uint64))
+        self._was = [_Array(np.empty(len(everything), dtype=t)) for t in (np.uint64, np.int64, np.int64)]
+        _lists().describe(everything, *(w.at for w in self._was))
         self._n = _Array(np.ascontiguousarray(self._table["n"]))
         # the written ranges in order, for gradients and results to be held against
         lo = np.array([t.data_ptr() for t in everything if t.numel()], dtype=np.uint64)
@@ -989,6 +990,10 @@ class AdamWState:
 
     def _apart(self, at, nbytes):
         return _lists().apart(at, self._n.at, len(self.params), nbytes, self._lo.at, self._hi.at, len(self._lo.a))
+
+    def _unchanged(self):
+        if not _lists().same(self._all, *(w.at for w in self._was)):
+            raise ValueError("the storage, size or type of a parameter or state has changed since its AdamWState was made")
 
     def __len__(self):
         return len(self.params)
@@ -1058,8 +1063,7 @@ def adamw_step(state, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_deca
         raise TypeError(f"gradients must be {state.dtype} or float32")
     if gdev != dev.index:
         raise ValueError("all tensors of one call must be on the same CUDA device")
-    if not _lists().same(state._all, state._where.at):
-        raise ValueError("a parameter's or state's storage has changed since its AdamWState was made")
+    state._unchanged()
     if not state._apart(to.at, 4 if gcode == 0 else 2):
         raise ValueError("gradients must not share memory with parameters or states")
     state._table["grad"] = to.a
@@ -1118,8 +1122,7 @@ def adamw_moments(state, out=None, stream=None):
         given = out[0] + out[1]
         if any(t is None for t in given):
             raise TypeError("out must be tensors")
-    if not _lists().same(state._all, state._where.at):
-        raise ValueError("a parameter's or state's storage has changed since its AdamWState was made")
+    state._unchanged()
     to = [_Array(np.empty(len(state), dtype=np.uint64)) for _ in range(2)]
     for ts, at, what in zip(out, to, ("out: m", "out: v")):
         code, index = _lists().read(ts, state._list, what, at.at, 0)

@@ -26,6 +26,8 @@ PyObject* fail(PyObject* type, const char* what, const char* text)
     return nullptr;
 }
 
+int64_t type_of(const at::Tensor& t) { return t.is_contiguous() ? static_cast<int64_t>(t.scalar_type()) : -1; }
+
 // read(tensors, like, what, addresses, elements) -> (type, device): fills the arrays at the two
 // addresses (elements may be 0) from a list of contiguous CUDA tensors of one type (0 fp32, 1 bf16, 2 f16; -1: no
 // tensor) and device.  like: None, or a list of tensors of the same length whose shapes they must have;
@@ -78,18 +80,46 @@ PyObject* read(PyObject*, PyObject* const* args, Py_ssize_t count)
     return Py_BuildValue("(ii)", type, device);
 }
 
-// same(tensors, addresses) -> whether every tensor of the list still lies where the array says.
-PyObject* same(PyObject*, PyObject* const* args, Py_ssize_t count)
+// describe(tensors, addresses, elements, types): fills the three arrays; a type is torch's number of it, -1 where the
+// tensor is not contiguous.
+PyObject* describe(PyObject*, PyObject* const* args, Py_ssize_t count)
 {
-    if (count != 2 || !PyList_Check(args[0])) {
-        PyErr_SetString(PyExc_TypeError, "same(tensors: list, addresses)");
+    if (count != 4 || !PyList_Check(args[0])) {
+        PyErr_SetString(PyExc_TypeError, "describe(tensors: list, addresses, elements, types)");
         return nullptr;
     }
-    const uint64_t* const at = address<const uint64_t>(args[1]);
+    uint64_t* const at = address<uint64_t>(args[1]);
+    int64_t* const elements = address<int64_t>(args[2]);
+    int64_t* const types = address<int64_t>(args[3]);
     if (PyErr_Occurred()) return nullptr;
     for (Py_ssize_t i = 0; i < PyList_GET_SIZE(args[0]); ++i) {
         PyObject* const o = PyList_GET_ITEM(args[0], i);
-        if (!THPVariable_Check(o) || reinterpret_cast<uint64_t>(THPVariable_Unpack(o).const_data_ptr()) != at[i]) Py_RETURN_FALSE;
+        if (!THPVariable_Check(o)) return fail(PyExc_TypeError, "entries", "%s must be tensors");
+        const at::Tensor& t = THPVariable_Unpack(o);
+        at[i] = reinterpret_cast<uint64_t>(t.const_data_ptr());
+        elements[i] = t.numel();
+        types[i] = type_of(t);
+    }
+    Py_RETURN_NONE;
+}
+
+// same(tensors, addresses, elements, types) -> whether every tensor of the list still is what `describe` left in the
+// arrays.  An address alone is not enough: a view of a few of its elements has it too.
+PyObject* same(PyObject*, PyObject* const* args, Py_ssize_t count)
+{
+    if (count != 4 || !PyList_Check(args[0])) {
+        PyErr_SetString(PyExc_TypeError, "same(tensors: list, addresses, elements, types)");
+        return nullptr;
+    }
+    const uint64_t* const at = address<const uint64_t>(args[1]);
+    const int64_t* const elements = address<const int64_t>(args[2]);
+    const int64_t* const types = address<const int64_t>(args[3]);
+    if (PyErr_Occurred()) return nullptr;
+    for (Py_ssize_t i = 0; i < PyList_GET_SIZE(args[0]); ++i) {
+        PyObject* const o = PyList_GET_ITEM(args[0], i);
+        if (!THPVariable_Check(o)) Py_RETURN_FALSE;
+        const at::Tensor& t = THPVariable_Unpack(o);
+        if (reinterpret_cast<uint64_t>(t.const_data_ptr()) != at[i] || t.numel() != elements[i] || type_of(t) != types[i]) Py_RETURN_FALSE;
     }
     Py_RETURN_TRUE;
 }
@@ -145,6 +175,7 @@ PyObject* disjoint(PyObject*, PyObject* const* args, Py_ssize_t count)
 
 PyMethodDef methods[] = {
     {"read", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(read)), METH_FASTCALL, nullptr},
+    {"describe", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(describe)), METH_FASTCALL, nullptr},
     {"same", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(same)), METH_FASTCALL, nullptr},
     {"disjoint", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(disjoint)), METH_FASTCALL, nullptr},
     {"apart", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(apart)), METH_FASTCALL, nullptr},

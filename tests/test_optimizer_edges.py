@@ -12,6 +12,62 @@ torch = pytest.importorskip("torch")
 HYPER = to.HYPER
 
 
+def _described(ts):
+    was = [cb._Array(np.zeros(len(ts), dtype=t)) for t in (np.uint64, np.int64, np.int64)]
+    cb._lists().describe(ts, *(w.at for w in was))
+    return [w.at for w in was], was
+
+
+@pytest.mark.parametrize("change", ["narrow", "resize", "type", "order", "replace", "none", "reshape"])
+def test_changed_tensors_are_seen(change):
+    """At the same address, too (on the CPU: nothing here touches the elements)."""
+    a, b = torch.zeros(7), torch.zeros(4, 4)
+    at, was = _described([a, b])
+    assert was[0].a.tolist() == [a.data_ptr(), b.data_ptr()] and was[1].a.tolist() == [7, 16]
+    assert cb._lists().same([a, b], *at)
+    where = b.data_ptr()
+    if change == "narrow":
+        b.data = b.data[:2]
+    elif change == "resize":
+        b.resize_(3, 3)
+    elif change == "type":
+        b.data = b.data.view(torch.int32)
+    elif change == "order":
+        b.data = b.data.t()
+    elif change == "replace":
+        b.data = b.data.clone()
+    elif change == "reshape":
+        b.data = b.data.view(2, 8)
+    assert (b.data_ptr() == where) == (change != "replace")
+    assert cb._lists().same([a, b], *at) == (change in ("none", "reshape"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_shrunk_tensors_are_refused(bits):
+    """A parameter or state that is fewer elements at the same address: nothing runs on the old count."""
+    for which in ("params", "m", "v"):
+        p = torch.ones(600, device="cuda")
+        state = cb.adamw_state([p, torch.ones(5, device="cuda")], bits=bits)
+        keep = [t.clone() for t in state._all]
+        whole = [t.data for t in state._all]
+        t = getattr(state, which)[0]
+        t.data = t.data[:4]
+        g = torch.ones(4 if which == "params" else 600, device="cuda")
+        with pytest.raises(ValueError, match="storage"):
+            cb.adamw_step(state, [g, None], 1, 1e-3)
+        with pytest.raises(ValueError, match="storage"):
+            cb.adamw_step(state, [None, torch.ones(5, device="cuda")], 1, 1e-3)
+        if bits == 8:
+            out = [[torch.zeros(n, device="cuda") for n in (g.numel(), 5)] for _ in range(2)]
+            with pytest.raises(ValueError, match="storage"):
+                cb.adamw_moments(state, out=out)
+        assert all(torch.equal(a, b) for a, b in zip(keep, whole))
+        t.data = next(w for w in whole if w.data_ptr() == t.data_ptr())
+        cb.adamw_step(state, [torch.ones(600, device="cuda"), None], 1, 1e-3)      # whole again
+    cb.check_status()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-40, 1.2e-38, 1e-30, 1e-13])
