@@ -4,6 +4,7 @@
 // and takes 0.02 here.  It only looks: nothing is allocated, launched or kept.
 #include <Python.h>
 
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -18,6 +19,22 @@ template <typename T>
 T* address(PyObject* v)
 {
     return reinterpret_cast<T*>(PyLong_AsVoidPtr(v));
+}
+
+// F with torch's exceptions (tensors under a function transform and symbolic sizes raise them where a size or an address
+// is asked for) as Python's: one that left the module would end the process.
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject* self, PyObject* const* args, Py_ssize_t count)
+{
+    HANDLE_TH_ERRORS
+    return F(self, args, count);
+    END_HANDLE_TH_ERRORS
+}
+
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyCFunction entry()
+{
+    return reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(guarded<F>));
 }
 
 PyObject* fail(PyObject* type, const char* what, const char* text)
@@ -174,11 +191,11 @@ PyObject* disjoint(PyObject*, PyObject* const* args, Py_ssize_t count)
 }
 
 PyMethodDef methods[] = {
-    {"read", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(read)), METH_FASTCALL, nullptr},
-    {"describe", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(describe)), METH_FASTCALL, nullptr},
-    {"same", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(same)), METH_FASTCALL, nullptr},
-    {"disjoint", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(disjoint)), METH_FASTCALL, nullptr},
-    {"apart", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(apart)), METH_FASTCALL, nullptr},
+    {"read", entry<read>(), METH_FASTCALL, nullptr},
+    {"describe", entry<describe>(), METH_FASTCALL, nullptr},
+    {"same", entry<same>(), METH_FASTCALL, nullptr},
+    {"disjoint", entry<disjoint>(), METH_FASTCALL, nullptr},
+    {"apart", entry<apart>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -1,5 +1,8 @@
 """The AdamW step, its states and the gradients' norm at their edges: subnormal eps; tensors that have no
 memory, have shrunk or are not plain tensors; copies of states; autograd's knowledge of a step."""
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -40,6 +43,55 @@ def test_changed_tensors_are_seen(change):
         b.data = b.data.view(2, 8)
     assert (b.data_ptr() == where) == (change != "replace")
     assert cb._lists().same([a, b], *at) == (change in ("none", "reshape"))
+
+
+# Calls with something that is no plain tensor, in a process of their own: an exception that leaves native code ends it.
+WRAPPED = """
+import sys
+import numpy as np
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+from torch.fx.experimental.symbolic_shapes import ShapeEnv
+import convolution_backward_b200 as cb
+
+L = cb._lists()
+arrays = [cb._Array(np.zeros(4, dtype=t)) for t in (np.uint64, np.int64, np.int64)]
+at = [a.at for a in arrays]
+calls = {
+    "norm": lambda x: cb.grad_norm([x]),
+    "read": lambda x: L.read([x], None, "gradients", at[0], at[1]),
+    "like": lambda x: L.read([x], [x], "gradients", at[0], 0),
+    "describe": lambda x: L.describe([x], *at),
+    "same": lambda x: L.same([x], *at),
+}
+env = ShapeEnv()
+
+
+def run(f):
+    if sys.argv[1] == "grad":
+        torch.func.grad(lambda x: (f(x), x.sum())[1])(torch.empty(2, 3, device="cuda"))
+    elif sys.argv[1] == "vmap":
+        torch.vmap(lambda x: (f(x), x)[1])(torch.empty(2, 3, device="cuda"))
+    else:
+        f(torch.empty(env.create_unbacked_symint(), 3, device="cuda"))
+
+
+with FakeTensorMode(shape_env=env):
+    for name, f in calls.items():
+        print("trying", name, file=sys.stderr, flush=True)
+        try:
+            run(f)
+        except (RuntimeError, ValueError):
+            print(name)
+"""
+
+
+@pytest.mark.parametrize("wrap", ["grad", "vmap", "symbolic"])
+def test_wrapped_tensors_raise(wrap):
+    r = subprocess.run([sys.executable, "-W", "ignore", "-c", WRAPPED, wrap], capture_output=True, text=True,
+                       cwd=to.os.path.dirname(to.os.path.dirname(to.os.path.abspath(__file__))), timeout=300)
+    assert r.returncode == 0, r.stderr[:2000]
+    assert r.stdout.split() == ["norm", "read", "like", "describe", "same"]
 
 
 @pytest.mark.gpu
@@ -96,5 +148,5 @@ def test_small_eps(eps, bits):
     assert (np.isinf(got[far]) & (np.sign(got[far]) == np.sign(ref[far]))).all()
     near = ~nan & ~far
     bound = to.E32 * np.abs(ref) + 3 * to.E32 * np.abs(w) + 2.0 ** -20 * np.abs(up)
-    assert (np.abs(got - ref)[near] <= bound[near]).all()
+    assert (np.abs(got[near] - ref[near]) <= bound[near]).all()
     cb.check_status()
