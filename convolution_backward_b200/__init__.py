@@ -232,6 +232,15 @@ def _need_cuda(*ts):
             raise ValueError("tensors must be contiguous (NHWC)")
 
 
+def _at(t):
+    """A tensor's address.  One whose storage was released is refused: its address is that of its offset, 0 for most,
+    which stands for an optional tensor that is not there."""
+    p = t.data_ptr()
+    if p < 1 << 40 and t.numel() and t.untyped_storage().data_ptr() == 0:
+        raise ValueError("a tensor's storage does not hold its elements")
+    return p
+
+
 def out_dims(H, W, KH, KW, stride=1, pad_h=0, pad_w=-1):
     """(Ho, Wo) of the forward convolution (host-only C call)."""
     prob = Problem(1, H, W, 1, 1, KH, KW, stride, pad_h, pad_w)
@@ -258,7 +267,7 @@ def pointwise(dY, W, out=None, stream=None):
             raise ValueError("out has the wrong shape or dtype")
     prob = Problem(N, H, Wd, C, K, 1, 1, 1, 0, 0)
     _call(_device_of(dY, W, out), "dgrad_pointwise", lib().dgrad_pointwise, ctypes.byref(prob), _dtype_code(dY),
-          dY.data_ptr(), W.data_ptr(), out.data_ptr(), stream=stream)
+          _at(dY), _at(W), _at(out), stream=stream)
     return out
 
 
@@ -291,8 +300,8 @@ def pointwise_splitk(dY, W, splits=0, workspace=None, out=None, stream=None):
         out = torch.empty((N, H, Wd, C), dtype=dY.dtype, device=dY.device)
     prob = Problem(N, H, Wd, C, K, 1, 1, 1, 0, 0)
     _call(_device_of(dY, W, out, workspace), "dgrad_pointwise_splitk", lib().dgrad_pointwise_splitk,
-          ctypes.byref(prob), _dtype_code(dY), int(used), dY.data_ptr(), W.data_ptr(), out.data_ptr(),
-          workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)
+          ctypes.byref(prob), _dtype_code(dY), int(used), _at(dY), _at(W), _at(out),
+          _at(workspace), workspace.numel() * workspace.element_size(), stream=stream)
     return out
 
 
@@ -317,7 +326,7 @@ def pointwise_splitk_noalloc(dY, W, out, splits=0, stream=None):
         raise ValueError("out must be (N,H,W,C) with dY's dtype")
     prob = Problem(N, H, Wd, C, K, 1, 1, 1, 0, 0)
     _call(_device_of(dY, W, out), "dgrad_pointwise_splitk_noalloc", lib().dgrad_pointwise_splitk_noalloc,
-          ctypes.byref(prob), _dtype_code(dY), int(splits), dY.data_ptr(), W.data_ptr(), out.data_ptr(),
+          ctypes.byref(prob), _dtype_code(dY), int(splits), _at(dY), _at(W), _at(out),
           stream=stream)
     return out
 
@@ -353,7 +362,7 @@ def depthwise(dY, W, *, H, W_out=None, stride=1, pad_h=0, pad_w=-1, mode="auto",
         if tuple(out.shape) != (N, H, W_out, C) or out.dtype != dY.dtype:
             raise ValueError("out has the wrong shape or dtype")
     _call(_device_of(dY, W, out), "dgrad_depthwise", lib().dgrad_depthwise, ctypes.byref(prob), _dtype_code(dY),
-          DW_MODES[mode], dY.data_ptr(), W.data_ptr(), out.data_ptr(), stream=stream)
+          DW_MODES[mode], _at(dY), _at(W), _at(out), stream=stream)
     return out
 
 
@@ -383,7 +392,7 @@ def dense(dY, W, *, H, W_out=None, stride=1, pad_h=0, pad_w=-1, out=None, stream
             raise ValueError("out has the wrong shape or dtype")
     prob = Problem(N, H, W_out, C, K, KH, KW, stride, pad_h, pad_w)
     _call(_device_of(dY, W, out), "dgrad_dense", lib().dgrad_dense, ctypes.byref(prob), _dtype_code(dY),
-          dY.data_ptr(), W.data_ptr(), out.data_ptr(), stream=stream)
+          _at(dY), _at(W), _at(out), stream=stream)
     return out
 
 
@@ -414,7 +423,7 @@ def grouped(dY, W, groups, *, H, W_out=None, stride=1, pad_h=0, pad_w=-1, out=No
             raise ValueError("out has the wrong shape or dtype")
     prob = Problem(N, H, W_out, C, K, KH, KW, stride, pad_h, pad_w)
     _call(_device_of(dY, W, out), "dgrad_grouped", lib().dgrad_grouped, ctypes.byref(prob), int(groups),
-          _dtype_code(dY), dY.data_ptr(), W.data_ptr(), out.data_ptr(), stream=stream)
+          _dtype_code(dY), _at(dY), _at(W), _at(out), stream=stream)
     return out
 
 
@@ -458,7 +467,7 @@ def depthwise_tc(dY, W, *, H, W_out=None, pad_h=0, pad_w=-1, workspace=None, out
         if tuple(out.shape) != (N, H, W_out, C) or out.dtype != dY.dtype:
             raise ValueError("out has the wrong shape or dtype")
     _call(_device_of(dY, W, out, workspace), "dgrad_depthwise_tc", lib().dgrad_depthwise_tc, ctypes.byref(prob),
-          _dtype_code(dY), dY.data_ptr(), W.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+          _dtype_code(dY), _at(dY), _at(W), _at(out), _at(workspace),
           workspace.numel() * workspace.element_size(), stream=stream)
     return out
 
@@ -541,7 +550,7 @@ def _out(al, out, like, shape):
 
 
 def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return None if t is None else _at(t)
 
 
 def layernorm_forward(X, gamma=None, beta=None, eps=1e-5, stats=False, out=None, stream=None):
@@ -568,8 +577,8 @@ def layernorm_forward(X, gamma=None, beta=None, eps=1e-5, stats=False, out=None,
         rstd = _empty(al, mean, mean.shape, torch.float32)
     if al is not None:
         al.uses(X, *given)
-    _call(dev, "dgrad_layernorm_forward", lib().dgrad_layernorm_forward, M, C, code, float(eps), X.data_ptr(),
-          _ptr(gamma), _ptr(beta), out.data_ptr(), _ptr(mean), _ptr(rstd), stream=stream)
+    _call(dev, "dgrad_layernorm_forward", lib().dgrad_layernorm_forward, M, C, code, float(eps), _at(X),
+          _ptr(gamma), _ptr(beta), _at(out), _ptr(mean), _ptr(rstd), stream=stream)
     return (out, mean, rstd) if stats else out
 
 
@@ -618,8 +627,8 @@ def layernorm_backward(dY, X, mean, rstd, gamma=None, param_grads=True, workspac
             ws_bytes = workspace.numel() * workspace.element_size()
     if al is not None:
         al.uses(dY, X, mean, rstd, *given)
-    _call(dev, "dgrad_layernorm_backward", lib().dgrad_layernorm_backward, M, C, code, dY.data_ptr(), X.data_ptr(),
-          _ptr(gamma), mean.data_ptr(), rstd.data_ptr(), out.data_ptr(), _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
+    _call(dev, "dgrad_layernorm_backward", lib().dgrad_layernorm_backward, M, C, code, _at(dY), _at(X),
+          _ptr(gamma), _at(mean), _at(rstd), _at(out), _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
           ws_bytes, stream=stream)
     return out, dgamma, dbeta
 
@@ -699,7 +708,7 @@ def groupnorm_forward(X, groups, gamma=None, beta=None, eps=1e-5, act=None, stat
     if al is not None:
         al.uses(X, *given)
     _call(dev, "dgrad_groupnorm_forward", lib().dgrad_groupnorm_forward, N, S, C, G, code, float(eps), acode,
-          X.data_ptr(), _ptr(gamma), _ptr(beta), out.data_ptr(), _ptr(mean), _ptr(rstd), _ptr(workspace), ws_bytes,
+          _at(X), _ptr(gamma), _ptr(beta), _at(out), _ptr(mean), _ptr(rstd), _ptr(workspace), ws_bytes,
           stream=stream)
     return (out, mean, rstd) if stats else out
 
@@ -737,8 +746,8 @@ def groupnorm_backward(dY, X, mean, rstd, gamma=None, beta=None, act=None, param
     workspace, ws_bytes = _workspace(al, workspace, X, _gn_workspace(True, N, S, C, G, code))
     if al is not None:
         al.uses(dY, X, mean, rstd, *given)
-    _call(dev, "dgrad_groupnorm_backward", lib().dgrad_groupnorm_backward, N, S, C, G, code, acode, dY.data_ptr(),
-          X.data_ptr(), _ptr(gamma), _ptr(beta), mean.data_ptr(), rstd.data_ptr(), out.data_ptr(), _ptr(dgamma),
+    _call(dev, "dgrad_groupnorm_backward", lib().dgrad_groupnorm_backward, N, S, C, G, code, acode, _at(dY),
+          _at(X), _ptr(gamma), _ptr(beta), _at(mean), _at(rstd), _at(out), _ptr(dgamma),
           _ptr(dbeta), _ptr(workspace), ws_bytes, stream=stream)
     return out, dgamma, dbeta
 
@@ -776,8 +785,8 @@ def gated_forward(X, W, act="silu", preact=False, out=None, stream=None):
     Z = _empty(al, X, (*X.shape[:-1], 2 * F), X.dtype) if preact else None
     if al is not None:
         al.uses(X, W, *given)
-    _call(dev, "dgrad_gated_forward", lib().dgrad_gated_forward, M, C, F, code, acode, X.data_ptr(), W.data_ptr(),
-          out.data_ptr(), _ptr(Z), stream=stream)
+    _call(dev, "dgrad_gated_forward", lib().dgrad_gated_forward, M, C, F, code, acode, _at(X), _at(W),
+          _at(out), _ptr(Z), stream=stream)
     return (out, Z) if preact else out
 
 
@@ -822,8 +831,8 @@ def gated_backward(dH, X, Z, W, act="silu", input_grad=True, weight_grad=True, w
         workspace = _empty(al, X, (max(_gated_workspace(M, C, F), 16),), torch.uint8)
     if al is not None:
         al.uses(dH, X, Z, W, *given)
-    _call(dev, "dgrad_gated_backward", lib().dgrad_gated_backward, M, C, F, code, acode, dH.data_ptr(), X.data_ptr(),
-          Z.data_ptr(), W.data_ptr(), _ptr(dX), _ptr(dW), workspace.data_ptr(),
+    _call(dev, "dgrad_gated_backward", lib().dgrad_gated_backward, M, C, F, code, acode, _at(dH), _at(X),
+          _at(Z), _at(W), _ptr(dX), _ptr(dW), _at(workspace),
           workspace.numel() * workspace.element_size(), stream=stream)
     return dX, dW
 
@@ -854,7 +863,7 @@ def dropout_forward(X, p, seed, offset=0, residual=None, out=None, stream=None):
     if al is not None:
         al.uses(X, *given)
     _call(dev, "dgrad_dropout_forward", lib().dgrad_dropout_forward, X.numel(), code, float(p),
-          _counter(seed, "seed"), _counter(offset, "offset"), X.data_ptr(), _ptr(residual), out.data_ptr(),
+          _counter(seed, "seed"), _counter(offset, "offset"), _at(X), _ptr(residual), _at(out),
           stream=stream)
     return out
 
@@ -872,7 +881,7 @@ def dropout_backward(dY, p, seed, offset=0, out=None, stream=None):
     if al is not None:
         al.uses(dY, *given)
     _call(dev, "dgrad_dropout_backward", lib().dgrad_dropout_backward, dY.numel(), code, float(p),
-          _counter(seed, "seed"), _counter(offset, "offset"), dY.data_ptr(), out.data_ptr(), stream=stream)
+          _counter(seed, "seed"), _counter(offset, "offset"), _at(dY), _at(out), stream=stream)
     return out
 
 
@@ -966,6 +975,8 @@ class AdamWState:
         _need_cuda(*everything)
         _device_of(*everything)
         self._list, self._all = list(self.params), everything
+        self._was = [_Array(np.empty(len(everything), dtype=t)) for t in (np.uint64, np.int64, np.int64)]
+        _lists().describe(everything, *(w.at for w in self._was))
         self._table = np.zeros(n, dtype=_TABLE)
         for name, ts in (("param", self.params), ("m", self.m), ("v", self.v), ("master", self.master),
                          ("m_max", self.m_max), ("v_max", self.v_max)):
@@ -977,8 +988,6 @@ class AdamWState:
         if status == 1:
             raise ValueError("parameters and states must not share memory")
         _check(status, "dgrad_adamw_check")
-        self._was = [_Array(np.empty(len(everything), dtype=t)) for t in (np.uint64, np.int64, np.int64)]
-        _lists().describe(everything, *(w.at for w in self._was))
         self._n = _Array(np.ascontiguousarray(self._table["n"]))
         # the written ranges in order, for gradients and results to be held against
         lo = np.array([t.data_ptr() for t in everything if t.numel()], dtype=np.uint64)
@@ -1028,7 +1037,7 @@ def _scalar(t, dtype, dev, what):
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     _device_of(t, _On(dev))
-    return t.data_ptr()
+    return _at(t)
 
 
 class _On:
@@ -1083,7 +1092,7 @@ def adamw_step(state, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_deca
         h.grad_scale = _scalar(grad_scale, torch.float32, dev, "grad_scale")
         given.append(grad_scale)
     if given:
-        scalars = array.array("q", [t.data_ptr() for t in given] + [1] * len(given))
+        scalars = array.array("q", [_at(t) for t in given] + [1] * len(given))
         where = scalars.buffer_info()[0]
         if not _lists().apart(where, where + 8 * len(given), len(given), 8, state._lo.at, state._hi.at, len(state._lo.a)):
             raise ValueError("lr, step and grad_scale must not share memory with parameters or states")
@@ -1174,14 +1183,14 @@ def grad_norm(grads, max_norm=None, workspace=None, stream=None):
     ws_bytes = _norm_workspace(len(grads))
     if workspace is None:       # behind the two results
         out = _empty(al, first, (4 + ws_bytes // 4,), torch.float32)
-        ws_at = out.data_ptr() + 16
+        ws_at = _at(out) + 16
     else:
         out = _empty(al, first, (2,), torch.float32)
-        ws_at, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws_at, ws_bytes = _at(workspace), workspace.numel() * workspace.element_size()
     if al is not None:
         al.uses(*grads, *given)
     _call(dev, "dgrad_grad_norm", lib().dgrad_grad_norm, len(grads), at, elements, code, limit,
-          out.data_ptr(), ws_at, ws_bytes, stream=stream)
+          _at(out), ws_at, ws_bytes, stream=stream)
     return out[0] if max_norm is None else (out[0], out[1])
 
 
@@ -1204,5 +1213,5 @@ def selftest_timeout(limit_cycles: int = 20_000_000, stream=None) -> None:
 def fma_probe(blocks: int, iters: int, packed: bool, sink, stream=None) -> int:
     """Launch the fp32 FMA-rate probe; returns the FLOP count it performs."""
     _call(_device_of(sink), "dgrad_fma_probe", lib().dgrad_fma_probe, int(blocks), int(iters), 1 if packed else 0,
-          sink.data_ptr(), stream=stream)
+          _at(sink), stream=stream)
     return int(blocks) * 256 * int(iters) * 16 * 2

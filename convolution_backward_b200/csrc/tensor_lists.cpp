@@ -43,6 +43,15 @@ PyObject* fail(PyObject* type, const char* what, const char* text)
     return nullptr;
 }
 
+// Whether a tensor's storage holds its elements: one that was released (as sharded training does), or a fake
+// tensor's, has none, and the address is that of the offset.
+bool held(const at::Tensor& t)
+{
+    if (t.numel() == 0) return true;
+    const c10::Storage& s = t.storage();
+    return s.data() != nullptr && s.nbytes() >= static_cast<size_t>(t.storage_offset() + t.numel()) * t.element_size();
+}
+
 int64_t type_of(const at::Tensor& t) { return t.is_contiguous() ? static_cast<int64_t>(t.scalar_type()) : -1; }
 
 // read(tensors, like, what, addresses, elements) -> (type, device): fills the arrays at the two
@@ -91,14 +100,15 @@ PyObject* read(PyObject*, PyObject* const* args, Py_ssize_t count)
             if (!THPVariable_Check(l) || !t.sizes().equals(THPVariable_Unpack(l).sizes()))
                 return fail(PyExc_ValueError, what, "%s must have their parameters' shapes");
         }
+        if (!held(t)) return fail(PyExc_ValueError, what, "%s: a tensor's storage does not hold its elements");
         at[i] = reinterpret_cast<uint64_t>(t.const_data_ptr());
         if (elements) elements[i] = t.numel();
     }
     return Py_BuildValue("(ii)", type, device);
 }
 
-// describe(tensors, addresses, elements, types): fills the three arrays; a type is torch's number of it, -1 where the
-// tensor is not contiguous.
+// describe(tensors, addresses, elements, types): fills the three arrays from tensors whose storages hold them; a type is
+// torch's number of it, -1 where the tensor is not contiguous.
 PyObject* describe(PyObject*, PyObject* const* args, Py_ssize_t count)
 {
     if (count != 4 || !PyList_Check(args[0])) {
@@ -113,6 +123,7 @@ PyObject* describe(PyObject*, PyObject* const* args, Py_ssize_t count)
         PyObject* const o = PyList_GET_ITEM(args[0], i);
         if (!THPVariable_Check(o)) return fail(PyExc_TypeError, "entries", "%s must be tensors");
         const at::Tensor& t = THPVariable_Unpack(o);
+        if (!held(t)) return fail(PyExc_ValueError, "parameters and states", "%s: a tensor's storage does not hold its elements");
         at[i] = reinterpret_cast<uint64_t>(t.const_data_ptr());
         elements[i] = t.numel();
         types[i] = type_of(t);
@@ -121,7 +132,7 @@ PyObject* describe(PyObject*, PyObject* const* args, Py_ssize_t count)
 }
 
 // same(tensors, addresses, elements, types) -> whether every tensor of the list still is what `describe` left in the
-// arrays.  An address alone is not enough: a view of a few of its elements has it too.
+// arrays.  An address alone is not enough: a view of a few of its elements has it too.  (A storage that is resized moves.)
 PyObject* same(PyObject*, PyObject* const* args, Py_ssize_t count)
 {
     if (count != 4 || !PyList_Check(args[0])) {

@@ -94,6 +94,80 @@ def test_wrapped_tensors_raise(wrap):
     assert r.stdout.split() == ["norm", "read", "like", "describe", "same"]
 
 
+def test_tensors_without_memory_are_refused_on_the_host():
+    """A fake tensor's address is its offset, as a released one's: 0 stands for no tensor in every table and argument."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        x, i = torch.empty(8, device="cuda"), torch.empty(1, dtype=torch.int64, device="cuda")
+        at = [cb._Array(np.zeros(4, dtype=np.uint64)) for _ in range(3)]
+        for t in (x, x[3:]):
+            for like in (None, [t]):
+                with pytest.raises(ValueError, match="storage"):
+                    cb._lists().read([t], like, "gradients", at[0].at, at[1].at)
+            with pytest.raises(ValueError, match="storage"):
+                cb._lists().describe([t], *(a.at for a in at))
+            with pytest.raises(ValueError, match="storage"):
+                cb._ptr(t)
+        with pytest.raises(ValueError, match="storage"):
+            cb._scalar(x[:1], torch.float32, x.device, "lr")
+        with pytest.raises(ValueError, match="storage"):
+            cb._scalar(i, torch.int64, x.device, "step")
+        with pytest.raises(ValueError, match="storage"):
+            cb.adamw_state([x])
+        with pytest.raises(ValueError, match="storage"):
+            cb.grad_norm([x])
+        assert cb._lists().read([x[:0]], None, "gradients", at[0].at, at[1].at) == (0, 0)
+        assert cb._ptr(x[:0]) == 0 and cb._ptr(None) is None
+    y = torch.zeros(10)
+    assert cb._ptr(y[3:]) == y.data_ptr() + 12
+    at, was = _described([y])
+    y.untyped_storage().resize_(20)
+    where = y.data_ptr()
+    assert not cb._lists().same([y], *at), where
+
+
+@pytest.mark.gpu
+def test_released_tensors_are_refused():
+    def gone(*shape, dtype=torch.float32, rows=None):
+        """A tensor, or its rows from `rows` on, whose storage was released after it was made."""
+        t = torch.ones(*shape, dtype=dtype, device="cuda")[rows:]
+        t.untyped_storage().resize_(0)
+        return t
+
+    p, q = torch.ones(600, device="cuda"), torch.ones(5, device="cuda")
+    for bits in (32, 8):
+        state = cb.adamw_state([p, q], bits=bits)
+        g, h = torch.ones(600, device="cuda"), torch.ones(5, device="cuda")
+        before = [t.clone() for t in state._all]
+        for bad in (gone(5), gone(9, rows=4)):
+            with pytest.raises(ValueError, match="storage"):
+                cb.adamw_step(state, [g, bad], 1, 1e-3)
+            with pytest.raises(ValueError, match="storage"):
+                cb.grad_norm([g, bad])
+        for kw in ({"grad_scale": gone(1)}, {"lr": gone(1)}, {"step": gone(1, dtype=torch.int64)}):
+            with pytest.raises(ValueError, match="storage"):
+                cb.adamw_step(state, [g, h], **{"step": 1, "lr": 1e-3, **kw})
+        assert all(torch.equal(a, b) for a, b in zip(before, state._all))
+        with pytest.raises(ValueError, match="storage"):
+            cb.adamw_state([gone(5)], bits=bits)
+        state.m[1].untyped_storage().resize_(0)
+        with pytest.raises(ValueError, match="storage"):
+            cb.adamw_step(state, [g, h], 1, 1e-3)
+    x, w = torch.ones(2, 3, 8, device="cuda"), torch.ones(8, device="cuda")
+    for args in ((x, 2, gone(8), w), (x, 2, w, gone(8)), (gone(2, 3, 8), 2), (gone(3, 3, 8, rows=1), 2)):
+        with pytest.raises(ValueError, match="storage"):
+            cb.groupnorm_forward(*args)
+    _, mean, rstd = cb.groupnorm_forward(x, 2, stats=True)
+    for args in ((x, x, mean, rstd, gone(8)), (gone(3, 3, 8, rows=1), x, mean, rstd), (x, x, gone(2, 2), rstd)):
+        with pytest.raises(ValueError, match="storage"):
+            cb.groupnorm_backward(*args)
+    with pytest.raises(ValueError, match="storage"):
+        cb.layernorm_forward(x, gone(8))
+    with pytest.raises(ValueError, match="storage"):
+        cb.dropout_forward(x, 0.5, 1, residual=gone(2, 3, 8))
+    cb.check_status()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("bits", [32, 8])
 def test_shrunk_tensors_are_refused(bits):
