@@ -936,7 +936,7 @@ class AdamWState:
     params: one dtype.  32-bit states: m, v fp32 of the parameters' shapes.  8-bit states: m int8 and v
     uint8 codes of the parameters' shapes, and m_max, v_max fp32 with an element for every 256 of a tensor.
     master: fp32 copies of 16-bit parameters, which are then what is stepped.  No two tensors may
-    share memory.  The tensors stay the caller's: save them as they are, load them with copy_; where the
+    share memory.  copy.copy shares the tensors, copy.deepcopy and pickle copy them.  The tensors stay the caller's: save them as they are, load them with copy_; where the
     storage of one has been replaced, or its size or type changed, adamw_step refuses the state.  A step writes them without autograd's
     knowledge: no graph that still needs the old parameters may be alive."""
 
@@ -999,6 +999,11 @@ class AdamWState:
 
     def _apart(self, at, nbytes):
         return _lists().apart(at, self._n.at, len(self.params), nbytes, self._lo.at, self._hi.at, len(self._lo.a))
+
+    def __reduce__(self):
+        """Copies and pickles are made anew from (copies of) the tensors: the addresses held here are this state's own."""
+        lists = (self.params, self.m, self.v, self.master, self.m_max, self.v_max)
+        return type(self), tuple(None if ts is None else list(ts) for ts in lists)
 
     def _unchanged(self):
         if not _lists().same(self._all, *(w.at for w in self._was)):

@@ -1,5 +1,7 @@
 """The AdamW step, its states and the gradients' norm at their edges: subnormal eps; tensors that have no
 memory, have shrunk or are not plain tensors; copies of states; autograd's knowledge of a step."""
+import copy
+import pickle
 import subprocess
 import sys
 
@@ -124,6 +126,39 @@ def test_tensors_without_memory_are_refused_on_the_host():
     y.untyped_storage().resize_(20)
     where = y.data_ptr()
     assert not cb._lists().same([y], *at), where
+
+
+def test_copies_of_states_are_made_from_their_tensors():
+    """A copied attribute would be the address of the first state's tables, which a step writes to."""
+    s = object.__new__(cb.AdamWState)
+    s.params, s.m, s.v, s.master, s.m_max, s.v_max = (torch.ones(3),), (torch.zeros(3),), (torch.zeros(3),), None, None, None
+    s._grads = cb._Array(np.zeros(1, dtype=np.uint64))
+    for again in (copy.copy, copy.deepcopy, lambda x: pickle.loads(pickle.dumps(x))):
+        with pytest.raises(ValueError, match="CUDA"):      # the constructor sees them
+            again(s)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_copied_states_step_on_their_own(bits):
+    _, grads, state = to._make([700, 3, 0, 256], "bf16", "bf16", True, bits, seed=31)
+    to._step(state, grads, 1)
+    deep, pickled = copy.deepcopy(state), pickle.loads(pickle.dumps(state))
+    shared = copy.copy(state)
+    assert [t.data_ptr() for t in shared._all] == [t.data_ptr() for t in state._all]
+    for other in (deep, pickled):
+        ours = {t.data_ptr() for t in state._all if t.numel()}
+        assert not ours & {t.data_ptr() for t in other._all}
+        assert all(torch.equal(a, b) for a, b in zip(state._all, other._all))
+    before = [t.clone() for t in state._all]
+    to._step(deep, grads, 2)
+    assert all(torch.equal(a, b) for a, b in zip(before, state._all))
+    to._step(shared, grads, 2)
+    assert all(torch.equal(a, b) for a, b in zip(deep._all, state._all))
+    del state, shared
+    to._step(pickled, grads, 2)
+    assert all(torch.equal(a, b) for a, b in zip(deep._all, pickled._all))
+    cb.check_status()
 
 
 @pytest.mark.gpu
