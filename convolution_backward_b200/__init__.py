@@ -937,8 +937,9 @@ class AdamWState:
     uint8 codes of the parameters' shapes, and m_max, v_max fp32 with an element for every 256 of a tensor.
     master: fp32 copies of 16-bit parameters, which are then what is stepped.  No two tensors may
     share memory.  copy.copy shares the tensors, copy.deepcopy and pickle copy them.  The tensors stay the caller's: save them as they are, load them with copy_; where the
-    storage of one has been replaced, or its size or type changed, adamw_step refuses the state.  A step writes them without autograd's
-    knowledge: no graph that still needs the old parameters may be alive."""
+    storage of one has been replaced, or its size or type changed, adamw_step refuses the state.  A step counts as an
+    in-place change of the parameters and master copies that it writes: a graph that has saved one of them raises
+    when it is run backward.  (The states are not counted, and the replay of a captured step counts nothing.)"""
 
     def __init__(self, params, m, v, master=None, m_max=None, v_max=None):
         import numpy as np
@@ -975,8 +976,10 @@ class AdamWState:
         _need_cuda(*everything)
         _device_of(*everything)
         self._list, self._all = list(self.params), everything
+        self._weights = self._list + list(self.master or ())
         self._was = [_Array(np.empty(len(everything), dtype=t)) for t in (np.uint64, np.int64, np.int64)]
-        _lists().describe(everything, *(w.at for w in self._was))
+        self._was_at = tuple(w.at for w in self._was)
+        _lists().describe(everything, *self._was_at)
         self._table = np.zeros(n, dtype=_TABLE)
         for name, ts in (("param", self.params), ("m", self.m), ("v", self.v), ("master", self.master),
                          ("m_max", self.m_max), ("v_max", self.v_max)):
@@ -1006,7 +1009,7 @@ class AdamWState:
         return type(self), tuple(None if ts is None else list(ts) for ts in lists)
 
     def _unchanged(self):
-        if not _lists().same(self._all, *(w.at for w in self._was)):
+        if not _lists().same(self._all, *self._was_at):
             raise ValueError("the storage, size or type of a parameter or state has changed since its AdamWState was made")
 
     def __len__(self):
@@ -1097,7 +1100,7 @@ def adamw_step(state, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_deca
         h.grad_scale = _scalar(grad_scale, torch.float32, dev, "grad_scale")
         given.append(grad_scale)
     if given:
-        scalars = array.array("q", [_at(t) for t in given] + [1] * len(given))
+        scalars = array.array("q", [a for a in (h.lr_device, h.step_device, h.grad_scale) if a] + [1] * len(given))
         where = scalars.buffer_info()[0]
         if not _lists().apart(where, where + 8 * len(given), len(given), 8, state._lo.at, state._hi.at, len(state._lo.a)):
             raise ValueError("lr, step and grad_scale must not share memory with parameters or states")
@@ -1112,6 +1115,7 @@ def adamw_step(state, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_deca
         al.uses(*grads, *given, *state._all)
     _call(dev, "dgrad_adamw_step", lib().dgrad_adamw_step, n, state._address, state._code, gcode, ctypes.byref(h),
           stream=stream)
+    _lists().written(state._weights, to.at, n)
 
 
 def adamw_moments(state, out=None, stream=None):
@@ -1150,6 +1154,8 @@ def adamw_moments(state, out=None, stream=None):
     if al is not None:
         al.uses(*given, *state._all)
     _call(dev, "dgrad_adamw_moments", lib().dgrad_adamw_moments, len(state), state._address, to[0].at, to[1].at, stream=stream)
+    if given:
+        _lists().written(given, to[0].at, len(state))
     return out
 
 

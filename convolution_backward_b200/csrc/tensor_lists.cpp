@@ -201,10 +201,32 @@ PyObject* disjoint(PyObject*, PyObject* const* args, Py_ssize_t count)
     Py_RETURN_TRUE;
 }
 
+// written(tensors, addresses, n): counts an in-place change of each tensor of the list but those whose addresses[i % n]
+// is 0, so that a graph that has saved one of them raises when it is run backward, as after torch's own in-place
+// operations.
+PyObject* written(PyObject*, PyObject* const* args, Py_ssize_t count)
+{
+    if (count != 3 || !PyList_Check(args[0])) {
+        PyErr_SetString(PyExc_TypeError, "written(tensors: list, addresses, n)");
+        return nullptr;
+    }
+    const uint64_t* const at = address<const uint64_t>(args[1]);
+    const Py_ssize_t n = PyLong_AsSsize_t(args[2]);
+    if (PyErr_Occurred()) return nullptr;
+    for (Py_ssize_t i = 0; i < PyList_GET_SIZE(args[0]); ++i) {
+        PyObject* const o = PyList_GET_ITEM(args[0], i);
+        if (!at[i % n] || !THPVariable_Check(o)) continue;
+        const at::Tensor& t = THPVariable_Unpack(o);
+        if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();     // inference tensors have no count
+    }
+    Py_RETURN_NONE;
+}
+
 PyMethodDef methods[] = {
     {"read", entry<read>(), METH_FASTCALL, nullptr},
     {"describe", entry<describe>(), METH_FASTCALL, nullptr},
     {"same", entry<same>(), METH_FASTCALL, nullptr},
+    {"written", entry<written>(), METH_FASTCALL, nullptr},
     {"disjoint", entry<disjoint>(), METH_FASTCALL, nullptr},
     {"apart", entry<apart>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},

@@ -229,6 +229,51 @@ def test_shrunk_tensors_are_refused(bits):
     cb.check_status()
 
 
+def test_written_tensors_count_a_change():
+    a, b, c, d = (torch.zeros(3) for _ in range(4))
+    with torch.inference_mode():
+        e = torch.zeros(3)
+    at = np.array([1, 0], dtype=np.uint64)
+    cb._lists().written([a, b, c, d, e], at.ctypes.data, 2)
+    assert [t._version for t in (a, b, c, d)] == [1, 0, 1, 0]
+    with pytest.raises(TypeError):
+        cb._lists().written((a,), at.ctypes.data, 2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_graph_that_needs_the_old_weights_raises(bits):
+    w, idle = (torch.ones(300, device="cuda", requires_grad=True) for _ in range(2))
+    state = cb.adamw_state([w, idle], bits=bits)
+    loss, other = (w * w).sum(), (idle * idle).sum()
+    versions = [t._version for t in state.params]
+    cb.adamw_step(state, [torch.ones(300, device="cuda"), None], 1, 1e-3)
+    assert [t._version - v for t, v in zip(state.params, versions)] == [1, 0]
+    half = cb.adamw_state([torch.ones(3, dtype=torch.bfloat16, device="cuda")], bits=bits, master=True)
+    before = [t._version for t in (*half.params, *half.master)]
+    cb.adamw_step(half, [torch.ones(3, dtype=torch.bfloat16, device="cuda")], 1, 1e-3)
+    assert [t._version - v for t, v in zip((*half.params, *half.master), before)] == [1, 1]
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    other.backward()
+    assert torch.equal(idle.grad, 2 * torch.ones_like(idle))
+    (w * w).sum().backward()
+    assert torch.equal(w.grad, 2 * w.detach())
+    if bits == 8:
+        out = [[torch.zeros(300, device="cuda") for _ in range(2)] for _ in range(2)]
+        cb.adamw_moments(state, out=out)
+        assert all(t._version == 1 for ts in out for t in ts)
+    with pytest.raises(cb.DgradError):
+        cb.adamw_step(state, [w.grad, None], 0, 1e-3)
+    assert w._version == versions[0] + 1         # refused: nothing was written
+    with torch.inference_mode():
+        cb.adamw_step(state, [w.grad, None], 2, 1e-3)
+        p = torch.ones(5, device="cuda")
+        cb.adamw_step(cb.adamw_state([p], bits=bits), [torch.ones(5, device="cuda")], 1, 1e-3)
+    assert (p < 1).all()
+    cb.check_status()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-40, 1.2e-38, 1e-30, 1e-13])
