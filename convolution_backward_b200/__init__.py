@@ -899,12 +899,16 @@ def _lists():
     if _reader is None:
         import importlib
 
-        import torch  # noqa: F401  (its libraries come first)
+        import torch       # its libraries come first
         try:
-            _reader = importlib.import_module("._tensor_lists", __name__)
+            reader = importlib.import_module("._tensor_lists", __name__)
         except ImportError as e:
             raise DgradUnavailable(f"cannot load _tensor_lists: {e}; build it with "
                                    "`python -m convolution_backward_b200._build`") from e
+        if reader.torch_version != torch.__version__.split("+")[0]:
+            raise DgradUnavailable(f"_tensor_lists was built against torch {reader.torch_version}, this is {torch.__version__}; "
+                                   "build it again with `python -m convolution_backward_b200._build`")
+        _reader = reader
     return _reader
 
 

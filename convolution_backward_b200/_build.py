@@ -6,13 +6,15 @@ linked statically.  ptxas register/spill reports go to _build/ptxas.log.  The
 same sources built with -DDGRAD_DEBUG (objects in _build/debug/) give
 libdgrad_debug.so, whose kernels check every hand-indexed store against its
 output buffer.  csrc/tensor_lists.cpp, the binding's reader of tensor lists, becomes the Python
-extension module convolution_backward_b200/_tensor_lists.so (g++, torch's headers).  Rebuilds only
-when a source, header or this file is newer than a library.
+extension module convolution_backward_b200/_tensor_lists (g++, torch's headers), and is left out where there is no
+torch: the libraries need none.  Rebuilds only when a source, header or this file is newer than a library, and the
+module also when torch or Python is another.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -27,7 +29,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdgrad.so")
 LIB_DEBUG = os.path.join(PKG, "libdgrad_debug.so")
 
-LISTS = os.path.join(PKG, "_tensor_lists.so")
+LISTS = os.path.join(PKG, "_tensor_lists" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))   # this Python's
+LISTS_FOR = os.path.join(BUILD, "tensor_lists.torch")      # the torch that it was built against
 LISTS_SRC = os.path.join(CSRC, "tensor_lists.cpp")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -57,27 +60,52 @@ def needs_build() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch():
+    """(package folder, version) of the installed torch, or None."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "unknown"
+    return list(spec.submodule_search_locations)[0], version
+
+
+def lists_need_build() -> bool:
+    if not os.path.exists(LISTS) or not os.path.exists(LISTS_FOR):
+        return True
+    with open(LISTS_FOR) as f:
+        if f.read() != _torch()[1]:
+            return True
+    return any(os.path.getmtime(f) > os.path.getmtime(LISTS) for f in (LISTS_SRC, os.path.abspath(__file__)))
+
+
 def _build_lists() -> None:
-    torch = importlib.util.find_spec("torch")
-    if torch is None or not torch.submodule_search_locations:
-        raise RuntimeError("torch not found: the binding is built against its headers")
-    root = list(torch.submodule_search_locations)[0]
+    root, version = _torch()
     tmp = LISTS + f".tmp{os.getpid()}"
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
-           "/usr/local/cuda/include", sysconfig.get_paths()["include"]]
+           sysconfig.get_paths()["include"]]
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", *[f"-I{i}" for i in inc], LISTS_SRC, "-o", tmp,
            "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {LISTS_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LISTS)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(LISTS_FOR, "w") as f:
+        f.write(version)
+    untagged = os.path.join(PKG, "_tensor_lists.so")       # one that any Python would load
+    if untagged != LISTS and os.path.exists(untagged):
+        os.remove(untagged)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=1) as ex:
         lists = None
-        if force or not os.path.exists(LISTS) or any(os.path.getmtime(f) > os.path.getmtime(LISTS)
-                                                     for f in (LISTS_SRC, os.path.abspath(__file__))):
+        if _torch() is None:
+            print("no torch: the Python binding's _tensor_lists module is not built")
+        elif force or lists_need_build():
             lists = ex.submit(_build_lists)
         if force or needs_build():
             _build_kernels()

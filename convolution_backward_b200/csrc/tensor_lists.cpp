@@ -6,6 +6,7 @@
 
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <algorithm>
 #include <cstdint>
@@ -236,4 +237,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_lists", nullptr, -1, metho
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__tensor_lists() { return PyModule_Create(&module); }
+// torch_version: the headers' torch, whose tensors are laid out as this module reads them.
+PyMODINIT_FUNC PyInit__tensor_lists()
+{
+    PyObject* const m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
