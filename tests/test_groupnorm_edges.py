@@ -144,3 +144,120 @@ def test_sums_up_to_the_range(shape, way):
     nan = torch.isnan(mean).repeat_interleave(D, dim=1)[:, None, :].expand_as(y)
     assert torch.isnan(y[nan]).all() and torch.equal(y[~nan], b.expand_as(y)[~nan])
     cb.check_status()
+
+
+# ------------------------------------------------------------------ which way, and sizes at the ends
+
+def _ways(N, S, C, G, dtype):
+    """(forward, backward): "cluster" or "streaming", from the workspaces: the cluster way needs none forward, and
+    2 C sums for each of its N K blocks along the positions (K up to 8) backward."""
+    cb._gn_workspace.cache_clear()
+    t = TYPES[dtype][0]
+    fwd = cb.groupnorm_forward_workspace_bytes(N, S, C, G, t)
+    bwd = cb.groupnorm_backward_workspace_bytes(N, S, C, G, t)
+    clusters = [-(-(N * k * 2 * C * 4) // 16) * 16 for k in (1, 2, 4, 8)]
+    return "streaming" if fwd else "cluster", "cluster" if bwd in clusters else "streaming"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("cluster", [1, 2, 4, 8])
+@pytest.mark.parametrize("shape", [(3, 100, 96, 8, 2), (2, 150, 40, 1, 1), (1, 300, 66, 6, 4), (5, 9, 256, 32, 5), (2, 130, 24, 8, 3)], ids=IDS)
+def test_every_cluster_size_runs(shape, cluster, dtype, monkeypatch):
+    """Sizes whose slices fit the shared memory of every cluster: the way that was named is the one that runs."""
+    N, S, C, G, slices = shape
+    monkeypatch.setenv("DGRAD_GN_WAY", "c")
+    monkeypatch.setenv("DGRAD_GN_CLUSTER", str(cluster))
+    monkeypatch.setenv("DGRAD_GN_SLICES", str(slices))
+    assert _ways(N, S, C, G, dtype) == ("cluster", "cluster")
+    assert cb.groupnorm_backward_workspace_bytes(N, S, C, G, TYPES[dtype][0]) == -(-(N * cluster * 2 * C * 4) // 16) * 16
+    x, g, b, dy = tg._inputs(N, S, C, dtype, seed=S + cluster)
+    y, mean, rstd = cb.groupnorm_forward(x, G, g, b, act="silu", stats=True)
+    tg._check_fwd(x, G, g, b, 1e-5, "silu", dtype, y, mean, rstd, "forward")
+    got = cb.groupnorm_backward(dy, x, mean, rstd, g, b, act="silu")
+    tg._check_bwd(dy, x, g, b, mean, rstd, "silu", dtype, got, "backward")
+    x[0, :, :C // G] = 100.1
+    y, mean, rstd = cb.groupnorm_forward(x, G, g, b, stats=True)
+    assert torch.equal(y[0, :, :C // G], b[:C // G].expand(S, C // G))
+    tg._check_fwd(x, G, g, b, 1e-5, None, dtype, y, mean, rstd, "one constant group")
+    cb.check_status()
+    cb._gn_workspace.cache_clear()
+
+
+def test_the_choice_takes_both_ways(monkeypatch):
+    monkeypatch.delenv("DGRAD_GN_WAY", raising=False)
+    assert _ways(2, 64, 512, 32, "bf16") == ("cluster", "cluster")
+    assert _ways(16, 4096, 384, 32, "bf16") == ("streaming", "streaming")
+    monkeypatch.setenv("DGRAD_GN_WAY", "s")
+    assert _ways(2, 64, 512, 32, "bf16") == ("streaming", "streaming")
+    monkeypatch.setenv("DGRAD_GN_WAY", "c")
+    assert _ways(16, 1024, 384, 32, "bf16") == ("cluster", "cluster")
+    assert _ways(1, 1 << 20, 8, 1, "bf16") == ("streaming", "streaming")      # fits nowhere
+    cb._gn_workspace.cache_clear()
+
+
+@pytest.mark.gpu
+def test_kept_choices_of_many_sizes(monkeypatch):
+    """More sizes in turn than a thread keeps choices for, forward and backward, twice over."""
+    monkeypatch.delenv("DGRAD_GN_WAY", raising=False)
+    cb._gn_workspace.cache_clear()
+    sizes = [(2, 64, 512, 32), (1, 16384, 8, 2), (3, 33, 21, 7), (4, 256, 96, 32), (2, 64, 512, 16), (2, 65, 512, 32), (1, 5000, 64, 8),
+             (7, 1, 40, 5), (2, 512, 64, 32), (64, 2, 512, 32), (5, 700, 66, 6), (1, 64, 512, 32)]
+    ins = [tg._inputs(N, S, C, "f32", seed=k) for k, (N, S, C, G) in enumerate(sizes)]
+    first = None
+    for turn in range(2):
+        outs = []
+        for (N, S, C, G), (x, g, b, dy) in zip(sizes, ins):
+            y, mean, rstd = cb.groupnorm_forward(x, G, g, b, act="silu", stats=True)
+            outs.append((y, mean, rstd, *cb.groupnorm_backward(dy, x, mean, rstd, g, b, act="silu")))
+            if turn == 0:
+                tg._check_fwd(x, G, g, b, 1e-5, "silu", "f32", y, mean, rstd, f"{N}x{S}x{C}")
+                tg._check_bwd(dy, x, g, b, mean, rstd, "silu", "f32", outs[-1][3:], f"{N}x{S}x{C}")
+        first = first or outs
+    assert all(torch.equal(p, q) for a, b in zip(first, outs) for p, q in zip(a, b))
+    cb.check_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(8192, 1, 64, 8), (3000, 3, 40, 5), (70000, 1, 8, 2), (513, 5, 33, 3), (2, 3, 65536, 32), (1, 2, 65535, 5)],
+                         ids=IDS)
+def test_many_samples_and_the_most_channels(shape, dtype, way):
+    N, S, C, G = shape
+    x, g, b, dy = tg._inputs(N, S, C, dtype, seed=C + S)
+    y, mean, rstd = cb.groupnorm_forward(x, G, g, b, act="silu", stats=True)
+    tg._check_fwd(x, G, g, b, 1e-5, "silu", dtype, y, mean, rstd, "forward")
+    got = cb.groupnorm_backward(dy, x, mean, rstd, g, b, act="silu")
+    tg._check_bwd(dy, x, g, b, mean, rstd, "silu", dtype, got, "backward")
+    cb.check_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [96, 99])
+def test_gradients_past_32_bits(C):
+    """More than 2^31 elements, all different samples: small whole numbers with mean 0 and rstd 1, so that n = x and every
+    sum is a whole number that fp32 holds (of random signs: far below 2^24).  dgamma and dbeta are those numbers rounded to
+    bf16; dX carries the divisions by m and four operations, and its rounding."""
+    N, S, G = 34, -(-(1 << 31) // (33 * C)), 3
+    D, m = C // G, S * (C // G)
+    r = torch.Generator(device="cuda").manual_seed(2)
+    xi, di = (torch.randint(-2, 3, (N, S, C), dtype=torch.int8, device="cuda", generator=r) for _ in range(2))
+    assert xi.numel() > 1 << 31
+    x, dy = xi.bfloat16(), di.bfloat16()
+    g = (1 + torch.arange(C, device="cuda") % 2).bfloat16()
+    mean, rstd = torch.zeros(N, G, device="cuda"), torch.ones(N, G, device="cuda")
+    dx, dg, db = cb.groupnorm_backward(dy, x, mean, rstd, g)
+    want_g, want_b = torch.zeros(C, dtype=torch.int64, device="cuda"), torch.zeros(C, dtype=torch.int64, device="cuda")
+    for n in range(N):
+        a, d = xi[n].double(), di[n].double()
+        want_g += (a * d).sum(0).long()
+        want_b += d.sum(0).long()
+        q = d * g.double()
+        qa = q.view(S, G, D).sum((0, 2)) / m
+        qb = (q * a).view(S, G, D).sum((0, 2)) / m
+        ref = q - qa.repeat_interleave(D) - a * qb.repeat_interleave(D)
+        bound = 2.0 ** -8 * ref.abs() + 1.01 * 4 * E32 * (q.abs() + qa.abs().repeat_interleave(D) + 2 * (a * qb.repeat_interleave(D)).abs())
+        assert ((dx[n].double() - ref).abs() <= bound + 1e-30).all(), n
+    assert torch.equal(dg, want_g.float().bfloat16()) and torch.equal(db, want_b.float().bfloat16())
+    assert want_g.abs().max() < 1 << 24 and want_b.abs().max() < 1 << 24
+    cb.check_status()
