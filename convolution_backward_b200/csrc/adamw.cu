@@ -4,8 +4,9 @@
 // For each element, all in fp32, with g = scale * grad:
 //     m' = b1 m + (1 - b1) g,   v' = b2 v + (1 - b2) g g
 //     p' = p (1 - lr wd) - lr (m' / (1 - b1^t)) / (sqrt(v' / (1 - b2^t)) + eps)
-// A handful of operations for 22 to 28 bytes (8-bit states 10 to 18): HBM bounds it, the 8-bit step its
-// instructions.  A launch takes a table of
+// A handful of operations for 22 to 28 bytes (8-bit states 10 to 18): HBM bounds it.  The 8-bit step has 78 to 109
+// instructions an element and is bound by nothing alone (slots 60 to 68% busy): a warp loads a block, computes and stores one after
+// the other, with three blocks of warps an SM.  A launch takes a table of
 // tensors among its parameters (no copy to the device, nothing kept between calls, so a
 // captured step carries its own), and its blocks take equal runs of 2048-element chunks.
 //
@@ -346,120 +347,120 @@ __device__ __forceinline__ void adamw_block(const AdamTensor& t, long long q, co
 {
     const int lane = threadIdx.x & 31;
     const long long i0 = q * kQuant + lane * 4;
-            float4 g[kSteps], w[kSteps], m[kSteps], v[kSteps];
-            uint32_t cm[kSteps], cv[kSteps];
-            float mtop = 0.f, vtop = 0.f;
+    float4 g[kSteps], w[kSteps], m[kSteps], v[kSteps];
+    uint32_t cm[kSteps], cv[kSteps];
+    float mtop = 0.f, vtop = 0.f;
+    if constexpr (MODE != 0) {
+        mtop = t.m_max[q];
+        vtop = t.v_max[q];
+    }
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j) {
+        const long long i = i0 + j * 128;
+        const int have = FULL ? 4 : static_cast<int>(max(0LL, min(4LL, t.n - i)));
+        g[j] = load4<GK, FULL>(t.g, i, have);
+        w[j] = MASTER ? load4<kF32, FULL>(t.w, i, have) : load4<PK, FULL>(t.p, i, have);
+        if constexpr (MODE == 0) {
+            m[j] = load4<kF32, FULL>(t.m, i, have);
+            v[j] = load4<kF32, FULL>(t.v, i, have);
+        } else {
+            cm[j] = load_codes<FULL>(t.m, i, have);
+            cv[j] = load_codes<FULL>(t.v, i, have);
+        }
+    }
+    float big_m = 0.f, big_v = 0.f;
+    float2 root[kSteps][2];
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j) {
+        float2 gg[2] = {make_float2(g[j].x, g[j].y), make_float2(g[j].z, g[j].w)};
+        float2 ww[2] = {make_float2(w[j].x, w[j].y), make_float2(w[j].z, w[j].w)};
+        float2 mm[2], vv[2];
+        if constexpr (MODE == 0) {
+            mm[0] = make_float2(m[j].x, m[j].y);
+            mm[1] = make_float2(m[j].z, m[j].w);
+            vv[0] = make_float2(v[j].x, v[j].y);
+            vv[1] = make_float2(v[j].z, v[j].w);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
             if constexpr (MODE != 0) {
-                mtop = t.m_max[q];
-                vtop = t.v_max[q];
+                mm[k] = decode_m2(P, cm[j], 2 * k, pair(mtop));
+                vv[k] = decode_v2(P, cv[j], 2 * k, pair(vtop));
             }
-    #pragma unroll
-            for (int j = 0; j < kSteps; ++j) {
-                const long long i = i0 + j * 128;
-                const int have = FULL ? 4 : static_cast<int>(max(0LL, min(4LL, t.n - i)));
-                g[j] = load4<GK, FULL>(t.g, i, have);
-                w[j] = MASTER ? load4<kF32, FULL>(t.w, i, have) : load4<PK, FULL>(t.p, i, have);
-                if constexpr (MODE == 0) {
-                    m[j] = load4<kF32, FULL>(t.m, i, have);
-                    v[j] = load4<kF32, FULL>(t.v, i, have);
-                } else {
-                    cm[j] = load_codes<FULL>(t.m, i, have);
-                    cv[j] = load_codes<FULL>(t.v, i, have);
-                }
-            }
-            float big_m = 0.f, big_v = 0.f;
-            float2 root[kSteps][2];
-    #pragma unroll
-            for (int j = 0; j < kSteps; ++j) {
-                float2 gg[2] = {make_float2(g[j].x, g[j].y), make_float2(g[j].z, g[j].w)};
-                float2 ww[2] = {make_float2(w[j].x, w[j].y), make_float2(w[j].z, w[j].w)};
-                float2 mm[2], vv[2];
-                if constexpr (MODE == 0) {
-                    mm[0] = make_float2(m[j].x, m[j].y);
-                    mm[1] = make_float2(m[j].z, m[j].w);
-                    vv[0] = make_float2(v[j].x, v[j].y);
-                    vv[1] = make_float2(v[j].z, v[j].w);
-                }
-    #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if constexpr (MODE != 0) {
-                        mm[k] = decode_m2(P, cm[j], 2 * k, pair(mtop));
-                        vv[k] = decode_v2(P, cv[j], 2 * k, pair(vtop));
-                    }
-                    step2(P, gg[k], mm[k], vv[k], ww[k], root[j][k], h, st);
-                    if constexpr (MODE != 0) {
-                        big_m = larger(larger(big_m, mm[k].x), mm[k].y);
-                        big_v = larger(larger(big_v, vv[k].x), vv[k].y);
-                    }
-                }
-                m[j] = make_float4(mm[0].x, mm[0].y, mm[1].x, mm[1].y);
-                v[j] = make_float4(vv[0].x, vv[0].y, vv[1].x, vv[1].y);
-                w[j] = make_float4(ww[0].x, ww[0].y, ww[1].x, ww[1].y);
-            }
-            CodeScale sm, sv;
-            float roots = 0.f;      // root_of(v' inv) = root_of(root roots), where ordinary numbers allow it
+            step2(P, gg[k], mm[k], vv[k], ww[k], root[j][k], h, st);
             if constexpr (MODE != 0) {
-                big_m = warp_largest(big_m);
-                big_v = warp_largest(big_v);
-                sm = code_scale<false>(big_m);
-                sv = code_scale<true>(big_v);
-                if (sv.k == 1.0f && st.ibc2 < 0x1p30f) roots = root_of(sv.inv / st.ibc2);
-                const long long nq = (t.n + kQuant - 1) / kQuant;
-                if (lane == 0 && store_ok(t.m_max, nq * 4, t.m_max + q, 4, h.status)) t.m_max[q] = big_m;
-                if (lane == 0 && store_ok(t.v_max, nq * 4, t.v_max + q, 4, h.status)) t.v_max[q] = big_v;
+                big_m = larger(larger(big_m, mm[k].x), mm[k].y);
+                big_v = larger(larger(big_v, vv[k].x), vv[k].y);
             }
-    #pragma unroll
-            for (int j = 0; j < kSteps; ++j) {
-                const long long i = i0 + j * 128;
-                const int have = FULL ? 4 : static_cast<int>(max(0LL, min(4LL, t.n - i)));
-                if (MASTER) store4<kF32, FULL>(t.w, i, have, w[j], t.n, h.status);
-                store4<PK, FULL>(t.p, i, have, w[j], t.n, h.status);
-                if constexpr (MODE == 0) {
-                    store4<kF32, FULL>(t.m, i, have, m[j], t.n, h.status);
-                    store4<kF32, FULL>(t.v, i, have, v[j], t.n, h.status);
-                } else {
-                    uint4 bits = make_uint4(0, 0, 0, 0);
-                    if constexpr (MODE == 2)
-                        bits = opt_philox(h, static_cast<unsigned long long>(t.block0 + q) * (kQuant / 4) + lane + j * 32);
-                    const uint32_t word[4] = {bits.x, bits.y, bits.z, bits.w};
-                    uint32_t om[2], ov[2];
-    #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float2 x = k ? make_float2(m[j].z, m[j].w) : make_float2(m[j].x, m[j].y);
-                        const float2 y = k ? make_float2(v[j].z, v[j].w) : make_float2(v[j].x, v[j].y);
-                        float2 dm = pair(0.f), dv = pair(0.f);
-                        if constexpr (MODE == 2) {
-                            dm = add2(make_float2(half_float(word[2 * k], 0), half_float(word[2 * k + 1], 0)), pair(-kTwo23));
-                            dv = add2(make_float2(half_float(word[2 * k], 1), half_float(word[2 * k + 1], 1)), pair(-kTwo23));
-                        }
-                        float2 wm = make_float2(fabsf(x.x), fabsf(x.y)), wv = y;
-            if (sm.k != 1.0f) wm = P.mul(wm, pair(sm.k));
-            if (sv.k != 1.0f) wv = P.mul(wv, pair(sv.k));
-            wm = P.mul(wm, pair(sm.inv));
-            wv = P.mul(wv, pair(sv.inv));
-                                    const float2 rm = make_float2(root_of(wm.x), root_of(wm.y));
-                        float2 rv = P.mul(root[j][k], pair(roots));
-                        if (roots == 0.f) rv = make_float2(root_of(wv.x), root_of(wv.y));
-                        rv = make_float2(root_of(rv.x), root_of(rv.y));
-                        bool below = false;
-                        float2 a = code2<false, MODE == 1>(P, wm, rm, dm, below), b = code2<true, MODE == 1>(P, wv, rv, dv, below);
-                        if (MODE == 2 && below) {
-                            const float2 la = low_of(rm), lb = low_of(rv);
-                            a = make_float2(code_of<false>(wm.x, la.x, dm.x), code_of<false>(wm.y, la.y, dm.y));
-                            b = make_float2(code_of<true>(wv.x, lb.x, dv.x), code_of<true>(wv.y, lb.y, dv.y));
-                        }
-                        // the low byte of 2^23 + code; m's codes are 128 higher there
-                        const float2 as = add2(make_float2(copysignf(a.x, x.x), copysignf(a.y, x.y)), pair(kTwo23 + 128.0f));
-                        // v' inf is inf, or NaN for 0: 1 or 0
-                    const float inf = __int_as_float(0x7F800000);
-                    const float2 bs = add2(make_float2(fmaxf(b.x, __saturatef(y.x * inf)), fmaxf(b.y, __saturatef(y.y * inf))), pair(kTwo23));
-                        om[k] = __byte_perm(__float_as_uint(as.x), __float_as_uint(as.y), 0x0040);
-                        ov[k] = __byte_perm(__float_as_uint(bs.x), __float_as_uint(bs.y), 0x0040);
-                    }
-                    store_codes<FULL>(t.m, i, have, __byte_perm(om[0], om[1], 0x5410) ^ 0x80808080u, t.n, h.status);
-                    store_codes<FULL>(t.v, i, have, __byte_perm(ov[0], ov[1], 0x5410), t.n, h.status);
+        }
+        m[j] = make_float4(mm[0].x, mm[0].y, mm[1].x, mm[1].y);
+        v[j] = make_float4(vv[0].x, vv[0].y, vv[1].x, vv[1].y);
+        w[j] = make_float4(ww[0].x, ww[0].y, ww[1].x, ww[1].y);
+    }
+    CodeScale sm, sv;
+    float roots = 0.f;      // root_of(v' inv) = root_of(root roots), where ordinary numbers allow it
+    if constexpr (MODE != 0) {
+        big_m = warp_largest(big_m);
+        big_v = warp_largest(big_v);
+        sm = code_scale<false>(big_m);
+        sv = code_scale<true>(big_v);
+        if (sv.k == 1.0f && st.ibc2 < 0x1p30f) roots = root_of(sv.inv / st.ibc2);
+        const long long nq = (t.n + kQuant - 1) / kQuant;
+        if (lane == 0 && store_ok(t.m_max, nq * 4, t.m_max + q, 4, h.status)) t.m_max[q] = big_m;
+        if (lane == 0 && store_ok(t.v_max, nq * 4, t.v_max + q, 4, h.status)) t.v_max[q] = big_v;
+    }
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j) {
+        const long long i = i0 + j * 128;
+        const int have = FULL ? 4 : static_cast<int>(max(0LL, min(4LL, t.n - i)));
+        if (MASTER) store4<kF32, FULL>(t.w, i, have, w[j], t.n, h.status);
+        store4<PK, FULL>(t.p, i, have, w[j], t.n, h.status);
+        if constexpr (MODE == 0) {
+            store4<kF32, FULL>(t.m, i, have, m[j], t.n, h.status);
+            store4<kF32, FULL>(t.v, i, have, v[j], t.n, h.status);
+        } else {
+            uint4 bits = make_uint4(0, 0, 0, 0);
+            if constexpr (MODE == 2)
+                bits = opt_philox(h, static_cast<unsigned long long>(t.block0 + q) * (kQuant / 4) + lane + j * 32);
+            const uint32_t word[4] = {bits.x, bits.y, bits.z, bits.w};
+            uint32_t om[2], ov[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float2 x = k ? make_float2(m[j].z, m[j].w) : make_float2(m[j].x, m[j].y);
+                const float2 y = k ? make_float2(v[j].z, v[j].w) : make_float2(v[j].x, v[j].y);
+                float2 dm = pair(0.f), dv = pair(0.f);
+                if constexpr (MODE == 2) {
+                    dm = add2(make_float2(half_float(word[2 * k], 0), half_float(word[2 * k + 1], 0)), pair(-kTwo23));
+                    dv = add2(make_float2(half_float(word[2 * k], 1), half_float(word[2 * k + 1], 1)), pair(-kTwo23));
                 }
+                float2 wm = make_float2(fabsf(x.x), fabsf(x.y)), wv = y;
+                if (sm.k != 1.0f) wm = P.mul(wm, pair(sm.k));
+                if (sv.k != 1.0f) wv = P.mul(wv, pair(sv.k));
+                wm = P.mul(wm, pair(sm.inv));
+                wv = P.mul(wv, pair(sv.inv));
+                const float2 rm = make_float2(root_of(wm.x), root_of(wm.y));
+                float2 rv = P.mul(root[j][k], pair(roots));
+                if (roots == 0.f) rv = make_float2(root_of(wv.x), root_of(wv.y));
+                rv = make_float2(root_of(rv.x), root_of(rv.y));
+                bool below = false;
+                float2 a = code2<false, MODE == 1>(P, wm, rm, dm, below), b = code2<true, MODE == 1>(P, wv, rv, dv, below);
+                if (MODE == 2 && below) {
+                    const float2 la = low_of(rm), lb = low_of(rv);
+                    a = make_float2(code_of<false>(wm.x, la.x, dm.x), code_of<false>(wm.y, la.y, dm.y));
+                    b = make_float2(code_of<true>(wv.x, lb.x, dv.x), code_of<true>(wv.y, lb.y, dv.y));
+                }
+                // the low byte of 2^23 + code; m's codes are 128 higher there
+                const float2 as = add2(make_float2(copysignf(a.x, x.x), copysignf(a.y, x.y)), pair(kTwo23 + 128.0f));
+                // v' inf is inf, or NaN for 0: 1 or 0
+                const float inf = __int_as_float(0x7F800000);
+                const float2 bs = add2(make_float2(fmaxf(b.x, __saturatef(y.x * inf)), fmaxf(b.y, __saturatef(y.y * inf))), pair(kTwo23));
+                om[k] = __byte_perm(__float_as_uint(as.x), __float_as_uint(as.y), 0x0040);
+                ov[k] = __byte_perm(__float_as_uint(bs.x), __float_as_uint(bs.y), 0x0040);
             }
+            store_codes<FULL>(t.m, i, have, __byte_perm(om[0], om[1], 0x5410) ^ 0x80808080u, t.n, h.status);
+            store_codes<FULL>(t.v, i, have, __byte_perm(ov[0], ov[1], 0x5410), t.n, h.status);
+        }
+    }
 }
 
 // A register more than 64 (80) a thread would leave an SM fewer blocks: 60 M parameters, fp32 states, 274 us with
@@ -586,8 +587,8 @@ struct NormTable {
     NormTensor t[CAP];
 };
 
-// Squares of fp32 values are exact in 64 bits, and their sums need not fear overflow, order or
-// length.  The sum of a thread's 16 squares is formed first, so that its chain is short.
+// Squares of fp32 values are exact in 64 bits, and their sums need not fear overflow, order or length.  A
+// thread adds them one after the other, a chain of 64-bit operations that its block's other warps hide.
 template <int EK, int CAP>
 __global__ void __launch_bounds__(kOptBlock) norm_kernel(const __grid_constant__ NormTable<CAP> tab)
 {

@@ -385,15 +385,15 @@ __global__ void __launch_bounds__(kT, 2) gn_cluster_bwd_kernel(const GnCluster a
     auto take = [&](const V& xv, const V& dv, int step) {
         float2 n[NP], dz[NP];
         slope(xv, dv, n, dz);
-                    if constexpr (VEC == 1) {
-                        xv.store(mine, static_cast<long long>(step) * kT * VEC);
-                        mine_dz[step * kT] = dz[0].x;
-                    } else {
-        #pragma unroll
-                        for (int q = 0; q < NQ; ++q)
-                            *reinterpret_cast<float4*>(mine_dz + (step * NQ + q) * kT * 4) =
-                                make_float4(dz[2 * q].x, dz[2 * q].y, dz[2 * q + 1].x, dz[2 * q + 1].y);
-                    }
+        if constexpr (VEC == 1) {
+            xv.store(mine, static_cast<long long>(step) * kT * VEC);
+            mine_dz[step * kT] = dz[0].x;
+        } else {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+                *reinterpret_cast<float4*>(mine_dz + (step * NQ + q) * kT * 4) =
+                    make_float4(dz[2 * q].x, dz[2 * q].y, dz[2 * q + 1].x, dz[2 * q + 1].y);
+        }
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             A[i] = __fadd2_rn(A[i], dz[i]);
@@ -413,6 +413,12 @@ __global__ void __launch_bounds__(kT, 2) gn_cluster_bwd_kernel(const GnCluster a
 #pragma unroll
             for (int u = 0; u < U; ++u) take(xv[u], dv[u], k + u);
         }
+        for (; k < kept; ++k) {
+            V xv, dv;
+            xv.load(a.x, it.first + k * stride);
+            dv.load(a.dy, it.first + k * stride);
+            take(xv, dv, k);
+        }
     } else {
         for (; k < kept; ++k) {
             gn_copy_wait<kAheadBwd - 1>();
@@ -421,14 +427,6 @@ __global__ void __launch_bounds__(kT, 2) gn_cluster_bwd_kernel(const GnCluster a
             dv.load(mine_dz + k * NQ * kT * 4, 0);
             take(xv, dv, k);
             bring(k + kAheadBwd);
-        }
-    }
-    if constexpr (VEC == 1) {
-        for (; k < kept; ++k) {
-            V xv, dv;
-            xv.load(a.x, it.first + k * stride);
-            dv.load(a.dy, it.first + k * stride);
-            take(xv, dv, k);
         }
     }
     float* const outA = sh.out;
