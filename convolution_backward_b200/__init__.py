@@ -1001,19 +1001,20 @@ class AdamWState:
         size = np.array([t.numel() * t.element_size() for t in everything if t.numel()], dtype=np.uint64)
         order = np.argsort(lo)
         self._lo, self._hi = _Array(lo[order]), _Array((lo + size)[order])
+        self._ranges = (self._lo.at, self._hi.at, len(order))
         # one step's gradients; a call of adamw_step fills them and has read them when it returns
         self._grads = _Array(np.zeros(n, dtype=np.uint64))
 
     def _apart(self, at, nbytes):
-        return _lists().apart(at, self._n.at, len(self.params), nbytes, self._lo.at, self._hi.at, len(self._lo.a))
+        return _lists().apart(at, self._n.at, len(self.params), nbytes, *self._ranges)
 
     def __reduce__(self):
         """Copies and pickles are made anew from (copies of) the tensors: the addresses held here are this state's own."""
         lists = (self.params, self.m, self.v, self.master, self.m_max, self.v_max)
         return type(self), tuple(None if ts is None else list(ts) for ts in lists)
 
-    def _unchanged(self):
-        if not _lists().same(self._all, *self._was_at):
+    def _unchanged(self, lists):
+        if not lists.same(self._all, *self._was_at):
             raise ValueError("the storage, size or type of a parameter or state has changed since its AdamWState was made")
 
     def __len__(self):
@@ -1077,15 +1078,16 @@ def adamw_step(state, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_deca
     grads = list(grads)
     dev = state.device
     to = state._grads
-    gcode, gdev = _lists().read(grads, state._list, "gradients", to.at, 0)
+    lists = _lists()
+    gcode, gdev = lists.read(grads, state._list, "gradients", to.at, 0)
     if gcode < 0:
         gcode, gdev = state._code, dev.index     # nothing to step
     if gcode != state._code and gcode != 0:
         raise TypeError(f"gradients must be {state.dtype} or float32")
     if gdev != dev.index:
         raise ValueError("all tensors of one call must be on the same CUDA device")
-    state._unchanged()
-    if not state._apart(to.at, 4 if gcode == 0 else 2):
+    state._unchanged(lists)
+    if not lists.apart(to.at, state._n.at, n, 4 if gcode == 0 else 2, *state._ranges):
         raise ValueError("gradients must not share memory with parameters or states")
     state._table["grad"] = to.a
     h = _AdamW()
@@ -1106,7 +1108,7 @@ def adamw_step(state, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_deca
     if given:
         scalars = array.array("q", [a for a in (h.lr_device, h.step_device, h.grad_scale) if a] + [1] * len(given))
         where = scalars.buffer_info()[0]
-        if not _lists().apart(where, where + 8 * len(given), len(given), 8, state._lo.at, state._hi.at, len(state._lo.a)):
+        if not lists.apart(where, where + 8 * len(given), len(given), 8, *state._ranges):
             raise ValueError("lr, step and grad_scale must not share memory with parameters or states")
     h.beta1, h.beta2 = betas
     h.eps, h.weight_decay, h.state_bits = eps, weight_decay, state.bits
@@ -1119,7 +1121,7 @@ def adamw_step(state, grads, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_deca
         al.uses(*grads, *given, *state._all)
     _call(dev, "dgrad_adamw_step", lib().dgrad_adamw_step, n, state._address, state._code, gcode, ctypes.byref(h),
           stream=stream)
-    _lists().written(state._weights, to.at, n)
+    lists.written(state._weights, to.at, n)
 
 
 def adamw_moments(state, out=None, stream=None):
@@ -1144,7 +1146,7 @@ def adamw_moments(state, out=None, stream=None):
         given = out[0] + out[1]
         if any(t is None for t in given):
             raise TypeError("out must be tensors")
-    state._unchanged()
+    state._unchanged(_lists())
     to = [_Array(np.empty(len(state), dtype=np.uint64)) for _ in range(2)]
     for ts, at, what in zip(out, to, ("out: m", "out: v")):
         code, index = _lists().read(ts, state._list, what, at.at, 0)
