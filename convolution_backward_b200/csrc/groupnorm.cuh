@@ -232,11 +232,14 @@ __device__ __forceinline__ float2 gn_statistics(float mean, float M2, float m, f
     return make_float2(mean, 1.0f / sqrtf(M2 / m + eps));
 }
 
-// Whether the mean of `count` values lies far above their spread, eight standard deviations or more (M2: the squares
-// about it): a few roundings of such a mean are no longer small beside the spread.
+// Whether the mean of `count` values lies so far above their spread (M2: the squares about it) that its own roundings,
+// some 2^-22 of it, show in the results: from 8 standard deviations on in fp32, from 128 in 16 bits, whose results are
+// rounded to 2^-9 and 2^-12.
+template <int EK>
 __device__ __forceinline__ bool gn_far(float mean, float M2, float count)
 {
-    return mean * mean * count > 64.f * M2 || (M2 == 0.f && mean != 0.f);   // squares of small values are 0
+    constexpr float far = EK == kF32 ? 8.f : 128.f;
+    return mean * mean * count > far * far * M2 || (M2 == 0.f && mean != 0.f);   // squares of small values are 0
 }
 
 // A thread's own copies of 16 bytes from global to shared memory: nobody else reads them, so

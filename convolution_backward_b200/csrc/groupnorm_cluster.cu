@@ -122,7 +122,7 @@ struct GnItem {
 // The statistics of a slice's groups, from what its blocks have in ex: stat on return, and a.mean and a.rstd.  Whole
 // block.  MARK: true where a mean is far above the spread, and that group's rstd in stat is negative.  The
 // cluster's blocks find the same.
-template <bool MARK>
+template <int EK, bool MARK>
 __device__ __forceinline__ bool slice_statistics(const GnCluster& a, const GnShared& sh, int rank, int ng, long long stat_at)
 {
     const GnSlices& p = a.p;
@@ -146,7 +146,7 @@ __device__ __forceinline__ bool slice_statistics(const GnCluster& a, const GnSha
         }
         const float2 stats = gn_statistics(mu, sq, m, a.eps);
         sh.stat[j] = stats.x;
-        const bool again = MARK && gn_far(stats.x, sq, m);
+        const bool again = MARK && gn_far<EK>(stats.x, sq, m);
         sh.stat[p.ng + j] = again ? -stats.y : stats.y;
         far = far || again;
         if (rank == 0) {
@@ -190,7 +190,8 @@ __device__ __forceinline__ void slice_results(const GnCluster& a, const GnShared
 // What is left of a slice where a mean is far above the spread: the statistics once more, with the blocks' means of
 // such groups formed from the differences to the first mean, and the results.  A function of its own that the kernel ends
 // with: what every other slice goes through keeps its registers (16 x 1024 x 512 bf16 13.0 us; a call that returned 13.4, the same
-// code in place 13.4).
+// code in place 13.4).  It takes 5 us more where it is taken (2 x 64 x 512 fp32 4.9 us,
+// far above 10.0).
 template <int EK, int VEC, int ACT>
 __device__ __noinline__ void finish_far_slice(const GnCluster& a)
 {
@@ -229,7 +230,7 @@ __device__ __noinline__ void finish_far_slice(const GnCluster& a)
             __syncthreads();
         }
     }
-    slice_statistics<false>(a, sh, t.rank, ng, static_cast<long long>(it.n) * p.G + it.c0 / p.D);
+    slice_statistics<EK, false>(a, sh, t.rank, ng, static_cast<long long>(it.n) * p.G + it.c0 / p.D);
     slice_results<EK, VEC, ACT>(a, sh, mine, t, it);
     if (p.K > 1) cluster_wait();
 }
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kT, 2) gn_cluster_fwd_kernel(const __grid_cons
     column_totals<kT, VEC>(s, it.on, t.r, t.c, p.R, p.tw, p.parts, sh.buf, sh.part, sh.out);
     group_totals<kT, 1>(sh.out, p.tw, 1, p.tw, 0, it.width, p.D, sh.ex + p.ng, p.ng);
 
-    if (slice_statistics<true>(a, sh, t.rank, ng, stat_at)) {
+    if (slice_statistics<EK, true>(a, sh, t.rank, ng, stat_at)) {
         finish_far_slice<EK, VEC, ACT>(a);
         return;
     }

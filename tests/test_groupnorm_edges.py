@@ -79,6 +79,22 @@ def test_means_far_above_the_spread(shape, way):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("far", [6, 30, 100, 1000])
+@pytest.mark.parametrize("shape", [(333, 21, 7), (256, 768, 32), (4000, 24, 1)], ids=IDS)
+def test_means_on_both_sides_of_the_bound(shape, far, dtype, way):
+    """From some spreads to many, under test_groupnorm's bounds."""
+    S, C, G = shape
+    x, g, b, dy = tg._inputs(2, S, C, dtype, seed=far, offset=0.0)
+    x = (x.float() + far).to(x.dtype)
+    y, mean, rstd = cb.groupnorm_forward(x, G, g, b, act="silu", stats=True)
+    tg._check_fwd(x, G, g, b, 1e-5, "silu", dtype, y, mean, rstd, "forward", whole=False)
+    got = cb.groupnorm_backward(dy, x, mean, rstd, g, b, act="silu")
+    tg._check_bwd(dy, x, g, b, mean, rstd, "silu", dtype, got, "backward")
+    cb.check_status()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("shape", [s for s in SHAPES if s[2] > 1 and s[0] > 1], ids=IDS)
 def test_a_far_mean_changes_its_own_group_alone(shape, way):
     S, C, G = shape
