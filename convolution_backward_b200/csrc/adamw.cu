@@ -5,7 +5,7 @@
 //     m' = b1 m + (1 - b1) g,   v' = b2 v + (1 - b2) g g
 //     p' = p (1 - lr wd) - lr (m' / (1 - b1^t)) / (sqrt(v' / (1 - b2^t)) + eps)
 // A handful of operations for 22 to 28 bytes (8-bit states 10 to 18): HBM bounds it.  The 8-bit step has 78 to 109
-// instructions an element and is bound by nothing alone (slots 60 to 68% busy): a warp loads a block, computes and stores one after
+// instructions an element and is bound by nothing alone (slots 59 to 70% busy): a warp loads a block, computes and stores one after
 // the other, with three blocks of warps an SM.  A launch takes a table of
 // tensors among its parameters (no copy to the device, nothing kept between calls, so a
 // captured step carries its own), and its blocks take equal runs of 2048-element chunks.

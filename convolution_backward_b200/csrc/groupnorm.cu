@@ -29,8 +29,8 @@ namespace dgrad {
 namespace {
 
 constexpr int kGnBlock = 256;
-// Blocks that fill a B200, forward and backward (16 x 4096 x 384 silu: 33.6 us, with 444 blocks 38.4, 888 37.7;
-// backward 32 x 12544 x 96 gelu: 93 us, with 444 97.6, 592 98.4).
+// Blocks that fill a B200, forward (16 x 4096 x 384 silu, bf16: 34.2 us, with 444 blocks 38.3, 888 37.6; fp32 60.1, 54.3, 58.9;
+// 32 x 12544 x 96 bf16 49.8, 55.5, 51.4, fp32 87.8, 92.4, 83.7) and backward (32 x 12544 x 96 gelu: 93 us, with 444 97.6, 592 98.4).
 constexpr int kGnTarget = 148 * 4, kGnTargetBwd = 148 * 2;
 constexpr int kGnLeast = 4;          // positions a thread takes at least, where there are enough
 
@@ -113,7 +113,7 @@ constexpr int kAhead = 8;        // 16-byte copies a thread has under way
 
 // All of a thread's steps down NT tensors.  16-byte vectors come through the thread's places in
 // `ring` (kAhead of them), single elements directly, eight of each tensor at a time (backward 6 x 4000 x
-// 1001 bf16: 90 us, with four 129).  The constructor has the first ones sent for; run calls
+// 1001 bf16, no activation: 89 us, with four 129).  The constructor has the first ones sent for; run calls
 // f(element, vectors) for every step.
 template <int EK, int VEC, int NT>
 struct GnDown {
@@ -232,8 +232,8 @@ __device__ __forceinline__ float left_of(float squares, float about)
     return squares == __int_as_float(0x7F800000) ? squares : about < 0.f ? 0.f : about;
 }
 
-// Four blocks an SM, and room for the loads of single elements (16 x 4096 x 384 fp32: 59.8 us, 60.9 with the registers that
-// the compiler takes by itself; 3 x 1961 x 1001 fp32 21.6, 26.9).
+// Four blocks an SM: with the registers that the compiler takes by itself the loads of single elements wait for each other
+// (3 x 1961 x 1001 fp32 27.0 us, 21.6 so; vectors take the same time either way).
 template <int EK, int VEC>
 __global__ void __launch_bounds__(kGnBlock, 4) gn_stats_kernel(const GnFwd a)
 {

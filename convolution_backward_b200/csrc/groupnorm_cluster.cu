@@ -516,8 +516,8 @@ int64_t gcd(int64_t a, int64_t b) { return b == 0 ? a : gcd(b, a % b); }
 // busiest SM, and 1.3 to 2.2 us more for clusters of 2 to 8, as long as everything stays in shared memory
 // and rows fill their 32-byte sectors; the streaming way 8.5 us and 0.25 us per MB of tensors (10 and
 // 0.33, fp32 0.22), and 0.008 for each block that shares a sample.  So the cluster way takes what one
-// wave of blocks holds: 16 x 256 x 1024 channels, 32 groups: 8.8 us forward against 13.4, 1 x 64 x 512: 5.2
-// against 6.6, backward 6.1 against 8.0; 16 x 4096 x 384 would be 41 us against 34.
+// wave of blocks holds: 16 x 256 x 1024 channels, 32 groups: 8.8 us forward against 15.2, 1 x 64 x 512: 5.1
+// against 7.3, backward 6.0 against 6.8; 16 x 4096 x 384 would be 40 us against 34.
 bool choose(int64_t N, int64_t S, int64_t C, int64_t G, int ek, bool backward, GnSlices* out)
 {
     const char* way = tuning_env("DGRAD_GN_WAY");      // 's': always the streaming way; 'c': the cluster way wherever it fits
@@ -553,7 +553,8 @@ bool choose(int64_t N, int64_t S, int64_t C, int64_t G, int ek, bool backward, G
             const int64_t on_sm = ctas <= room ? 1 : 2, waves = (ctas + 2 * room - 1) / (2 * room);
             const int64_t limit = on_sm == 1 ? 232448 : 115712;
             if (rest + steps * step_bytes > limit || (!forced && waves > 1)) continue;
-            // half-used sectors; fp32 rows of two vectors were as slow (1 x 16384 x 128 backward 21 us, streaming 16)
+            // half-used sectors.  fp32 rows of two vectors: fitted to 1 x 16384 x 128, whose backward pass takes 20.7 us (streaming
+            // 13.5); 1 x 8192 x 256 would take 11.7 with such rows and is given wider ones, 17.9
             const double sectors = tw * es < 32 ? 3.5 : tw * es >= 64 ? 1.0 : es == 4 ? 2.2 : 1.2;
             const double cost = (backward ? 5.6 : 5.2) + (K == 1 ? 0.0 : 1.0 + 0.15 * K) +
                                 step_us * sectors * static_cast<double>(waves * on_sm * steps);
