@@ -940,10 +940,11 @@ class AdamWState:
     params: one dtype.  32-bit states: m, v fp32 of the parameters' shapes.  8-bit states: m int8 and v
     uint8 codes of the parameters' shapes, and m_max, v_max fp32 with an element for every 256 of a tensor.
     master: fp32 copies of 16-bit parameters, which are then what is stepped.  No two tensors may
-    share memory.  copy.copy shares the tensors, copy.deepcopy and pickle copy them.  The tensors stay the caller's: save them as they are, load them with copy_; where the
-    storage of one has been replaced, or its size or type changed, adamw_step refuses the state.  A step counts as an
-    in-place change of the parameters and master copies that it writes: a graph that has saved one of them raises
-    when it is run backward.  (The states are not counted, and the replay of a captured step counts nothing.)"""
+    share memory.  copy.copy shares the tensors, copy.deepcopy and pickle copy them.  The tensors stay the
+    caller's: save them as they are, load them with copy_; where the storage of one has been replaced, or its size
+    or type changed, adamw_step refuses the state.  A step counts as an in-place change of the parameters and
+    master copies that it writes: a graph that has saved one of them raises when it is run backward.  (The states
+    are not counted, and the replay of a captured step counts nothing.)"""
 
     def __init__(self, params, m, v, master=None, m_max=None, v_max=None):
         import numpy as np

@@ -189,9 +189,8 @@ __device__ __forceinline__ void slice_results(const GnCluster& a, const GnShared
 
 // What is left of a slice where a mean is far above the spread: the statistics once more, with the blocks' means of
 // such groups formed from the differences to the first mean, and the results.  A function of its own that the kernel ends
-// with: what every other slice goes through keeps its registers (16 x 1024 x 512 bf16 13.0 us; a call that returned 13.4, the same
-// code in place 13.4).  It takes 5 us more where it is taken (2 x 64 x 512 fp32 4.9 us,
-// far above 10.0).
+// with: what every other slice goes through keeps its registers (16 x 1024 x 512 bf16 13.0 us; a call that returned 13.4, the
+// same code in place 13.4).  A slice that takes it takes 5 us more (2 x 64 x 512 fp32 10.0 us, 4.9 without).
 template <int EK, int VEC, int ACT>
 __device__ __noinline__ void finish_far_slice(const GnCluster& a)
 {

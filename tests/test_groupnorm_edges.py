@@ -162,6 +162,37 @@ def test_sums_up_to_the_range(shape, way):
     cb.check_status()
 
 
+@pytest.mark.gpu
+def test_far_means_captured_and_on_two_streams(way):
+    """Replays on inputs with and without far means, and two calls at once."""
+    N, S, C, G = 4, 200, 96, 8
+    near, g, b, _ = tg._inputs(N, S, C, "f32", seed=41)
+    far = near + 3000.0
+    far[1] = 100.1
+    want = [cb.groupnorm_forward(t, G, g, b, act="silu", stats=True) for t in (near, far)]
+    x = near.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = cb.groupnorm_forward(x, G, g, b, act="silu", stats=True)
+    for k in (1, 0, 1, 1, 0):
+        x.copy_((near, far)[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, want[k]))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for t, s in zip((near, far), streams):
+            with torch.cuda.stream(s):
+                got.append(cb.groupnorm_forward(t, G, g, b, act="silu", stats=True))
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for w, o in zip(want, got) for p, q in zip(w, o))
+    z = far.clone()
+    assert cb.groupnorm_forward(z, G, g, b, act="silu", out=z) is z and torch.equal(z, want[1][0])     # in place
+    cb.check_status()
+
+
 # ------------------------------------------------------------------ which way, and sizes at the ends
 
 def _ways(N, S, C, G, dtype):
